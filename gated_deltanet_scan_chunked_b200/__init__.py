@@ -7,9 +7,11 @@ seeded synthetic workloads; ``build`` compiles the library.
 from .gdn import (GdnError, bwd_workspace_size, conv_workspace_size,  # noqa: F401
                   gdn_check_device_error, gdn_chunk_bwd, gdn_chunk_fwd, gdn_chunk_fwd_conv,
                   gdn_conv_frontend, gdn_decode_conv, gdn_decode_multi, gdn_decode_step,
-                  gdn_gr_read, gdn_gr_write, load, workspace_size)
+                  gdn_glr_bwd, gdn_glr_fwd, gdn_glr_step, gdn_gr_read, gdn_gr_write,
+                  glr_bwd_workspace_size, glr_checkpoint_shape, load, workspace_size)
 
 __all__ = ["gdn_chunk_fwd", "gdn_chunk_bwd", "gdn_decode_step", "gdn_decode_multi",
            "gdn_check_device_error", "gdn_conv_frontend", "gdn_chunk_fwd_conv", "gdn_decode_conv", "gdn_gr_read",
-           "gdn_gr_write", "GdnError", "load",
+           "gdn_gr_write", "gdn_glr_fwd", "gdn_glr_bwd", "gdn_glr_step", "GdnError", "load",
+           "glr_bwd_workspace_size", "glr_checkpoint_shape",
            "workspace_size", "bwd_workspace_size", "conv_workspace_size"]

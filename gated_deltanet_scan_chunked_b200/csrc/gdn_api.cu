@@ -490,6 +490,145 @@ extern "C" gdn_status gdn_gr_write(uint8_t* codes, float* scales, const void* y,
   return launch_gr_write(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
+namespace {
+
+// Checks shared by the gated linear recurrence's entry points.
+gdn_status glr_check(gdn_glr_gate gate, const void* beta, int32_t C, gdn_dtype dt) {
+  if (C < 1) return GDN_ERR_INVALID_ARG;
+  if (gate != GDN_GLR_GATE_NONE && gate != GDN_GLR_GATE_BETA && gate != GDN_GLR_GATE_COMPLEMENT)
+    return GDN_ERR_INVALID_ARG;
+  if (beta != nullptr && gate != GDN_GLR_GATE_BETA) return GDN_ERR_INVALID_ARG;
+  if (dt != GDN_BF16 && dt != GDN_FP32) return GDN_ERR_UNSUPPORTED;
+  if (C > kGlrMaxChannels) return GDN_ERR_UNSUPPORTED;
+  return GDN_OK;
+}
+
+gdn_status glr_check_packed(const int32_t* cu_seqlens, int32_t n_seq, int64_t total_T, int32_t C) {
+  if (n_seq < 1 || total_T < 0 || (cu_seqlens == nullptr && n_seq != 1))
+    return GDN_ERR_INVALID_ARG;
+  if (total_T > 0x7fffffffLL) return GDN_ERR_INVALID_ARG;  // cu_seqlens is int32
+  if (cu_seqlens && (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u)) return GDN_ERR_INVALID_ARG;
+  return GDN_OK;
+}
+
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+
+// Every pointer 16-byte aligned; no output on an input or on another output.
+bool spans_ok(const Span* in, int n_in, const Span* out, int n_out) {
+  for (int i = 0; i < n_in; ++i)
+    if (in[i].p && !aligned16(in[i].p)) return false;
+  for (int i = 0; i < n_out; ++i) {
+    if (out[i].p && !aligned16(out[i].p)) return false;
+    for (int j = 0; j < n_in; ++j)
+      if (overlaps(out[i].p, out[i].bytes, in[j].p, in[j].bytes)) return false;
+    for (int j = 0; j < i; ++j)
+      if (overlaps(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return false;
+  }
+  return true;
+}
+
+}  // namespace
+
+extern "C" gdn_status gdn_glr_fwd(const void* x, const void* log_alpha, const void* beta,
+                                  gdn_glr_gate gate, const float* initial_state,
+                                  const int32_t* cu_seqlens, int32_t n_seq, int64_t total_T,
+                                  int32_t C, gdn_dtype in_dtype, void* y, float* final_state,
+                                  float* checkpoints, gdn_stream_t stream) {
+  gdn_status st = glr_check(gate, beta, C, in_dtype);
+  if (st == GDN_OK) st = glr_check_packed(cu_seqlens, n_seq, total_T, C);
+  if (st != GDN_OK) return st;
+  const bool need_beta = gate == GDN_GLR_GATE_BETA;
+  if (total_T > 0 && (!x || !log_alpha || (need_beta && !beta) || !y)) return GDN_ERR_INVALID_ARG;
+  const size_t es = in_dtype == GDN_BF16 ? 2 : 4;
+  const size_t nb = (size_t)total_T * C * es, sb = (size_t)n_seq * C * 4;
+  const size_t cb = (size_t)((total_T + kGlrTile - 1) / kGlrTile) * C * 4;
+  // (an exact in-place state update is allowed: the state is then listed as an output only)
+  const Span in[] = {{x, nb}, {log_alpha, nb}, {beta, nb},
+                     {initial_state == final_state ? nullptr : initial_state, sb}};
+  const Span out[] = {{y, nb}, {final_state, sb}, {checkpoints, cb}};
+  if (!spans_ok(in, 4, out, 3)) return GDN_ERR_INVALID_ARG;
+  GlrArgs a = {};
+  a.x = x; a.log_alpha = log_alpha; a.beta = beta; a.initial_state = initial_state;
+  a.cu_seqlens = cu_seqlens; a.n_seq = n_seq; a.total_T = total_T; a.C = C; a.dtype = in_dtype;
+  a.gate = gate; a.y = y; a.final_state = final_state; a.checkpoints = checkpoints;
+  a.err = error_word_ptr();
+  if (a.err == nullptr) return GDN_ERR_CUDA;
+  return launch_glr_fwd(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" size_t gdn_glr_bwd_workspace_size(int64_t total_T, int32_t C) {
+  if (total_T < 0 || total_T > 0x7fffffffLL || C < 1 || C > kGlrMaxChannels) return 0;
+  const size_t n = (size_t)((total_T + kGlrTile - 1) / kGlrTile) * C * 4;
+  return (n + 255) & ~(size_t)255;
+}
+
+extern "C" gdn_status gdn_glr_bwd(const void* x, const void* log_alpha, const void* beta,
+                                  gdn_glr_gate gate, const float* initial_state,
+                                  const int32_t* cu_seqlens, int32_t n_seq, int64_t total_T,
+                                  int32_t C, gdn_dtype in_dtype, const void* dy,
+                                  const float* d_final_state, const float* checkpoints, void* dx,
+                                  void* dlog_alpha, void* dbeta, float* d_initial_state,
+                                  void* workspace, size_t workspace_bytes, gdn_stream_t stream) {
+  gdn_status st = glr_check(gate, beta, C, in_dtype);
+  if (st == GDN_OK) st = glr_check_packed(cu_seqlens, n_seq, total_T, C);
+  if (st != GDN_OK) return st;
+  const bool need_beta = gate == GDN_GLR_GATE_BETA;
+  if (dbeta != nullptr && !need_beta) return GDN_ERR_INVALID_ARG;
+  if (total_T > 0 && (!x || !log_alpha || !dy || !dx || !dlog_alpha ||
+                      (need_beta && (!beta || !dbeta))))
+    return GDN_ERR_INVALID_ARG;
+  const size_t es = in_dtype == GDN_BF16 ? 2 : 4;
+  const size_t nb = (size_t)total_T * C * es, sb = (size_t)n_seq * C * 4;
+  const size_t cb = (size_t)((total_T + kGlrTile - 1) / kGlrTile) * C * 4;
+  const bool recompute = checkpoints == nullptr && total_T > 0;
+  if (recompute && (workspace == nullptr || workspace_bytes < cb ||
+                    (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
+    return GDN_ERR_INVALID_ARG;
+  const Span in[] = {{x, nb}, {log_alpha, nb}, {beta, nb}, {initial_state, sb}, {dy, nb},
+                     {d_final_state, sb}, {checkpoints, cb}};
+  const Span out[] = {{dx, nb}, {dlog_alpha, nb}, {dbeta, nb}, {d_initial_state, sb},
+                      {recompute ? workspace : nullptr, cb}};
+  if (!spans_ok(in, 7, out, 5)) return GDN_ERR_INVALID_ARG;
+  GlrArgs a = {};
+  a.x = x; a.log_alpha = log_alpha; a.beta = beta; a.initial_state = initial_state;
+  a.cu_seqlens = cu_seqlens; a.n_seq = n_seq; a.total_T = total_T; a.C = C; a.dtype = in_dtype;
+  a.gate = gate;
+  a.err = error_word_ptr();
+  if (a.err == nullptr) return GDN_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  a.checkpoints = const_cast<float*>(checkpoints);
+  if (recompute) {
+    a.checkpoints = static_cast<float*>(workspace);
+    st = launch_glr_fwd(a, s);
+    if (st != GDN_OK) return st;
+  }
+  a.dy = dy; a.d_final_state = d_final_state; a.dx = dx; a.dlog_alpha = dlog_alpha;
+  a.dbeta = dbeta; a.d_initial_state = d_initial_state;
+  return launch_glr_bwd(a, s);
+}
+
+extern "C" gdn_status gdn_glr_step(const void* x, const void* log_alpha, const void* beta,
+                                   gdn_glr_gate gate, float* state, int32_t N, int32_t C,
+                                   gdn_dtype in_dtype, void* y, gdn_stream_t stream) {
+  gdn_status st = glr_check(gate, beta, C, in_dtype);
+  if (st != GDN_OK) return st;
+  if (N < 0) return GDN_ERR_INVALID_ARG;
+  if (N == 0) return GDN_OK;
+  if (!x || !log_alpha || (gate == GDN_GLR_GATE_BETA && !beta) || !state || !y)
+    return GDN_ERR_INVALID_ARG;
+  const size_t n = (size_t)N * C, nb = n * (in_dtype == GDN_BF16 ? 2 : 4);
+  const Span in[] = {{x, nb}, {log_alpha, nb}, {beta, nb}};
+  const Span out[] = {{state, n * 4}, {y, nb}};
+  if (!spans_ok(in, 3, out, 2)) return GDN_ERR_INVALID_ARG;
+  GlrArgs a = {};
+  a.x = x; a.log_alpha = log_alpha; a.beta = beta; a.total_T = N; a.C = C; a.dtype = in_dtype;
+  a.gate = gate; a.final_state = state; a.y = y;
+  return launch_glr_step(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
 extern "C" gdn_status gdn_selftest_bounded_wait(int32_t iterations, gdn_stream_t stream) {
   if (iterations < 1) return GDN_ERR_INVALID_ARG;
   int* err = error_word_ptr();

@@ -159,6 +159,38 @@ struct GrWriteArgs {
 
 size_t gr_read_workspace_bytes(int64_t T, int32_t n_r, int32_t d, int32_t rank);
 
+// Gated linear recurrence (gdn_glr.cu): tokens per tile, which is also how far
+// apart the forward's checkpoints lie.
+constexpr int kGlrTile = 64;
+constexpr int kGlrMaxChannels = 65535 * 32;  // groups of 32 channels along the grid
+
+struct GlrArgs {
+  const void* x;               // [total_T, C] input dtype, as are log_alpha, beta, y, dy
+  const void* log_alpha;
+  const void* beta;            // gate BETA only
+  const float* initial_state;  // [n_seq, C] or nullptr (zeros)
+  const int32_t* cu_seqlens;   // nullptr: one sequence
+  int32_t n_seq;
+  int64_t total_T;             // the step: rows
+  int32_t C;
+  gdn_dtype dtype;
+  int32_t gate;                // gdn_glr_gate
+  void* y;                     // nullptr: only checkpoints are written
+  float* final_state;          // [n_seq, C] or nullptr; the step: the state, rewritten
+  float* checkpoints;          // [ceil(total_T / kGlrTile), C]: the state before each tile
+  const void* dy;
+  const float* d_final_state;  // [n_seq, C] or nullptr (zeros)
+  void* dx;
+  void* dlog_alpha;
+  void* dbeta;                 // gate BETA only
+  float* d_initial_state;      // [n_seq, C] or nullptr
+  int* err;
+};
+
+gdn_status launch_glr_fwd(const GlrArgs& a, cudaStream_t stream);
+gdn_status launch_glr_bwd(const GlrArgs& a, cudaStream_t stream);
+gdn_status launch_glr_step(const GlrArgs& a, cudaStream_t stream);
+
 // The library's device error word on the current device (nullptr on failure).
 int* device_error_word();
 

@@ -108,6 +108,21 @@ def load(path: str = LIB_PATH):
     f = lib.gdn_gr_write
     f.restype = ctypes.c_int
     f.argtypes = [_vp] * 4 + [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, _vp]
+    f = lib.gdn_glr_fwd
+    f.restype = ctypes.c_int
+    f.argtypes = [_vp] * 3 + [ctypes.c_int, _vp, _vp, ctypes.c_int32, ctypes.c_int64,
+                              ctypes.c_int32, ctypes.c_int] + [_vp] * 4
+    f = lib.gdn_glr_bwd_workspace_size
+    f.restype = ctypes.c_size_t
+    f.argtypes = [ctypes.c_int64, ctypes.c_int32]
+    f = lib.gdn_glr_bwd
+    f.restype = ctypes.c_int
+    f.argtypes = [_vp] * 3 + [ctypes.c_int, _vp, _vp, ctypes.c_int32, ctypes.c_int64,
+                              ctypes.c_int32, ctypes.c_int] + [_vp] * 8 + [ctypes.c_size_t, _vp]
+    f = lib.gdn_glr_step
+    f.restype = ctypes.c_int
+    f.argtypes = [_vp] * 3 + [ctypes.c_int, _vp, ctypes.c_int32, ctypes.c_int32, ctypes.c_int,
+                              _vp, _vp]
     lib.gdn_selftest_bounded_wait.restype = ctypes.c_int
     lib.gdn_selftest_bounded_wait.argtypes = [ctypes.c_int32, _vp]
     lib.gdn_check_device_error.restype = ctypes.c_int
@@ -564,6 +579,201 @@ def gdn_gr_write(codes, scales, y, s, stream=None):
     if st != GDN_OK:
         raise GdnError(st, "gdn_gr_write")
     return codes, scales
+
+
+# --- gated linear recurrence, beam search -------------------------------------
+
+GLR_TILE = 64  # tokens between two checkpoints
+_GATE_NONE, _GATE_BETA, _GATE_COMPLEMENT = 0, 1, 2
+
+
+class _on:
+    """The device of a call's tensors made current, and the stream that it runs
+    on: the given one, or that device's current one."""
+
+    def __init__(self, dev, stream):
+        self._back = None
+        now = torch.cuda.current_device()
+        if dev.index != now:
+            self._back = now
+            torch.cuda.set_device(dev)
+        self.given = stream
+        if stream is None:
+            self.handle = torch.cuda.current_stream(dev).cuda_stream
+        else:
+            self.handle = stream.cuda_stream
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        if self._back is not None:
+            torch.cuda.set_device(self._back)
+
+    def keep(self, *tensors):
+        """Memory made here (on torch's current stream) is used on a given
+        stream: it must not go to others before that use is over."""
+        if self.given is not None:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(self.given)
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _need(t: Optional[torch.Tensor], name: str, dtype, shape, dev):
+    """t (if given) is a dense CUDA tensor on dev of that type and shape."""
+    if t is None:
+        return
+    if t.device != dev or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        _check(t, name, dtype, dev)
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+
+
+def _glr_gate(beta):
+    if isinstance(beta, str):
+        if beta != "complement":
+            raise ValueError("beta must be a tensor, None or 'complement'")
+        return _GATE_COMPLEMENT, None
+    return (_GATE_NONE, None) if beta is None else (_GATE_BETA, beta)
+
+
+def _glr_inputs(x, log_alpha, beta):
+    """(device, dtype code, shape, gate code, beta tensor) of a call."""
+    dev = x.device
+    _check(x, "x")
+    dt = _dtype_code(x)
+    if x.dim() != 2:
+        raise ValueError("x must be [tokens, channels], got %s" % (tuple(x.shape),))
+    gate, beta = _glr_gate(beta)
+    _need(log_alpha, "log_alpha", x.dtype, x.shape, dev)
+    _need(beta, "beta", x.dtype, x.shape, dev)
+    return dev, dt, x.shape, gate, beta
+
+
+def _glr_sequences(cu_seqlens, dev):
+    if cu_seqlens is None:
+        return 1
+    _check(cu_seqlens, "cu_seqlens", torch.int32, dev)
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+        raise ValueError("cu_seqlens must be [n_seq + 1]")
+    return cu_seqlens.shape[0] - 1
+
+
+def glr_checkpoint_shape(total_T: int, C: int):
+    """Shape of the recurrence's checkpoints: [ceil(total_T / 64), C]."""
+    return ((total_T + GLR_TILE - 1) // GLR_TILE, C)
+
+
+def gdn_glr_fwd(x, log_alpha, beta=None, initial_state=None, cu_seqlens=None, y=None,
+                final_state=None, output_final_state=True, checkpoints=None, stream=None):
+    """Gated linear recurrence h_t = a_t h_{t-1} + b_t x_t per channel, a =
+    exp(log_alpha), over packed sequences: returns (y, final_state,
+    checkpoints).
+
+    x, log_alpha [T, C] (bf16 or fp32); beta: the input gate b as a tensor [T,
+    C], None (b = 1) or "complement" (b = 1 - a); initial_state [n_seq, C]
+    fp32 or None; cu_seqlens [n_seq + 1] int32 (device) or None.  y /
+    final_state may be passed in (final_state may be initial_state itself).
+    checkpoints: None (not written), True (allocated here) or a tensor of
+    glr_checkpoint_shape(T, C) fp32, for gdn_glr_bwd.
+    """
+    lib = _lib or load()
+    dev, dt, shape, gate, beta = _glr_inputs(x, log_alpha, beta)
+    T, C = shape
+    n_seq = _glr_sequences(cu_seqlens, dev)
+    with _on(dev, stream) as on:
+        _need(initial_state, "initial_state", torch.float32, (n_seq, C), dev)
+        if y is None:
+            y = torch.empty_like(x)
+            on.keep(y)
+        else:
+            _need(y, "y", x.dtype, shape, dev)
+        if final_state is not None:
+            _need(final_state, "final_state", torch.float32, (n_seq, C), dev)
+        elif output_final_state:
+            final_state = torch.empty((n_seq, C), dtype=torch.float32, device=dev)
+            on.keep(final_state)
+        if checkpoints is True:
+            checkpoints = torch.empty(glr_checkpoint_shape(T, C), dtype=torch.float32, device=dev)
+            on.keep(checkpoints)
+        else:
+            _need(checkpoints, "checkpoints", torch.float32, glr_checkpoint_shape(T, C), dev)
+        st = lib.gdn_glr_fwd(_addr(x), _addr(log_alpha), _addr(beta), gate, _addr(initial_state),
+                             _addr(cu_seqlens), n_seq, T, C, dt, _addr(y), _addr(final_state),
+                             _addr(checkpoints), on.handle)
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_glr_fwd")
+    return y, final_state, checkpoints
+
+
+def glr_bwd_workspace_size(total_T: int, C: int) -> int:
+    """Bytes of workspace gdn_glr_bwd needs when it is given no checkpoints."""
+    return int(load().gdn_glr_bwd_workspace_size(total_T, C))
+
+
+def gdn_glr_bwd(x, log_alpha, dy, beta=None, initial_state=None, d_final_state=None,
+                cu_seqlens=None, checkpoints=None, want_d_initial_state=True, workspace=None,
+                stream=None) -> dict:
+    """Gradients of a gdn_glr_fwd call with the same inputs: dx, dlog_alpha
+    (and dbeta for a tensor beta) [T, C] in x's dtype, d_initial_state [n_seq,
+    C] fp32 when asked for.  dy [T, C]; d_final_state [n_seq, C] fp32 or None.
+    ``checkpoints``: what the forward returned for them; without it they are
+    computed again into ``workspace`` (a uint8 CUDA tensor of at least
+    glr_bwd_workspace_size(T, C) bytes, or None: allocated here)."""
+    lib = _lib or load()
+    dev, dt, shape, gate, beta = _glr_inputs(x, log_alpha, beta)
+    T, C = shape
+    n_seq = _glr_sequences(cu_seqlens, dev)
+    _check(dy, "dy")
+    _need(dy, "dy", x.dtype, shape, dev)
+    for name, t in (("initial_state", initial_state), ("d_final_state", d_final_state)):
+        _need(t, name, torch.float32, (n_seq, C), dev)
+    _need(checkpoints, "checkpoints", torch.float32, glr_checkpoint_shape(T, C), dev)
+    _check(workspace, "workspace", torch.uint8, dev)
+    with _on(dev, stream) as on:
+        out = dict(dx=torch.empty_like(x), dlog_alpha=torch.empty_like(x))
+        if gate == _GATE_BETA:
+            out["dbeta"] = torch.empty_like(x)
+        if want_d_initial_state:
+            out["d_initial_state"] = torch.empty((n_seq, C), dtype=torch.float32, device=dev)
+        on.keep(*out.values())
+        if checkpoints is None and workspace is None:
+            workspace = torch.empty(max(int(lib.gdn_glr_bwd_workspace_size(T, C)), 1),
+                                    dtype=torch.uint8, device=dev)
+            on.keep(workspace)
+        st = lib.gdn_glr_bwd(_addr(x), _addr(log_alpha), _addr(beta), gate, _addr(initial_state),
+                             _addr(cu_seqlens), n_seq, T, C, dt, _addr(dy), _addr(d_final_state),
+                             _addr(checkpoints), _addr(out["dx"]), _addr(out["dlog_alpha"]),
+                             _addr(out.get("dbeta")), _addr(out.get("d_initial_state")),
+                             _addr(workspace), 0 if workspace is None else workspace.numel(),
+                             on.handle)
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_glr_bwd")
+    return out
+
+
+def gdn_glr_step(x, log_alpha, state, beta=None, y=None, stream=None) -> torch.Tensor:
+    """One token per sequence of the gated linear recurrence: x, log_alpha [N,
+    C]; beta as for gdn_glr_fwd; ``state`` [N, C] fp32 is updated in place.
+    Returns y [N, C]."""
+    lib = _lib or load()
+    dev, dt, shape, gate, beta = _glr_inputs(x, log_alpha, beta)
+    _check(state, "state")
+    _need(state, "state", torch.float32, shape, dev)
+    with _on(dev, stream) as on:
+        if y is None:
+            y = torch.empty_like(x)
+            on.keep(y)
+        else:
+            _need(y, "y", x.dtype, shape, dev)
+        st = lib.gdn_glr_step(_addr(x), _addr(log_alpha), _addr(beta), gate, _addr(state),
+                              shape[0], shape[1], dt, _addr(y), on.handle)
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_glr_step")
+    return y
 
 
 def gdn_check_device_error(stream=None) -> int:

@@ -466,6 +466,99 @@ gdn_status gdn_chunk_bwd(
     gdn_stream_t stream);
 
 /*
+ * Gated linear recurrence (GLR): the delta rule's elementwise sibling, with a
+ * state of one value per channel instead of a matrix per head,
+ *
+ *     h_t = a_t h_{t-1} + b_t x_t,   a_t = exp(log_alpha_t),   y_t = h_t
+ *
+ * per channel of C, over the same packed batches (cu_seqlens).  The pages
+ * have no counterpart; the gates follow the delta rule's (decay as
+ * log_alpha, write gate beta), but are held per channel and so in in_dtype,
+ * like an activation.  The state is fp32 throughout and is rounded to
+ * in_dtype once, in y.
+ *
+ * The input gate b: */
+typedef enum {
+  GDN_GLR_GATE_NONE = 0,       /* b = 1                                  */
+  GDN_GLR_GATE_BETA = 1,       /* b = beta [total_T, C]                  */
+  GDN_GLR_GATE_COMPLEMENT = 2  /* b = 1 - a (a moving average of x)      */
+} gdn_glr_gate;
+
+/*
+ * gdn_glr_fwd -- the recurrence over a packed batch (prefill).
+ *
+ *   x, log_alpha   [total_T, C] in_dtype; log_alpha <= 0 (-inf: a = 0, the
+ *                  state before that token, if finite, is forgotten)
+ *   beta           [total_T, C] in_dtype with GDN_GLR_GATE_BETA, else NULL
+ *   gate           the input gate (gdn_glr_gate)
+ *   initial_state  [n_seq, C] fp32 or NULL (zeros)
+ *   cu_seqlens, n_seq, total_T   as for gdn_chunk_fwd.  A malformed
+ *                  cu_seqlens is reported by gdn_check_device_error; nothing
+ *                  outside the outputs is written, but their contents are
+ *                  not meaningful then.
+ *   C              channels (>= 1, any; at most 2,097,120)
+ *   y              [total_T, C] in_dtype, written
+ *   final_state    [n_seq, C] fp32 or NULL; may be initial_state exactly
+ *   checkpoints    [ceil(total_T / 64), C] fp32 or NULL: the state before
+ *                  every 64th packed token, which gdn_glr_bwd takes (their
+ *                  contents are otherwise unspecified)
+ * Apart from final_state = initial_state, outputs must not overlap inputs or
+ * each other.  One kernel; every element is read once and written once.
+ * The result does not depend on timing, and not on the packing beyond
+ * rounding.
+ */
+gdn_status gdn_glr_fwd(const void* x, const void* log_alpha, const void* beta,
+                       gdn_glr_gate gate, const float* initial_state,
+                       const int32_t* cu_seqlens, int32_t n_seq, int64_t total_T, int32_t C,
+                       gdn_dtype in_dtype, void* y, float* final_state, float* checkpoints,
+                       gdn_stream_t stream);
+
+/* Workspace bytes of a gdn_glr_bwd call without checkpoints (0 for arguments
+ * it never accepts): room for them. */
+size_t gdn_glr_bwd_workspace_size(int64_t total_T, int32_t C);
+
+/*
+ * gdn_glr_bwd -- gradients of a gdn_glr_fwd call, for training.
+ *
+ *   the forward's inputs, and
+ *   dy              [total_T, C] in_dtype: dLoss/dy
+ *   d_final_state   [n_seq, C] fp32 or NULL (zeros)
+ *   checkpoints     what gdn_glr_fwd wrote for the same inputs, or NULL: they
+ *                   are computed first (a second kernel, which reads x,
+ *                   log_alpha and beta once more) into the workspace
+ * Outputs, fully overwritten:
+ *   dx, dlog_alpha  [total_T, C] in_dtype, and
+ *   dbeta           the same with GDN_GLR_GATE_BETA, else NULL.  Summed in
+ *                   fp32 and rounded to in_dtype once: each is as large as
+ *                   an activation, and fp32 copies would double the writes.
+ *                   dlog_alpha includes the input gate's part with
+ *                   GDN_GLR_GATE_COMPLEMENT, and is 0 where a = 0.
+ *   d_initial_state [n_seq, C] fp32 or NULL (not written)
+ *   workspace       needed without checkpoints only: 256-byte aligned,
+ *                   gdn_glr_bwd_workspace_size bytes; calls that may overlap
+ *                   must not share one
+ * Outputs must not overlap inputs or each other.
+ */
+gdn_status gdn_glr_bwd(const void* x, const void* log_alpha, const void* beta,
+                       gdn_glr_gate gate, const float* initial_state,
+                       const int32_t* cu_seqlens, int32_t n_seq, int64_t total_T, int32_t C,
+                       gdn_dtype in_dtype, const void* dy, const float* d_final_state,
+                       const float* checkpoints, void* dx, void* dlog_alpha, void* dbeta,
+                       float* d_initial_state, void* workspace, size_t workspace_bytes,
+                       gdn_stream_t stream);
+
+/*
+ * gdn_glr_step -- one token for each of N sequences (decode).
+ *   x, log_alpha, beta   [N, C] in_dtype (beta as for gdn_glr_fwd)
+ *   state                [N, C] fp32, read and overwritten
+ *   y                    [N, C] in_dtype, written
+ * Continues a gdn_glr_fwd from its final_state.  N = 0 is a no-op.
+ */
+gdn_status gdn_glr_step(const void* x, const void* log_alpha, const void* beta,
+                        gdn_glr_gate gate, float* state, int32_t N, int32_t C,
+                        gdn_dtype in_dtype, void* y, gdn_stream_t stream);
+
+/*
  * gdn_check_device_error -- synchronise `stream`, then read and clear the
  * library's device-side error word on the current device.  Returns GDN_OK,
  * GDN_ERR_TIMEOUT (a kernel's bounded wait ran out and the kernel returned
