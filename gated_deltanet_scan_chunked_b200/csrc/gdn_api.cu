@@ -516,18 +516,24 @@ struct Span {
   size_t bytes;
 };
 
-// Every pointer 16-byte aligned; no output on an input or on another output.
-bool spans_ok(const Span* in, int n_in, const Span* out, int n_out) {
-  for (int i = 0; i < n_in; ++i)
-    if (in[i].p && !aligned16(in[i].p)) return false;
+// No output on an input or on another output.
+bool disjoint(const Span* in, int n_in, const Span* out, int n_out) {
   for (int i = 0; i < n_out; ++i) {
-    if (out[i].p && !aligned16(out[i].p)) return false;
     for (int j = 0; j < n_in; ++j)
       if (overlaps(out[i].p, out[i].bytes, in[j].p, in[j].bytes)) return false;
     for (int j = 0; j < i; ++j)
       if (overlaps(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return false;
   }
   return true;
+}
+
+// The same, and every pointer 16-byte aligned.
+bool spans_ok(const Span* in, int n_in, const Span* out, int n_out) {
+  for (int i = 0; i < n_in; ++i)
+    if (in[i].p && !aligned16(in[i].p)) return false;
+  for (int i = 0; i < n_out; ++i)
+    if (out[i].p && !aligned16(out[i].p)) return false;
+  return disjoint(in, n_in, out, n_out);
 }
 
 }  // namespace
@@ -629,6 +635,96 @@ extern "C" gdn_status gdn_glr_step(const void* x, const void* log_alpha, const v
   return launch_glr_step(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
+namespace {
+
+gdn_status beam_check(int32_t n_groups, int32_t K, int32_t V, int32_t M, gdn_dtype dt) {
+  if (n_groups < 0 || K < 1 || V < 1 || M < 1) return GDN_ERR_INVALID_ARG;
+  if ((int64_t)K * V < M) return GDN_ERR_INVALID_ARG;
+  if (dt != GDN_BF16 && dt != GDN_FP32) return GDN_ERR_UNSUPPORTED;
+  if (K > kMaxBeams || M > kMaxBeamCandidates || (int64_t)K * V > 0x7fffffffLL)
+    return GDN_ERR_UNSUPPORTED;
+  if ((int64_t)n_groups * K > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
+  return GDN_OK;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+}  // namespace
+
+extern "C" size_t gdn_beam_select_workspace_size(int32_t n_groups, int32_t K, int32_t V,
+                                                 int32_t M, gdn_dtype in_dtype) {
+  if (beam_check(n_groups, K, V, M, in_dtype) != GDN_OK || n_groups == 0) return 0;
+  return beam_plan((int64_t)n_groups * K, K, V, M, in_dtype).bytes;
+}
+
+extern "C" gdn_status gdn_beam_select(const void* logits, int64_t ld, const float* scores,
+                                      const uint8_t* finished, int32_t end_token,
+                                      int32_t n_groups, int32_t K, int32_t V, int32_t M,
+                                      gdn_dtype in_dtype, float* out_scores,
+                                      int32_t* out_parents, int32_t* out_tokens,
+                                      uint8_t* out_finished, void* workspace,
+                                      size_t workspace_bytes, gdn_stream_t stream) {
+  gdn_status st = beam_check(n_groups, K, V, M, in_dtype);
+  if (st != GDN_OK) return st;
+  if (ld < V || end_token < -1 || end_token >= V) return GDN_ERR_INVALID_ARG;
+  if (finished != nullptr && end_token < 0) return GDN_ERR_INVALID_ARG;
+  if (n_groups == 0) return GDN_OK;
+  if (!logits || !scores || !out_scores || !out_parents || !out_tokens) return GDN_ERR_INVALID_ARG;
+  const size_t es = in_dtype == GDN_BF16 ? 2 : 4;
+  if ((reinterpret_cast<uintptr_t>(logits) & (es - 1)) != 0 || !aligned4(scores) ||
+      !aligned4(out_scores) || !aligned4(out_parents) || !aligned4(out_tokens))
+    return GDN_ERR_INVALID_ARG;
+  const int64_t rows = (int64_t)n_groups * K;
+  if (ld > 0x7fffffffffffffffLL / 4 / rows) return GDN_ERR_INVALID_ARG;
+  if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+      workspace_bytes < beam_plan(rows, K, V, M, in_dtype).bytes)
+    return GDN_ERR_INVALID_ARG;
+  // In place (exactly, with M = K) is allowed for the scores and the flags:
+  // they are then listed as outputs only.
+  const bool same = M == K;
+  const size_t n = (size_t)n_groups * M;
+  const Span in[] = {{logits, ((size_t)(rows - 1) * ld + V) * es},
+                     {same && scores == out_scores ? nullptr : scores, (size_t)rows * 4},
+                     {same && finished == out_finished ? nullptr : finished, (size_t)rows}};
+  const Span out[] = {{out_scores, n * 4}, {out_parents, n * 4}, {out_tokens, n * 4},
+                      {out_finished, n}, {workspace, workspace_bytes}};
+  if (!disjoint(in, 3, out, 5)) return GDN_ERR_INVALID_ARG;
+  BeamArgs a = {};
+  a.logits = logits; a.ld = ld; a.scores = scores; a.finished = finished;
+  a.end_token = end_token; a.n_groups = n_groups; a.K = K; a.V = V; a.M = M; a.dtype = in_dtype;
+  a.out_scores = out_scores; a.out_parents = out_parents; a.out_tokens = out_tokens;
+  a.out_finished = out_finished;
+  return launch_beam_select(a, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" gdn_status gdn_state_reorder(void* const* states, const size_t* row_bytes,
+                                        int32_t n_states, const int32_t* parents,
+                                        int32_t n_groups, int32_t K, gdn_stream_t stream) {
+  if (n_groups < 0 || K < 1 || n_states < 1 || !states || !row_bytes) return GDN_ERR_INVALID_ARG;
+  if (K > kMaxBeams || n_states > kMaxReorderStates) return GDN_ERR_UNSUPPORTED;
+  if (n_groups == 0) return GDN_OK;
+  if (!parents || !aligned4(parents)) return GDN_ERR_INVALID_ARG;
+  const size_t rows = (size_t)n_groups * K;
+  ReorderArgs a = {};
+  Span out[kMaxReorderStates];
+  int n = 0;
+  for (int t = 0; t < n_states; ++t) {
+    if (row_bytes[t] > 0x7fffffffffffULL / rows) return GDN_ERR_INVALID_ARG;
+    if (row_bytes[t] == 0) continue;
+    if (!states[t]) return GDN_ERR_INVALID_ARG;
+    out[n] = {states[t], row_bytes[t] * rows};
+    a.states[n] = states[t];
+    a.row_bytes[n++] = (int64_t)row_bytes[t];
+  }
+  const Span in[] = {{parents, rows * 4}};
+  if (!disjoint(in, 1, out, n)) return GDN_ERR_INVALID_ARG;
+  if (n == 0) return GDN_OK;
+  a.n_states = n; a.parents = parents; a.n_groups = n_groups; a.K = K;
+  a.err = error_word_ptr();
+  if (a.err == nullptr) return GDN_ERR_CUDA;
+  return launch_state_reorder(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
 extern "C" gdn_status gdn_selftest_bounded_wait(int32_t iterations, gdn_stream_t stream) {
   if (iterations < 1) return GDN_ERR_INVALID_ARG;
   int* err = error_word_ptr();
@@ -652,7 +748,7 @@ extern "C" gdn_status gdn_check_device_error(gdn_stream_t stream) {
       return GDN_ERR_CUDA;
   }
   if (word & kErrTimeout) return GDN_ERR_TIMEOUT;
-  if (word & kErrBadSeqlens) return GDN_ERR_INVALID_ARG;
+  if (word & (kErrBadSeqlens | kErrBadIndex)) return GDN_ERR_INVALID_ARG;
   return GDN_OK;
 }
 

@@ -14,6 +14,7 @@ namespace gdn {
 enum : int {
   kErrTimeout = 1,      // a bounded wait ran out
   kErrBadSeqlens = 2,   // cu_seqlens not monotone / out of range
+  kErrBadIndex = 4,     // a beam's parent outside its group
 };
 
 struct PrefillArgs {
@@ -190,6 +191,53 @@ struct GlrArgs {
 gdn_status launch_glr_fwd(const GlrArgs& a, cudaStream_t stream);
 gdn_status launch_glr_bwd(const GlrArgs& a, cudaStream_t stream);
 gdn_status launch_glr_step(const GlrArgs& a, cudaStream_t stream);
+
+// Beam search (gdn_beam.cu).
+constexpr int kMaxBeams = 32;           // beams of a group
+constexpr int kMaxBeamCandidates = 64;  // candidates chosen per group
+constexpr int kMaxReorderStates = 16;   // state tensors of one reordering
+constexpr int kBeamMergeKeys = 8192;    // candidates that the merge holds in shared memory
+constexpr int kBeamMergeSmem = kBeamMergeKeys * 9;
+
+struct BeamArgs {
+  const void* logits;         // [n_groups * K] rows of V, ld elements apart
+  int64_t ld;
+  const float* scores;        // [n_groups, K]
+  const uint8_t* finished;    // [n_groups, K] or nullptr
+  int32_t end_token;          // -1: none
+  int32_t n_groups, K, V, M;
+  gdn_dtype dtype;
+  float* out_scores;          // [n_groups, M]
+  int32_t* out_parents;
+  int32_t* out_tokens;
+  uint8_t* out_finished;      // or nullptr
+  // set by the launcher: the cut, and the workspace's parts
+  int32_t n_seg;
+  int64_t seg_len;            // elements per segment
+  float2* sums;               // [rows, n_seg]: maximum, sum of exp(x - maximum)
+  unsigned long long* keys;   // [rows, n_seg, M], largest first, 0: none
+};
+
+struct BeamPlan {
+  int32_t n_seg;
+  int64_t seg_len;
+  size_t sum_bytes, bytes;    // of the sums; of the whole workspace
+};
+BeamPlan beam_plan(int64_t rows, int32_t K, int32_t V, int32_t M, gdn_dtype dtype);
+gdn_status launch_beam_select(BeamArgs a, void* ws, cudaStream_t stream);
+
+struct ReorderArgs {
+  void* states[kMaxReorderStates];         // [n_groups * K] rows each
+  int64_t row_bytes[kMaxReorderStates];
+  int32_t n_states;
+  const int32_t* parents;                  // [n_groups, K]
+  int32_t n_groups, K;
+  int* err;
+  // set by the launcher
+  int32_t width[kMaxReorderStates];        // bytes of a thread's column
+  int64_t first_block[kMaxReorderStates], blocks_per_group[kMaxReorderStates];
+};
+gdn_status launch_state_reorder(ReorderArgs a, cudaStream_t stream);
 
 // The library's device error word on the current device (nullptr on failure).
 int* device_error_word();

@@ -123,6 +123,16 @@ def load(path: str = LIB_PATH):
     f.restype = ctypes.c_int
     f.argtypes = [_vp] * 3 + [ctypes.c_int, _vp, ctypes.c_int32, ctypes.c_int32, ctypes.c_int,
                               _vp, _vp]
+    f = lib.gdn_beam_select_workspace_size
+    f.restype = ctypes.c_size_t
+    f.argtypes = [ctypes.c_int32] * 4 + [ctypes.c_int]
+    f = lib.gdn_beam_select
+    f.restype = ctypes.c_int
+    f.argtypes = [_vp, ctypes.c_int64, _vp, _vp] + [ctypes.c_int32] * 5 + [ctypes.c_int] + [
+        _vp] * 5 + [ctypes.c_size_t, _vp]
+    f = lib.gdn_state_reorder
+    f.restype = ctypes.c_int
+    f.argtypes = [_vp, _vp, ctypes.c_int32, _vp, ctypes.c_int32, ctypes.c_int32, _vp]
     lib.gdn_selftest_bounded_wait.restype = ctypes.c_int
     lib.gdn_selftest_bounded_wait.argtypes = [ctypes.c_int32, _vp]
     lib.gdn_check_device_error.restype = ctypes.c_int
@@ -774,6 +784,106 @@ def gdn_glr_step(x, log_alpha, state, beta=None, y=None, stream=None) -> torch.T
     if st != GDN_OK:
         raise GdnError(st, "gdn_glr_step")
     return y
+
+
+def beam_workspace_size(n_groups: int, K: int, V: int, n_candidates: int,
+                        dtype=torch.bfloat16) -> int:
+    """Bytes of workspace gdn_beam_select needs (0: never accepted)."""
+    return int(load().gdn_beam_select_workspace_size(n_groups, K, V, n_candidates,
+                                                     _dtype_code_of(dtype)))
+
+
+def gdn_beam_select(logits, scores, n_candidates, finished=None, end_token=-1, out=None,
+                    workspace=None, stream=None):
+    """Beam search's choice: the ``n_candidates`` (M) best continuations of each
+    group over its K beams and the vocabulary, by scores[g, k] + log softmax of
+    logits[g, k], best first; ties go to the lowest k V + v.
+
+    logits [G, K, V] bf16 or fp32 with a contiguous last dimension and rows at
+    one distance (a slice of a padded vocabulary may be given as it is);
+    scores [G, K] fp32; finished [G, K] uint8 or bool or None: those beams are
+    continued by ``end_token`` alone, at their own score.  Returns (scores,
+    parents, tokens, finished), [G, M] fp32, int32, int32 and uint8, or writes
+    them into ``out``, four such tensors (with M = K, out[0] may be scores and
+    out[3] finished).  ``workspace``: a uint8 CUDA tensor of at least
+    beam_workspace_size(...) bytes, or None (allocated here)."""
+    lib = _lib or load()
+    dev = logits.device
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor (libgdn has no CPU path)")
+    dt = _dtype_code_of(logits.dtype)
+    if logits.dim() != 3:
+        raise ValueError("logits must be [groups, beams, vocabulary], got %s"
+                         % (tuple(logits.shape),))
+    G, K, V = logits.shape
+    M = int(n_candidates)
+    sg, ld, sv = logits.stride()
+    if K == 1:
+        ld = sg
+    if G * K == 1:
+        ld = V
+    if (V > 1 and sv != 1) or (G > 1 and sg != K * ld):
+        raise ValueError("logits must have a contiguous vocabulary and equally spaced rows, got "
+                         "strides %s" % (logits.stride(),))
+    _check(scores, "scores")
+    _need(scores, "scores", torch.float32, (G, K), dev)
+    if finished is not None:
+        if finished.dtype == torch.bool:
+            finished = finished.view(torch.uint8)
+        _need(finished, "finished", torch.uint8, (G, K), dev)
+    _check(workspace, "workspace", torch.uint8, dev)
+    with _on(dev, stream) as on:
+        if out is None:
+            out = (torch.empty((G, M), dtype=torch.float32, device=dev),
+                   torch.empty((G, M), dtype=torch.int32, device=dev),
+                   torch.empty((G, M), dtype=torch.int32, device=dev),
+                   torch.empty((G, M), dtype=torch.uint8, device=dev))
+            on.keep(*out)
+        else:
+            for t, name, dtype in zip(out, ("out scores", "out parents", "out tokens",
+                                            "out finished"),
+                                      (torch.float32, torch.int32, torch.int32, torch.uint8)):
+                _check(t, name)
+                _need(t, name, dtype, (G, M), dev)
+        if workspace is None:
+            n = int(lib.gdn_beam_select_workspace_size(G, K, V, M, dt))
+            workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
+            on.keep(workspace)
+        st = lib.gdn_beam_select(_addr(logits), ld, _addr(scores), _addr(finished),
+                                 int(end_token), G, K, V, M, dt, _addr(out[0]), _addr(out[1]),
+                                 _addr(out[2]), _addr(out[3]), _addr(workspace),
+                                 workspace.numel(), on.handle)
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_beam_select")
+    return tuple(out)
+
+
+def gdn_state_reorder(states, parents, stream=None):
+    """The states of the chosen beams, in place: with parents [G, K] int32, row
+    g K + j of every tensor becomes what row g K + parents[g, j] was.
+    ``states``: a tensor or a list of up to 16, each contiguous with G * K rows
+    (recurrent states, conv states, token histories; any type)."""
+    lib = _lib or load()
+    many = [states] if isinstance(states, torch.Tensor) else list(states)
+    dev = parents.device
+    _check(parents, "parents", torch.int32)
+    if parents.dim() != 2 or not many:
+        raise ValueError("parents must be [groups, beams], and there must be a state")
+    G, K = parents.shape
+    n = len(many)
+    ptrs, sizes = (ctypes.c_void_p * n)(), (ctypes.c_size_t * n)()
+    for i, t in enumerate(many):
+        if t.device != dev or not t.is_contiguous():
+            _check(t, "states[%d]" % i, None, dev)
+        if t.dim() < 1 or t.shape[0] != G * K:
+            raise ValueError("states[%d] must have %d rows, got %s" % (i, G * K, tuple(t.shape)))
+        ptrs[i] = t.data_ptr()
+        sizes[i] = t.nbytes // (G * K) if G * K else 0
+    with _on(dev, stream) as on:
+        st = lib.gdn_state_reorder(ptrs, sizes, n, _addr(parents), G, K, on.handle)
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_state_reorder")
+    return states
 
 
 def gdn_check_device_error(stream=None) -> int:

@@ -559,11 +559,87 @@ gdn_status gdn_glr_step(const void* x, const void* log_alpha, const void* beta,
                         gdn_dtype in_dtype, void* y, gdn_stream_t stream);
 
 /*
+ * Beam search over n_groups independent groups (requests) of K beams, rows
+ * g K + k of every [n_groups * K, ...] tensor.  (The pages have no
+ * counterpart; these calls end a decode step.)  A recurrent model keeps no
+ * cache whose page table could be permuted, so the surviving beams' states
+ * themselves move.
+ */
+
+/* Workspace bytes gdn_beam_select needs (0 for arguments it never accepts). */
+size_t gdn_beam_select_workspace_size(int32_t n_groups, int32_t K, int32_t V, int32_t M,
+                                      gdn_dtype in_dtype);
+
+/*
+ * gdn_beam_select -- the M best continuations of every group.
+ *
+ * The candidates of a group are all (beam k, token v), scored
+ *     c = scores[k] + logits[k][v] - log sum_v' exp(logits[k][v'])
+ * and ordered by c, then by the lowest k V + v (within a beam, by the logit).
+ * A finished beam has one continuation, end_token at c = scores[k]; its other
+ * tokens score -inf.  A beam whose score is not finite scores -inf throughout,
+ * and so does a row of logits that are all -inf; neither these beams' nor
+ * finished beams' logits are read.  If fewer than M candidates are finite, the
+ * rest of the M are candidates of score -inf, the lowest k V + v first.
+ * A NaN logit counts as -inf; +inf logits share their row equally.
+ *
+ *   logits         n_groups * K rows of V logits, in_dtype; row r begins at
+ *                  logits + r ld (elements).  Aligned to its element size
+ *                  only; rows may begin anywhere.
+ *   ld             elements from row to row (>= V)
+ *   scores         [n_groups, K] fp32 cumulative log probabilities
+ *   finished       [n_groups, K] bytes (non-zero: finished) or NULL (none)
+ *   end_token      in [0, V), or -1: no token ends a beam (finished must
+ *                  then be NULL)
+ *   K              beams per group, 1 .. 32
+ *   V              vocabulary; K V < 2^31
+ *   M              candidates chosen per group, 1 .. 64, at most K V
+ *   out_scores     [n_groups, M] fp32, best first
+ *   out_parents    [n_groups, M] int32, k
+ *   out_tokens     [n_groups, M] int32, v
+ *   out_finished   [n_groups, M] bytes or NULL: 1 if the parent was finished
+ *                  or the token is end_token
+ *   workspace      256-byte aligned, gdn_beam_select_workspace_size bytes;
+ *                  calls that may overlap must not share one
+ * With M = K, out_scores may be scores and out_finished may be finished (in
+ * place, for a loop without copies); otherwise outputs must not overlap
+ * inputs or each other.  The logits are read once.  Two kernels.
+ */
+gdn_status gdn_beam_select(const void* logits, int64_t ld, const float* scores,
+                           const uint8_t* finished, int32_t end_token, int32_t n_groups,
+                           int32_t K, int32_t V, int32_t M, gdn_dtype in_dtype,
+                           float* out_scores, int32_t* out_parents, int32_t* out_tokens,
+                           uint8_t* out_finished, void* workspace, size_t workspace_bytes,
+                           gdn_stream_t stream);
+
+/*
+ * gdn_state_reorder -- the states of the chosen beams, in place: row g K + j
+ * of every tensor becomes what row g K + parents[g][j] was.
+ *
+ *   states      HOST array of n_states device pointers, each n_groups * K
+ *               dense rows (recurrent states, conv states, token histories;
+ *               any element type)
+ *   row_bytes   HOST array: bytes of one row of each (>= 0)
+ *   n_states    1 .. 16; the tensors must not overlap
+ *   parents     [n_groups, K] int32, each in [0, K).  Any map is allowed, a
+ *               parent may repeat.  A row whose parent is out of range stays
+ *               as it was, and gdn_check_device_error reports
+ *               GDN_ERR_INVALID_ARG.
+ *   K           1 .. 32
+ * No second copy of the state and no workspace: rows that keep their place
+ * are neither read nor written.  The states need only their element's
+ * alignment; 16-byte aligned rows move fastest.  One kernel.
+ */
+gdn_status gdn_state_reorder(void* const* states, const size_t* row_bytes, int32_t n_states,
+                             const int32_t* parents, int32_t n_groups, int32_t K,
+                             gdn_stream_t stream);
+
+/*
  * gdn_check_device_error -- synchronise `stream`, then read and clear the
  * library's device-side error word on the current device.  Returns GDN_OK,
  * GDN_ERR_TIMEOUT (a kernel's bounded wait ran out and the kernel returned
  * early; its outputs are incomplete), GDN_ERR_INVALID_ARG (a kernel found a
- * malformed cu_seqlens) or GDN_ERR_CUDA (the synchronisation itself failed).
+ * malformed cu_seqlens or a parent out of range) or GDN_ERR_CUDA (the synchronisation itself failed).
  * This call blocks the host; the compute entry points never do.
  */
 gdn_status gdn_check_device_error(gdn_stream_t stream);
