@@ -8,17 +8,22 @@
 // (A1 A2, A2 h1 + h2).  A sequence's first token takes a = 0 and adds
 // a_t h_0 to its input, so packed sequences need no other care.
 //
-// Layout.  A CTA of 8 warps owns a tile of 64 tokens x 32 VEC channels: warp
-// w has tokens 8 w .. 8 w + 7, a lane VEC neighbouring channels.  The carry
-// along the tokens passes three levels, each in a fixed order (results do not
-// depend on timing): 8 tokens in a thread's registers, 8 warps through
-// shared memory, and the CTAs of a cluster, which hold consecutive tiles of
-// the same channels, through distributed shared memory.  The cluster walks
-// the packed tokens in steps of (cluster size) tiles, the carry kept in
-// registers; nothing is exchanged through global memory, so there is no
-// workspace and no flag to wait on.  Every input is read once and every
-// output written once; the next tile's inputs are loaded into registers
-// while this one is folded.
+// Layout.  A CTA of 8 warps owns a tile of 8 kRun tokens x 64 channels: warp w
+// has the run of kRun tokens from w kRun on, a lane two channels (which the
+// packed fp32 instructions take together).  The carry along the tokens passes
+// three levels, each in a fixed order (results do not depend on timing): a
+// thread's run in registers, the 8 runs of a tile by one warp through shared
+// memory, and the CTAs of a cluster, which hold consecutive tiles of the same
+// channels, through distributed shared memory.  The cluster walks the packed
+// tokens in steps of (cluster size) tiles, the carry kept in registers;
+// nothing is exchanged through global memory, so there is no workspace and no
+// flag to wait on.  Every input is read once and every output written once.
+// Inputs come by 16-byte asynchronous copies into two shared-memory stages,
+// so that the next steps' loads are in flight while this one is folded.
+//
+// Rows of C elements that are not a multiple of 16 bytes begin anywhere: then
+// a row's piece is copied from the 16-byte boundary below it, one copy more,
+// and read from its remainder on (kAl = false).
 #include <atomic>
 
 #include "gdn_common.cuh"
@@ -29,65 +34,14 @@ namespace gdn {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kTok = kGlrTile / kWarps;  // tokens per thread and tile
 constexpr int kThreads = 32 * kWarps;
+constexpr int kChan = 64;  // channels of a CTA
 constexpr int kMaxCluster = 8;
-static_assert(kTok == 8 && kGlrTile == 64, "one lane per token of a warp's run");
 
 enum : int { kGateNone = GDN_GLR_GATE_NONE, kGateBeta = GDN_GLR_GATE_BETA,
              kGateComp = GDN_GLR_GATE_COMPLEMENT };
 
-// VEC neighbouring channels of one token as they lie in memory.
-template <typename T, int VEC>
-struct Raw;
-template <>
-struct Raw<float, 1> {
-  float r;
-  __device__ __forceinline__ void load(const float* p) { r = __ldg(p); }
-  __device__ __forceinline__ void zero() { r = 0.f; }
-  __device__ __forceinline__ void get(float* f) const { f[0] = r; }
-  static __device__ __forceinline__ void store(float* p, const float* f) { *p = f[0]; }
-};
-template <>
-struct Raw<float, 2> {
-  float2 r;
-  __device__ __forceinline__ void load(const float* p) {
-    r = __ldg(reinterpret_cast<const float2*>(p));
-  }
-  __device__ __forceinline__ void zero() { r = make_float2(0.f, 0.f); }
-  __device__ __forceinline__ void get(float* f) const { f[0] = r.x; f[1] = r.y; }
-  static __device__ __forceinline__ void store(float* p, const float* f) {
-    *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
-  }
-};
-template <>
-struct Raw<__nv_bfloat16, 1> {
-  unsigned short r;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    r = __ldg(reinterpret_cast<const unsigned short*>(p));
-  }
-  __device__ __forceinline__ void zero() { r = 0; }
-  __device__ __forceinline__ void get(float* f) const { f[0] = __uint_as_float((uint32_t)r << 16); }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* f) {
-    *p = __float2bfloat16_rn(f[0]);
-  }
-};
-template <>
-struct Raw<__nv_bfloat16, 2> {
-  uint32_t r;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    r = __ldg(reinterpret_cast<const uint32_t*>(p));
-  }
-  __device__ __forceinline__ void zero() { r = 0; }
-  // (a bf16 is the high half of its fp32 value)
-  __device__ __forceinline__ void get(float* f) const {
-    f[0] = __uint_as_float(r << 16);
-    f[1] = __uint_as_float(r & 0xffff0000u);
-  }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* f) {
-    *reinterpret_cast<uint32_t*>(p) = sm100::pack_bf16(f[0], f[1]);
-  }
-};
+using f2 = uint64_t;  // two channels of a lane, fp32
 
 // a = exp(l) and 1 - a.  Channels that remember a thousand tokens have a
 // within 1e-3 of 1, where an error of exp in one direction adds up over all of
@@ -95,23 +49,33 @@ struct Raw<__nv_bfloat16, 2> {
 // term left out, l^7/5040, is below 2^-24 of the sum for |l| < 1/4) and a is
 // 1 + that, rounded once; further out the hardware 2^x, good to 2^-22,
 // serves, since such a channel forgets within a few tokens.
-__device__ __forceinline__ void decay(float l, float& a, float& one_minus_a) {
-  float p = __fmaf_rn(l, 1.f / 720.f, 1.f / 120.f);
-  p = __fmaf_rn(l, p, 1.f / 24.f);
-  p = __fmaf_rn(l, p, 1.f / 6.f);
-  p = __fmaf_rn(l, p, 0.5f);
-  p = __fmaf_rn(l, p, 1.f);
-  p = __fmul_rn(l, p);
-  const float e = sm100::ex2_approx(__fmul_rn(l, 1.4426950408889634f));
-  const bool near = fabsf(l) < 0.25f;
-  a = near ? __fadd_rn(1.f, p) : e;
-  one_minus_a = near ? -p : __fadd_rn(1.f, -e);
+__device__ __forceinline__ f2 both(float v) { return f2_pack(v, v); }
+template <int GATE>
+__device__ __forceinline__ void decay2(f2 l, f2& a, f2& one_minus_a) {
+  f2 p = f2_fma(l, both(1.f / 720.f), both(1.f / 120.f));
+  p = f2_fma(l, p, both(1.f / 24.f));
+  p = f2_fma(l, p, both(1.f / 6.f));
+  p = f2_fma(l, p, both(0.5f));
+  p = f2_fma(l, p, both(1.f));
+  p = f2_mul(l, p);
+  float l0, l1, z0, z1, n0, n1;
+  f2_unpack(l, l0, l1);
+  f2_unpack(f2_mul(l, both(1.4426950408889634f)), z0, z1);
+  f2_unpack(f2_add(p, both(1.f)), n0, n1);
+  const float e0 = sm100::ex2_approx(z0), e1 = sm100::ex2_approx(z1);
+  const bool s0 = fabsf(l0) < 0.25f, s1 = fabsf(l1) < 0.25f;
+  a = f2_pack(s0 ? n0 : e0, s1 ? n1 : e1);
+  if (GATE == kGateComp) {
+    float p0, p1;
+    f2_unpack(p, p0, p1);
+    one_minus_a = f2_pack(s0 ? -p0 : __fadd_rn(1.f, -e0), s1 ? -p1 : __fadd_rn(1.f, -e1));
+  }
 }
 
-// Input gate b of one channel: its factor of x.
+// The input b x of two channels.
 template <int GATE>
-__device__ __forceinline__ float gate_of(float beta, float one_minus_a) {
-  return GATE == kGateNone ? 1.f : GATE == kGateBeta ? beta : one_minus_a;
+__device__ __forceinline__ f2 gated(f2 x, f2 beta, f2 one_minus_a) {
+  return GATE == kGateNone ? x : f2_mul(GATE == kGateBeta ? beta : one_minus_a, x);
 }
 
 // Last sequence s with cu[s] <= t (so that empty sequences are passed over).
@@ -125,246 +89,334 @@ __device__ __forceinline__ int seq_at(const int32_t* cu, int n_seq, int64_t t) {
   return lo;
 }
 
-// Which of a warp's kTok tokens from t0 on begin or end a sequence (bit i:
-// token t0 + i); lane i (< kTok) also gets token i's sequence.
+// Which of a run's tokens from t0 on begin or end a sequence (bit i: token
+// t0 + i; tokens outside [0, total_T) neither).
 struct Marks {
   uint32_t first, last;
-  int seq;
 };
+template <int RUN>
 __device__ __forceinline__ Marks marks_of(const int32_t* cu, int n_seq, int64_t total_T,
                                           int64_t t0, int lane) {
   Marks m;
-  m.seq = 0;
   if (cu == nullptr) {
     m.first = t0 == 0 ? 1u : 0u;
     const int64_t d = total_T - 1 - t0;
-    m.last = d >= 0 && d < kTok ? 1u << (int)d : 0u;
+    m.last = d >= 0 && d < RUN ? 1u << (int)d : 0u;
     return m;
   }
   bool f = false, l = false;
   const int64_t t = t0 + lane;
-  if (lane < kTok && t < total_T) {
-    m.seq = seq_at(cu, n_seq, t);
-    f = __ldg(cu + m.seq) == t;
-    l = __ldg(cu + m.seq + 1) == t + 1;
+  if (lane < RUN && t >= 0 && t < total_T) {
+    const int s = seq_at(cu, n_seq, t);
+    f = __ldg(cu + s) == t;
+    l = __ldg(cu + s + 1) == t + 1;
   }
   m.first = __ballot_sync(0xffffffffu, f);
   m.last = __ballot_sync(0xffffffffu, l);
   return m;
 }
+__device__ __forceinline__ int64_t seq_of(const GlrArgs& p, int64_t t) {
+  return p.cu_seqlens == nullptr ? 0 : seq_at(p.cu_seqlens, p.n_seq, t);
+}
 
-// One composed run of tokens per channel.
-template <int VEC>
-struct __align__(8 * VEC) Run {
-  float A[VEC], h[VEC];
+// A composed run, two channels.
+struct __align__(16) Run {
+  f2 A, h;
 };
 
 // h behind a run that is entered with h.  A run whose A is 0 forgets what was
 // before it, even an infinity or NaN: those belong to another sequence.
-__device__ __forceinline__ float through(float A, float run_h, float h) {
-  return A == 0.f ? run_h : __fmaf_rn(A, h, run_h);
+__device__ __forceinline__ f2 through(const Run& r, f2 h) {
+  float a0, a1, r0, r1, n0, n1;
+  f2_unpack(r.A, a0, a1);
+  f2_unpack(r.h, r0, r1);
+  f2_unpack(f2_fma(r.A, h, r.h), n0, n1);
+  return f2_pack(a0 == 0.f ? r0 : n0, a1 == 0.f ? r1 : n1);
 }
 
-// Rows of a [n_seq, C] state: load / store VEC channels of sequence s.
-template <int VEC>
-__device__ __forceinline__ void state_get(const float* p, int64_t s, int C, int c, float* f) {
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) f[j] = p == nullptr ? 0.f : p[s * C + c + j];
+// A lane's two channels: neighbours where rows are aligned, else 32 apart.
+template <bool AL>
+struct Chan {
+  int c0, c1;
+  bool ok0, ok1;
+  __device__ __forceinline__ Chan(int cb, int lane, int C) {
+    c0 = cb + (AL ? 2 * lane : lane);
+    c1 = AL ? c0 + 1 : c0 + 32;
+    ok0 = c0 < C;
+    ok1 = c1 < C;
+  }
+  // rows of a [.., C] fp32 array (nullptr: zeros)
+  __device__ __forceinline__ f2 get(const float* p, int64_t row, int C) const {
+    return f2_pack(p != nullptr && ok0 ? p[row * C + c0] : 0.f,
+                   p != nullptr && ok1 ? p[row * C + c1] : 0.f);
+  }
+  __device__ __forceinline__ void put(float* p, int64_t row, int C, f2 v) const {
+    float v0, v1;
+    f2_unpack(v, v0, v1);
+    if (ok0) p[row * C + c0] = v0;
+    if (ok1) p[row * C + c1] = v1;
+  }
+};
+
+// Shared-memory image of one input tensor's piece of a tile.
+template <typename T, bool AL>
+struct Piece {
+  static constexpr int kCopies = kChan * (int)sizeof(T) / 16 + (AL ? 0 : 1);  // 16 bytes each
+  static constexpr int kPitch = 16 * kCopies;                                 // bytes of a row
+  static constexpr int bytes(int rows) { return rows * kPitch; }
+  // A lane's two channels of one row; rem: where the row's piece begins.
+  static __device__ __forceinline__ f2 get(const char* row, int rem, int lane) {
+    if (sizeof(T) == 2) {
+      uint32_t lo, hi;
+      if (AL) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(row + 4 * lane);
+        lo = w << 16;
+        hi = w & 0xffff0000u;
+      } else {
+        lo = (uint32_t) * reinterpret_cast<const unsigned short*>(row + rem + 2 * lane) << 16;
+        hi = (uint32_t) * reinterpret_cast<const unsigned short*>(row + rem + 2 * lane + 64) << 16;
+      }
+      return f2_pack(__uint_as_float(lo), __uint_as_float(hi));
+    }
+    if (AL) return *reinterpret_cast<const f2*>(row + 8 * lane);
+    return f2_pack(*reinterpret_cast<const float*>(row + rem + 4 * lane),
+                   *reinterpret_cast<const float*>(row + rem + 4 * lane + 128));
+  }
+};
+
+template <typename T, bool AL>
+__device__ __forceinline__ void put_out(T* row, const Chan<AL>& ch, f2 v) {
+  float v0, v1;
+  f2_unpack(v, v0, v1);
+  if (AL) {
+    if (ch.ok0) {
+      if (sizeof(T) == 2)
+        *reinterpret_cast<uint32_t*>(row + ch.c0) = sm100::pack_bf16(v0, v1);
+      else
+        *reinterpret_cast<f2*>(row + ch.c0) = v;
+    }
+  } else {
+    if (ch.ok0) Elem<T>::store(row + ch.c0, v0);
+    if (ch.ok1) Elem<T>::store(row + ch.c1, v1);
+  }
 }
-template <int VEC>
-__device__ __forceinline__ void state_put(float* p, int64_t s, int C, int c, const float* f) {
+
+// 16 bytes of which the first n (0 .. 16) are read, the rest zero filled.
+__device__ __forceinline__ void copy16(uint32_t dst, const char* src, int n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+
+// Copies the tile's rows [t0, t0 + ROWS) of N tensors into a stage.  Tokens
+// outside [0, T) become zeros: a = exp(0) = 1 and x = 0 leave a state as it is.
+template <typename T, bool AL, int ROWS, int N>
+__device__ __forceinline__ void load_stage(uint32_t stage, const char* const (&src)[N], int64_t t0,
+                                           int64_t total_T, int C, int cb) {
+  using P = Piece<T, AL>;
+  const int64_t row_bytes = (int64_t)C * (int)sizeof(T);
+  const int64_t all = total_T * row_bytes;
+  for (int i = threadIdx.x; i < ROWS * P::kCopies; i += kThreads) {
+    const int r = i / P::kCopies, q = i % P::kCopies;
+    const int64_t t = t0 + r;
+    int64_t off = t * row_bytes + (int64_t)cb * (int)sizeof(T);
+    if (!AL) off &= ~(int64_t)15;
+    off += 16 * q;
+    int n = 0;
+    if (t >= 0 && t < total_T) {
+      if (AL)
+        n = cb * (int)sizeof(T) + 16 * q < row_bytes ? 16 : 0;
+      else
+        n = all - off >= 16 ? 16 : all - off > 0 ? (int)(all - off) : 0;
+    }
+    if (n == 0) off = 0;
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) p[s * C + c + j] = f[j];
+    for (int k = 0; k < N; ++k)
+      copy16(stage + k * P::bytes(ROWS) + r * P::kPitch + 16 * q, src[k] + off, n);
+  }
+}
+
+__device__ __forceinline__ void st_cluster_run(uint32_t addr, const Run& r) {
+  asm volatile("st.shared::cluster.v2.b64 [%0], {%1, %2};" ::"r"(addr), "l"(r.A), "l"(r.h)
+               : "memory");
+}
+
+// One warp: turns the runs of a tile (in[w], in the order `first, first +
+// dir, ...`) into what lies before each (in place), and gives the whole.
+__device__ __forceinline__ Run fold_tile(Run (*runs)[32], int lane, bool backwards) {
+  Run r[kWarps];
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) r[w] = runs[backwards ? kWarps - 1 - w : w][lane];
+  Run all;
+  all.A = both(1.f);
+  all.h = both(0.f);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    runs[backwards ? kWarps - 1 - w : w][lane] = all;
+    all.h = through(r[w], all.h);
+    all.A = f2_mul(all.A, r[w].A);
+  }
+  return all;
 }
 
 // Sequences without tokens carry their state through: out[s] = in[s] (or 0).
 // Also reports a malformed cu_seqlens.  Rows are shared out over the
 // cluster's warps.
-template <int VEC>
-__device__ __forceinline__ void empty_sequences(const int32_t* cu, int n_seq, int64_t total_T,
-                                                const float* in, float* out, int C, int c,
-                                                bool c_ok, int first_row, int stride, int* err) {
-  for (int s = first_row; s < n_seq; s += stride) {
-    int64_t lo = 0, hi = total_T;
-    if (cu != nullptr) {
-      lo = __ldg(cu + s);
-      hi = __ldg(cu + s + 1);
-      const bool ok = lo >= 0 && hi >= lo && hi <= total_T && (s != 0 || lo == 0) &&
-                      (s != n_seq - 1 || hi == total_T);
+template <bool AL>
+__device__ __forceinline__ void empty_sequences(const GlrArgs& p, const float* in, float* out,
+                                                const Chan<AL>& ch, int first_row, int stride,
+                                                bool report) {
+  for (int s = first_row; s < p.n_seq; s += stride) {
+    int64_t lo = 0, hi = p.total_T;
+    if (p.cu_seqlens != nullptr) {
+      lo = __ldg(p.cu_seqlens + s);
+      hi = __ldg(p.cu_seqlens + s + 1);
+      const bool ok = lo >= 0 && hi >= lo && hi <= p.total_T && (s != 0 || lo == 0) &&
+                      (s != p.n_seq - 1 || hi == p.total_T);
       if (!ok) {
-        if (err != nullptr && (threadIdx.x & 31) == 0) atomicOr(err, kErrBadSeqlens);
+        if (report && (threadIdx.x & 31) == 0) atomicOr(p.err, kErrBadSeqlens);
         continue;
       }
     }
-    if (lo == hi && out != nullptr && c_ok) {
-      float f[VEC];
-      state_get<VEC>(in, s, C, c, f);
-      state_put<VEC>(out, s, C, c, f);
-    }
+    if (lo == hi && out != nullptr) ch.put(out, s, p.C, ch.get(in, s, p.C));
   }
 }
 
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+// Shared memory of a CTA: the runs of a tile (RUNS sets), the cluster's tiles
+// (two buffers), two stages of inputs.
+template <typename T, bool AL>
+constexpr int scan_smem(int run, int tensors, int run_sets) {
+  return run_sets * kWarps * 32 * (int)sizeof(Run) + 2 * kMaxCluster * 32 * (int)sizeof(Run) +
+         2 * tensors * Piece<T, AL>::bytes(kWarps * run);
 }
 
-template <typename Tin, int VEC, int GATE>
+// Tokens of a thread's run.
+template <typename T, bool AL>
+constexpr int fwd_run() { return sizeof(T) == 2 && AL ? 16 : 8; }
+constexpr int kBwdRun = 8;
+static_assert(kBwdRun * kWarps == kGlrTile, "the backward starts each tile from a checkpoint");
+
+template <typename T, int GATE, bool AL>
 __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(const GlrArgs p) {
-  __shared__ Run<VEC> warp_run[kWarps][32];
-  __shared__ Run<VEC> tile_run[2][kMaxCluster][32];
-  using R = Raw<Tin, VEC>;
+  constexpr int RUN = fwd_run<T, AL>();
+  constexpr int ROWS = kWarps * RUN;
+  constexpr int N = GATE == kGateBeta ? 3 : 2;
+  using P = Piece<T, AL>;
+  extern __shared__ __align__(128) char smem[];
+  Run(*runs)[32] = reinterpret_cast<Run(*)[32]>(smem);
+  Run(*tiles)[32] = runs + kWarps;  // [2][kMaxCluster]
+  char* stages = reinterpret_cast<char*>(tiles + 2 * kMaxCluster);
+  const uint32_t stages_u = sm100::smem_u32(stages);
+  constexpr int kStage = N * P::bytes(ROWS);
+
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n_cta = (int)gridDim.x, rank = (int)blockIdx.x;  // one cluster along x
-  const int C = p.C;
-  const int c = ((int)blockIdx.y * 32 + lane) * VEC;
-  const bool c_ok = c < C;
-  const int64_t T = p.total_T;
-  const int64_t n_tiles = (T + kGlrTile - 1) / kGlrTile;
+  const int C = p.C, cb = (int)blockIdx.y * kChan;
+  const Chan<AL> ch(cb, lane, C);
+  const int64_t T_ = p.total_T;
+  const int64_t n_tiles = (T_ + ROWS - 1) / ROWS;
   const int64_t n_steps = (n_tiles + n_cta - 1) / n_cta;
-  const Tin* X = static_cast<const Tin*>(p.x) + c;
-  const Tin* L = static_cast<const Tin*>(p.log_alpha) + c;
-  const Tin* B = static_cast<const Tin*>(p.beta) + c;
-  Tin* Y = static_cast<Tin*>(p.y) + c;
-
-  R rx[kTok], rl[kTok], rb[kTok];
+  const char* src[N];
+  src[0] = static_cast<const char*>(p.x);
+  src[1] = static_cast<const char*>(p.log_alpha);
+  if (N == 3) src[N - 1] = static_cast<const char*>(p.beta);
   auto load = [&](int64_t step) {
-    const int64_t t0 = (step * n_cta + rank) * kGlrTile + warp * kTok;
-#pragma unroll
-    for (int i = 0; i < kTok; ++i) {
-      const int64_t t = t0 + i;
-      if (c_ok && t < T) {
-        rx[i].load(X + t * C);
-        rl[i].load(L + t * C);
-        if (GATE == kGateBeta) rb[i].load(B + t * C);
-      } else {  // a = exp(0) = 1, x = 0: leaves a state as it is
-        rx[i].zero();
-        rl[i].zero();
-        if (GATE == kGateBeta) rb[i].zero();
-      }
-    }
+    if (step < n_steps)
+      load_stage<T, AL, ROWS, N>(stages_u + (int)(step & 1) * kStage, src,
+                                 (step * n_cta + rank) * ROWS, T_, C, cb);
+    sm100::cp_async_commit();
   };
 
-  float carry[VEC];  // state before this step's first tile
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) carry[j] = 0.f;
+  f2 carry = both(0.f);  // state before this step's first tile
   if (n_steps > 0) {
     load(0);
+    load(1);
     sm100::cluster_sync();  // every CTA runs before any writes into another's shared memory
   }
-
   for (int64_t step = 0; step < n_steps; ++step) {
-    const int64_t tile = step * n_cta + rank;
-    const int64_t t0 = tile * kGlrTile + warp * kTok;
-    const Marks m = marks_of(p.cu_seqlens, p.n_seq, T, t0, lane);
-    float a[kTok][VEC], u[kTok][VEC];
+    const int64_t t0 = (step * n_cta + rank) * ROWS + warp * RUN;
+    const Marks m = marks_of<RUN>(p.cu_seqlens, p.n_seq, T_, t0, lane);
+    sm100::cp_async_wait_group1();
+    __syncthreads();
+    f2 a[RUN], u[RUN];
+    {
+      const char* st = stages + (int)(step & 1) * kStage + warp * RUN * P::kPitch;
+      const uint32_t inc = (uint32_t)C * (uint32_t)sizeof(T);
+      uint32_t rem = ((uint32_t)t0 * (uint32_t)C + (uint32_t)cb) * (uint32_t)sizeof(T);
 #pragma unroll
-    for (int i = 0; i < kTok; ++i) {
-      float x[VEC], l[VEC], b[VEC];
-      rx[i].get(x);
-      rl[i].get(l);
-      if (GATE == kGateBeta) rb[i].get(b);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        float q;
-        decay(l[j], a[i][j], q);
-        const float g = gate_of<GATE>(b[j], q);
-        u[i][j] = GATE == kGateNone ? x[j] : __fmul_rn(g, x[j]);
+      for (int i = 0; i < RUN; ++i) {
+        const char* row = st + i * P::kPitch;
+        const int at = AL ? 0 : (int)(rem & 15u);
+        const f2 x = P::get(row, at, lane);
+        const f2 l = P::get(row + P::bytes(ROWS), at, lane);
+        f2 b = 0, q = 0;
+        if (GATE == kGateBeta) b = P::get(row + 2 * P::bytes(ROWS), at, lane);
+        decay2<GATE>(l, a[i], q);
+        u[i] = gated<GATE>(x, b, q);
+        rem += inc;
       }
     }
-    if (step + 1 < n_steps) load(step + 1);
-    if (m.first != 0) {
+    Run run;
+    if (m.first == 0) {
+      run.A = a[0];
+      run.h = u[0];
 #pragma unroll
-      for (int i = 0; i < kTok; ++i) {
-        const int s = __shfl_sync(0xffffffffu, m.seq, i);
-        if ((m.first >> i & 1) && c_ok) {
-          float h0[VEC];
-          state_get<VEC>(p.initial_state, s, C, c, h0);
+      for (int i = 1; i < RUN; ++i) {
+        run.A = f2_mul(run.A, a[i]);
+        run.h = f2_fma(a[i], run.h, u[i]);
+      }
+    } else {
+      run.A = both(1.f);
+      run.h = both(0.f);
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            // (without a state, 0: a = inf or NaN stays the caller's own)
-            if (p.initial_state != nullptr) u[i][j] = __fmaf_rn(a[i][j], h0[j], u[i][j]);
-            a[i][j] = 0.f;
-          }
+      for (int i = 0; i < RUN; ++i) {
+        if (m.first >> i & 1) {
+          // (without a state, nothing: a_t = inf or NaN stays out of it)
+          if (p.initial_state != nullptr)
+            u[i] = f2_fma(a[i], ch.get(p.initial_state, seq_of(p, t0 + i), C), u[i]);
+          a[i] = run.A = both(0.f);
+          run.h = u[i];
+        } else {
+          run.A = f2_mul(run.A, a[i]);
+          run.h = f2_fma(a[i], run.h, u[i]);
         }
       }
     }
-    // this thread's run of tokens, then the warps' runs
-    Run<VEC> run;
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      run.A[j] = a[0][j];
-      run.h[j] = u[0][j];
-#pragma unroll
-      for (int i = 1; i < kTok; ++i) {
-        run.A[j] = __fmul_rn(run.A[j], a[i][j]);
-        run.h[j] = (m.first >> i & 1) ? u[i][j] : __fmaf_rn(a[i][j], run.h[j], u[i][j]);
-      }
-    }
-    warp_run[warp][lane] = run;
-    __syncthreads();
-    Run<VEC> before;  // the warps before this one
-    Run<VEC> all;     // the whole tile
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      all.A[j] = 1.f;
-      all.h[j] = 0.f;
-    }
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w == warp) before = all;
-      const Run<VEC> r = warp_run[w][lane];
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        all.A[j] = __fmul_rn(all.A[j], r.A[j]);
-        all.h[j] = through(r.A[j], r.h[j], all.h[j]);
-      }
-    }
-    // warp w hands the tile's run to CTA w of the cluster.  The two buffers
+    runs[warp][lane] = run;
+    __syncthreads();  // the runs are complete, and this stage is read
+    load(step + 2);
+    // The tile's run goes to every CTA of the cluster.  The two buffers
     // alternate: a CTA writes step s + 2 only after the barrier of step s + 1,
     // which every CTA reaches after its reads of step s.
-    Run<VEC>(*tr)[32] = tile_run[step & 1];
-    if (warp < n_cta) {
-      const uint32_t dst = sm100::mapa_shared(sm100::smem_u32(&tr[rank][lane]), (uint32_t)warp);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        st_cluster_f32(dst + 4 * j, all.A[j]);
-        st_cluster_f32(dst + 4 * (VEC + j), all.h[j]);
-      }
+    Run(*tr)[32] = tiles + (int)(step & 1) * kMaxCluster;
+    if (warp == 0) {
+      const Run all = fold_tile(runs, lane, false);
+      const uint32_t mine = sm100::smem_u32(&tr[rank][lane]);
+      for (int r = 0; r < n_cta; ++r)
+        st_cluster_run(sm100::mapa_shared(mine, (uint32_t)r), all);
     }
     sm100::cluster_sync();
-    float h[VEC];
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) h[j] = carry[j];
+    f2 h = carry;
     for (int r = 0; r < n_cta; ++r) {
-      if (r == rank) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) h[j] = carry[j];
-      }
-      const Run<VEC> q = tr[r][lane];
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) carry[j] = through(q.A[j], q.h[j], carry[j]);
+      if (r == rank) h = carry;
+      carry = through(tr[r][lane], carry);
     }
-    if (p.checkpoints != nullptr && warp == 0 && c_ok && tile < n_tiles)
-      state_put<VEC>(p.checkpoints, tile, C, c, h);
+    h = through(runs[warp][lane], h);
+    if (p.checkpoints != nullptr && warp % (kGlrTile / RUN) == 0 && t0 < T_)
+      ch.put(p.checkpoints, t0 / kGlrTile, C, h);
+    if (p.y == nullptr) continue;
+    T* y = static_cast<T*>(p.y) + t0 * C;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) h[j] = through(before.A[j], before.h[j], h[j]);
-    if (c_ok && p.y != nullptr) {
-#pragma unroll
-      for (int i = 0; i < kTok; ++i) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j)
-          h[j] = (m.first >> i & 1) ? u[i][j] : __fmaf_rn(a[i][j], h[j], u[i][j]);
-        if (t0 + i < T) R::store(Y + (t0 + i) * C, h);
-        if ((m.last >> i & 1) && p.final_state != nullptr) {
-          // (uniform over the warp's channels that exist; lanes past C hold no sequence)
-          const int s = p.cu_seqlens == nullptr ? 0 : seq_at(p.cu_seqlens, p.n_seq, t0 + i);
-          state_put<VEC>(p.final_state, s, C, c, h);
-        }
-      }
+    for (int i = 0; i < RUN; ++i) {
+      // (a sequence's first token: a = 0, and whatever h was is dropped)
+      h = (m.first >> i & 1) ? u[i] : f2_fma(a[i], h, u[i]);
+      if (t0 + i < T_) put_out<T, AL>(y, ch, h);
+      y += C;
+      if ((m.last >> i & 1) && p.final_state != nullptr)
+        ch.put(p.final_state, seq_of(p, t0 + i), C, h);
     }
   }
-  empty_sequences<VEC>(p.cu_seqlens, p.n_seq, T, p.initial_state, p.final_state, C, c, c_ok,
-                       rank * kWarps + warp, n_cta * kWarps, blockIdx.y == 0 ? p.err : nullptr);
+  empty_sequences<AL>(p, p.initial_state, p.final_state, ch, rank * kWarps + warp,
+                      n_cta * kWarps, blockIdx.y == 0);
 }
 
 // Backward.  With e_t = a_t dh_t (what token t hands to t - 1),
@@ -376,214 +428,149 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(const GlrArgs p) {
 // tiles from the last to the first.  The h_{t-1} of a tile are folded again
 // from the tile's checkpoint (the state before it, from the forward), so the
 // forward carry needs the first two levels only.
-template <typename Tin, int VEC, int GATE>
+template <typename T, int GATE, bool AL>
 __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(const GlrArgs p) {
-  __shared__ Run<VEC> warp_fwd[kWarps][32], warp_rev[kWarps][32];
-  __shared__ Run<VEC> tile_run[2][kMaxCluster][32];
-  using R = Raw<Tin, VEC>;
+  constexpr int RUN = kBwdRun;
+  constexpr int ROWS = kWarps * RUN;
+  constexpr int N = GATE == kGateBeta ? 4 : 3;  // x, log_alpha, dy, beta
+  using P = Piece<T, AL>;
+  extern __shared__ __align__(128) char smem[];
+  Run(*fwd_runs)[32] = reinterpret_cast<Run(*)[32]>(smem);
+  Run(*rev_runs)[32] = fwd_runs + kWarps;
+  Run(*tiles)[32] = rev_runs + kWarps;
+  char* stages = reinterpret_cast<char*>(tiles + 2 * kMaxCluster);
+  const uint32_t stages_u = sm100::smem_u32(stages);
+  constexpr int kStage = N * P::bytes(ROWS);
+
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n_cta = (int)gridDim.x, rank = (int)blockIdx.x;
-  const int C = p.C;
-  const int c = ((int)blockIdx.y * 32 + lane) * VEC;
-  const bool c_ok = c < C;
-  const int64_t T = p.total_T;
-  const int64_t n_tiles = (T + kGlrTile - 1) / kGlrTile;
+  const int C = p.C, cb = (int)blockIdx.y * kChan;
+  const Chan<AL> ch(cb, lane, C);
+  const int64_t T_ = p.total_T;
+  const int64_t n_tiles = (T_ + ROWS - 1) / ROWS;
   const int64_t n_steps = (n_tiles + n_cta - 1) / n_cta;
-  const Tin* X = static_cast<const Tin*>(p.x) + c;
-  const Tin* L = static_cast<const Tin*>(p.log_alpha) + c;
-  const Tin* B = static_cast<const Tin*>(p.beta) + c;
-  const Tin* DY = static_cast<const Tin*>(p.dy) + c;
-  Tin* DX = static_cast<Tin*>(p.dx) + c;
-  Tin* DL = static_cast<Tin*>(p.dlog_alpha) + c;
-  Tin* DB = static_cast<Tin*>(p.dbeta) + c;
-
+  const char* src[N];
+  src[0] = static_cast<const char*>(p.x);
+  src[1] = static_cast<const char*>(p.log_alpha);
+  src[2] = static_cast<const char*>(p.dy);
+  if (N == 4) src[N - 1] = static_cast<const char*>(p.beta);
   // tiles in reverse: rank r of step s has tile n_tiles - 1 - (s n_cta + r),
   // negative (nothing to do, all neutral) behind the first tile
-  R rx[kTok], rl[kTok], rb[kTok], rd[kTok];
-  float ck[VEC];
   auto load = [&](int64_t step) {
-    const int64_t tile = n_tiles - 1 - (step * n_cta + rank);
-    const int64_t t0 = tile * kGlrTile + warp * kTok;
-#pragma unroll
-    for (int i = 0; i < kTok; ++i) {
-      const int64_t t = t0 + i;
-      if (c_ok && t >= 0 && t < T) {
-        rx[i].load(X + t * C);
-        rl[i].load(L + t * C);
-        if (GATE == kGateBeta) rb[i].load(B + t * C);
-        rd[i].load(DY + t * C);
-      } else {
-        rx[i].zero();
-        rl[i].zero();
-        if (GATE == kGateBeta) rb[i].zero();
-        rd[i].zero();
-      }
-    }
-    state_get<VEC>(c_ok && tile >= 0 ? p.checkpoints : nullptr, tile, C, c, ck);
+    if (step < n_steps)
+      load_stage<T, AL, ROWS, N>(stages_u + (int)(step & 1) * kStage, src,
+                                 (n_tiles - 1 - (step * n_cta + rank)) * ROWS, T_, C, cb);
+    sm100::cp_async_commit();
   };
 
-  float carry[VEC];  // e of the token behind this step's last tile
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) carry[j] = 0.f;
+  f2 carry = both(0.f);  // e of the token behind this step's last tile
   if (n_steps > 0) {
     load(0);
     sm100::cluster_sync();
   }
-
   for (int64_t step = 0; step < n_steps; ++step) {
     const int64_t tile = n_tiles - 1 - (step * n_cta + rank);
-    const int64_t t0 = tile * kGlrTile + warp * kTok;
-    Marks m;
-    m.first = m.last = 0;
-    m.seq = 0;
-    if (tile >= 0) m = marks_of(p.cu_seqlens, p.n_seq, T, t0, lane);
-    float a[kTok][VEC], x[kTok][VEC], b[kTok][VEC], d[kTok][VEC], h[VEC];
-#pragma unroll
-    for (int i = 0; i < kTok; ++i) {
-      float l[VEC], be[VEC];
-      rx[i].get(x[i]);
-      rl[i].get(l);
-      rd[i].get(d[i]);
-      if (GATE == kGateBeta) rb[i].get(be);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        float q;
-        decay(l[j], a[i][j], q);
-        b[i][j] = gate_of<GATE>(be[j], q);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) h[j] = ck[j];
-    if (step + 1 < n_steps) load(step + 1);
-    // dh_T joins its sequence's last dy
-    if (m.last != 0 && p.d_final_state != nullptr) {
-#pragma unroll
-      for (int i = 0; i < kTok; ++i) {
-        const int s = __shfl_sync(0xffffffffu, m.seq, i);
-        if ((m.last >> i & 1) && c_ok) {
-          float f[VEC];
-          state_get<VEC>(p.d_final_state, s, C, c, f);
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) d[i][j] = __fadd_rn(d[i][j], f[j]);
-        }
-      }
-    }
-    // h before a token: h_0 of its sequence where that begins
-    auto enter = [&](int i, float* hh) {
-      if (m.first >> i & 1) {
-        const int s = p.cu_seqlens == nullptr ? 0 : seq_at(p.cu_seqlens, p.n_seq, t0 + i);
-        state_get<VEC>(c_ok ? p.initial_state : nullptr, s, C, c, hh);
-      }
+    const int64_t t0 = tile * ROWS + warp * RUN;
+    const Marks m = marks_of<RUN>(p.cu_seqlens, p.n_seq, T_, t0, lane);
+    f2 h = both(0.f);
+    if (warp == 1 && tile >= 0) h = ch.get(p.checkpoints, tile, C);
+    sm100::cp_async_wait_all();
+    __syncthreads();  // this step's inputs have landed; the other stage is read
+    load(step + 1);
+    const char* st = stages + (int)(step & 1) * kStage + warp * RUN * P::kPitch;
+    const uint32_t inc = (uint32_t)C * (uint32_t)sizeof(T);
+    const uint32_t rem0 = ((uint32_t)t0 * (uint32_t)C + (uint32_t)cb) * (uint32_t)sizeof(T);
+    auto in = [&](int k, int i) {  // tensor k at token i of the run
+      return P::get(st + k * P::bytes(ROWS) + i * P::kPitch,
+                    AL ? 0 : (int)((rem0 + (uint32_t)i * inc) & 15u), lane);
     };
-    Run<VEC> fr, rr;
+    // dh_T joins its sequence's last dy; h_0 enters where a sequence begins
+    auto dy_at = [&](int i) {
+      f2 d = in(2, i);
+      if ((m.last >> i & 1) && p.d_final_state != nullptr)
+        d = f2_add(d, ch.get(p.d_final_state, seq_of(p, t0 + i), C));
+      return d;
+    };
+    f2 a[RUN], u[RUN], om[RUN];  // om: 1 - a
+    Run fr, rr;
+    fr.A = rr.A = both(1.f);
+    fr.h = rr.h = both(0.f);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      fr.A[j] = rr.A[j] = 1.f;
-      fr.h[j] = rr.h[j] = 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < kTok; ++i) {
-      enter(i, fr.h);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        fr.A[j] = (m.first >> i & 1) ? 0.f : __fmul_rn(fr.A[j], a[i][j]);
-        fr.h[j] = __fmaf_rn(a[i][j], fr.h[j], __fmul_rn(b[i][j], x[i][j]));
+    for (int i = 0; i < RUN; ++i) {
+      decay2<GATE>(in(1, i), a[i], om[i]);
+      u[i] = gated<GATE>(in(0, i), GATE == kGateBeta ? in(N - 1, i) : 0, om[i]);
+      if (m.first >> i & 1) {
+        fr.h = ch.get(p.initial_state, seq_of(p, t0 + i), C);
+        fr.A = both(0.f);
       }
+      fr.A = f2_mul(fr.A, a[i]);
+      fr.h = f2_fma(a[i], fr.h, u[i]);
     }
 #pragma unroll
-    for (int i = kTok - 1; i >= 0; --i) {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const bool last = m.last >> i & 1;
-        rr.A[j] = last ? 0.f : __fmul_rn(rr.A[j], a[i][j]);
-        rr.h[j] = __fmul_rn(a[i][j], __fadd_rn(d[i][j], last ? 0.f : rr.h[j]));
-      }
+    for (int i = RUN - 1; i >= 0; --i) {
+      if (m.last >> i & 1) rr.A = rr.h = both(0.f);
+      rr.A = f2_mul(rr.A, a[i]);
+      rr.h = f2_mul(a[i], f2_add(dy_at(i), rr.h));
     }
-    warp_fwd[warp][lane] = fr;
-    warp_rev[warp][lane] = rr;
+    // (a run with a first token forgets what was before it even where a is
+    // infinite or NaN)
+    if (m.first != 0) fr.A = both(0.f);
+    if (m.last != 0) rr.A = both(0.f);
+    fwd_runs[warp][lane] = fr;
+    rev_runs[warp][lane] = rr;
     __syncthreads();
-    Run<VEC> behind, all;  // the warps behind this one, the whole tile, in reverse
+    Run(*tr)[32] = tiles + (int)(step & 1) * kMaxCluster;  // (two buffers: see the forward)
+    if (warp == 0) {
+      const Run all = fold_tile(rev_runs, lane, true);
+      const uint32_t mine = sm100::smem_u32(&tr[rank][lane]);
+      for (int r = 0; r < n_cta; ++r)
+        st_cluster_run(sm100::mapa_shared(mine, (uint32_t)r), all);
+    } else if (warp == 1) {  // the state before each run, left in its h
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      all.A[j] = 1.f;
-      all.h[j] = 0.f;
-    }
-#pragma unroll
-    for (int w = kWarps - 1; w >= 0; --w) {
-      if (w == warp) behind = all;
-      const Run<VEC> r = warp_rev[w][lane];
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        all.A[j] = __fmul_rn(all.A[j], r.A[j]);
-        all.h[j] = through(r.A[j], r.h[j], all.h[j]);
+      for (int w = 0; w < kWarps; ++w) {
+        const Run r = fwd_runs[w][lane];
+        fwd_runs[w][lane].h = h;
+        h = through(r, h);
       }
-    }
-    Run<VEC>(*tr)[32] = tile_run[step & 1];  // (two buffers: see the forward)
-    if (warp < n_cta) {
-      const uint32_t dst = sm100::mapa_shared(sm100::smem_u32(&tr[rank][lane]), (uint32_t)warp);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        st_cluster_f32(dst + 4 * j, all.A[j]);
-        st_cluster_f32(dst + 4 * (VEC + j), all.h[j]);
-      }
-    }
-    // the state before this warp's tokens
-    for (int w = 0; w < warp; ++w) {
-      const Run<VEC> r = warp_fwd[w][lane];
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) h[j] = through(r.A[j], r.h[j], h[j]);
     }
     sm100::cluster_sync();
-    float e[VEC];
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) e[j] = carry[j];
+    f2 e = carry;
     for (int r = 0; r < n_cta; ++r) {
-      if (r == rank) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) e[j] = carry[j];
-      }
-      const Run<VEC> q = tr[r][lane];
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) carry[j] = through(q.A[j], q.h[j], carry[j]);
+      if (r == rank) e = carry;
+      carry = through(tr[r][lane], carry);
     }
+    e = through(rev_runs[warp][lane], e);
+    h = fwd_runs[warp][lane].h;
+    // h_{t-1} of every token (into u), then the gradients from the last token back
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) e[j] = through(behind.A[j], behind.h[j], e[j]);
-    // h_{t-1} of every token, then the gradients from the last token back
-    float hb[kTok][VEC];
-#pragma unroll
-    for (int i = 0; i < kTok; ++i) {
-      enter(i, h);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        hb[i][j] = h[j];
-        h[j] = __fmaf_rn(a[i][j], h[j], __fmul_rn(b[i][j], x[i][j]));
-      }
+    for (int i = 0; i < RUN; ++i) {
+      if (m.first >> i & 1) h = ch.get(p.initial_state, seq_of(p, t0 + i), C);
+      const f2 before = h;
+      h = f2_fma(a[i], h, u[i]);
+      u[i] = before;
     }
+    const int64_t o0 = t0 * C;
 #pragma unroll
-    for (int i = kTok - 1; i >= 0; --i) {
-      const int64_t t = t0 + i;
-      float dx[VEC], dl[VEC], db[VEC];
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float dh = __fadd_rn(d[i][j], (m.last >> i & 1) ? 0.f : e[j]);
-        e[j] = __fmul_rn(a[i][j], dh);
-        dx[j] = GATE == kGateNone ? dh : __fmul_rn(b[i][j], dh);
-        db[j] = __fmul_rn(x[i][j], dh);
-        dl[j] = __fmul_rn(GATE == kGateComp ? __fsub_rn(hb[i][j], x[i][j]) : hb[i][j], e[j]);
-      }
-      if (c_ok && t >= 0 && t < T) {
-        R::store(DX + t * C, dx);
-        R::store(DL + t * C, dl);
-        if (GATE == kGateBeta) R::store(DB + t * C, db);
-        if ((m.first >> i & 1) && p.d_initial_state != nullptr) {
-          const int s = p.cu_seqlens == nullptr ? 0 : seq_at(p.cu_seqlens, p.n_seq, t);
-          state_put<VEC>(p.d_initial_state, s, C, c, e);
-        }
+    for (int i = RUN - 1; i >= 0; --i) {
+      const f2 x = in(0, i);
+      f2 dh = dy_at(i);
+      if (!(m.last >> i & 1)) dh = f2_add(dh, e);
+      e = f2_mul(a[i], dh);
+      if (t0 + i >= 0 && t0 + i < T_) {
+        const int64_t o = o0 + (int64_t)i * C;
+        put_out<T, AL>(static_cast<T*>(p.dx) + o, ch,
+                       gated<GATE>(dh, GATE == kGateBeta ? in(N - 1, i) : 0, om[i]));
+        f2 hb = u[i];
+        if (GATE == kGateComp) hb = f2_fma(x, both(-1.f), hb);
+        put_out<T, AL>(static_cast<T*>(p.dlog_alpha) + o, ch, f2_mul(hb, e));
+        if (GATE == kGateBeta) put_out<T, AL>(static_cast<T*>(p.dbeta) + o, ch, f2_mul(x, dh));
+        if ((m.first >> i & 1) && p.d_initial_state != nullptr)
+          ch.put(p.d_initial_state, seq_of(p, t0 + i), C, e);
       }
     }
   }
-  empty_sequences<VEC>(p.cu_seqlens, p.n_seq, T, p.d_final_state, p.d_initial_state, C, c, c_ok,
-                       rank * kWarps + warp, n_cta * kWarps, blockIdx.y == 0 ? p.err : nullptr);
+  empty_sequences<AL>(p, p.d_final_state, p.d_initial_state, ch, rank * kWarps + warp,
+                      n_cta * kWarps, blockIdx.y == 0);
 }
 
 // One token: [N, C] arrays, all dense and of one shape, so n = N C values in
@@ -597,11 +584,12 @@ __global__ void __launch_bounds__(256) glr_step_kernel(const Tin* __restrict__ x
                                                        Tin* __restrict__ y, int64_t n) {
   const int64_t i0 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 8;
   if (i0 >= n) return;
-  auto one = [&](float xv, float lv, float bv, float h) {
-    float a, q;
-    decay(lv, a, q);
-    const float g = gate_of<GATE>(bv, q);
-    return __fmaf_rn(a, h, GATE == kGateNone ? xv : __fmul_rn(g, xv));
+  auto two = [&](float x0, float x1, float l0, float l1, float b0, float b1, float& h0,
+                 float& h1) {
+    f2 a, q = 0;
+    decay2<GATE>(f2_pack(l0, l1), a, q);
+    const f2 u = gated<GATE>(f2_pack(x0, x1), f2_pack(b0, b1), q);
+    f2_unpack(f2_fma(a, f2_pack(h0, h1), u), h0, h1);
   };
   if (i0 + 8 <= n) {
 #pragma unroll
@@ -610,17 +598,16 @@ __global__ void __launch_bounds__(256) glr_step_kernel(const Tin* __restrict__ x
       float4 bv = make_float4(0.f, 0.f, 0.f, 0.f);
       if (GATE == kGateBeta) bv = Elem<Tin>::load4(beta + i0 + k);
       float4 h = *reinterpret_cast<const float4*>(state + i0 + k);
-      h.x = one(xv.x, lv.x, bv.x, h.x);
-      h.y = one(xv.y, lv.y, bv.y, h.y);
-      h.z = one(xv.z, lv.z, bv.z, h.z);
-      h.w = one(xv.w, lv.w, bv.w, h.w);
+      two(xv.x, xv.y, lv.x, lv.y, bv.x, bv.y, h.x, h.y);
+      two(xv.z, xv.w, lv.z, lv.w, bv.z, bv.w, h.z, h.w);
       *reinterpret_cast<float4*>(state + i0 + k) = h;
       Elem<Tin>::store4(y + i0 + k, h);
     }
   } else {
     for (int64_t i = i0; i < n; ++i) {
-      const float h = one(Elem<Tin>::load(x + i), Elem<Tin>::load(la + i),
-                          GATE == kGateBeta ? Elem<Tin>::load(beta + i) : 0.f, state[i]);
+      float h = state[i], unused = 0.f;
+      two(Elem<Tin>::load(x + i), 0.f, Elem<Tin>::load(la + i), 0.f,
+          GATE == kGateBeta ? Elem<Tin>::load(beta + i) : 0.f, 0.f, h, unused);
       state[i] = h;
       Elem<Tin>::store(y + i, h);
     }
@@ -629,23 +616,32 @@ __global__ void __launch_bounds__(256) glr_step_kernel(const Tin* __restrict__ x
 
 using ScanKernel = void (*)(GlrArgs);
 
-template <typename Tin, int VEC>
-ScanKernel scan_kernel(bool bwd, int gate) {
-  switch (gate) {
-    case kGateNone:
-      return bwd ? glr_bwd_kernel<Tin, VEC, kGateNone> : glr_fwd_kernel<Tin, VEC, kGateNone>;
-    case kGateBeta:
-      return bwd ? glr_bwd_kernel<Tin, VEC, kGateBeta> : glr_fwd_kernel<Tin, VEC, kGateBeta>;
-    default:
-      return bwd ? glr_bwd_kernel<Tin, VEC, kGateComp> : glr_fwd_kernel<Tin, VEC, kGateComp>;
-  }
+// One compiled scan: its kernel, shared memory and tokens per tile.
+struct Scan {
+  ScanKernel kernel;
+  int smem, rows;
+};
+
+template <typename T, bool AL, int GATE>
+Scan scan_of(bool bwd) {
+  constexpr int F = fwd_run<T, AL>(), G = GATE == kGateBeta ? 1 : 0;
+  return bwd ? Scan{glr_bwd_kernel<T, GATE, AL>, scan_smem<T, AL>(kBwdRun, 3 + G, 2),
+                    kWarps * kBwdRun}
+             : Scan{glr_fwd_kernel<T, GATE, AL>, scan_smem<T, AL>(F, 2 + G, 1), kWarps * F};
+}
+template <typename T, bool AL>
+Scan scan_for(bool bwd, int gate) {
+  return gate == kGateNone   ? scan_of<T, AL, kGateNone>(bwd)
+         : gate == kGateBeta ? scan_of<T, AL, kGateBeta>(bwd)
+                             : scan_of<T, AL, kGateComp>(bwd);
 }
 
-cudaLaunchConfig_t scan_config(int cluster, int groups, cudaStream_t stream,
+cudaLaunchConfig_t scan_config(const Scan& k, int cluster, int groups, cudaStream_t stream,
                                cudaLaunchAttribute* attr) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)cluster, (unsigned)groups);
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)k.smem;
   cfg.stream = stream;
   attr->id = cudaLaunchAttributeClusterDimension;
   attr->val.clusterDim.x = (unsigned)cluster;
@@ -662,37 +658,40 @@ constexpr int kMaxDevices = 64;
 constexpr int kVariants = 2 * 2 * 2 * 3;
 std::atomic<int> g_fit[kMaxDevices][kVariants][kMaxCluster + 1];
 
-int clusters_that_fit(int dev, int variant, ScanKernel k, int cluster) {
+int clusters_that_fit(int dev, int variant, const Scan& k, int cluster) {
   std::atomic<int>& slot = g_fit[dev][variant][cluster];
   int n = slot.load(std::memory_order_relaxed);
   if (n != 0) return n;
   cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = scan_config(cluster, 1, nullptr, &attr);
-  if (cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess || n < 1) return 0;
+  const cudaLaunchConfig_t cfg = scan_config(k, cluster, 1, nullptr, &attr);
+  if (cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem) !=
+          cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, k.kernel, &cfg) != cudaSuccess || n < 1)
+    return 0;
   slot.store(n, std::memory_order_relaxed);
   return n;
 }
 
 gdn_status launch_scan(const GlrArgs& a, bool bwd, cudaStream_t stream) {
   const bool bf16 = a.dtype == GDN_BF16;
-  const int vec = a.C % 2 == 0 ? 2 : 1;  // an odd row length leaves every other row odd
-  const ScanKernel k =
-      bf16 ? (vec == 2 ? scan_kernel<__nv_bfloat16, 2>(bwd, a.gate)
-                       : scan_kernel<__nv_bfloat16, 1>(bwd, a.gate))
-           : (vec == 2 ? scan_kernel<float, 2>(bwd, a.gate) : scan_kernel<float, 1>(bwd, a.gate));
-  const int variant = ((bf16 ? 0 : 1) * 2 + (vec - 1)) * 2 * 3 + (bwd ? 3 : 0) + a.gate;
+  const bool al = (int64_t)a.C * (bf16 ? 2 : 4) % 16 == 0;
+  const Scan k = bf16 ? (al ? scan_for<__nv_bfloat16, true>(bwd, a.gate)
+                            : scan_for<__nv_bfloat16, false>(bwd, a.gate))
+                      : (al ? scan_for<float, true>(bwd, a.gate)
+                            : scan_for<float, false>(bwd, a.gate));
+  const int variant = ((bf16 ? 0 : 1) * 2 + (al ? 0 : 1)) * 6 + (bwd ? 3 : 0) + a.gate;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return GDN_ERR_CUDA;
-  const int groups = (a.C + 32 * vec - 1) / (32 * vec);
-  if (groups > 65535) return GDN_ERR_UNSUPPORTED;
+  const int groups = (a.C + kChan - 1) / kChan;
   // The largest cluster (consecutive tiles in flight per channel group) at
   // which all groups' clusters are on the device at once.
-  const int64_t n_tiles = (a.total_T + kGlrTile - 1) / kGlrTile;
+  const int64_t n_tiles = (a.total_T + k.rows - 1) / k.rows;
   int cluster = (int)(n_tiles < kMaxCluster ? (n_tiles < 1 ? 1 : n_tiles) : kMaxCluster);
   while (cluster > 1 && clusters_that_fit(dev, variant, k, cluster) < groups) --cluster;
+  if (clusters_that_fit(dev, variant, k, cluster) < 1) return GDN_ERR_CUDA;
   cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = scan_config(cluster, groups, stream, &attr);
-  return cudaLaunchKernelEx(&cfg, k, a) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  const cudaLaunchConfig_t cfg = scan_config(k, cluster, groups, stream, &attr);
+  return cudaLaunchKernelEx(&cfg, k.kernel, a) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 template <typename Tin>
