@@ -90,34 +90,43 @@ __device__ __forceinline__ int seq_at(const int32_t* cu, int n_seq, int64_t t) {
 }
 
 // Which of a run's tokens from t0 on begin or end a sequence (bit i: token
-// t0 + i; tokens outside [0, total_T) neither).
+// t0 + i; tokens outside [0, total_T) neither); lane i has token i's sequence.
+// The bounds [lo, hi) of the sequence that the run leaves into are kept: most
+// runs lie inside it and need no look at the offsets.
+template <int RUN, bool BACK>
 struct Marks {
-  uint32_t first, last;
+  uint32_t first = 0, last = 0;
+  int seq = 0;
+  int64_t lo = 0, hi = 0;
+
+  __device__ __forceinline__ void look(const GlrArgs& p, int64_t t0, int lane) {
+    first = last = 0;
+    if (p.cu_seqlens == nullptr) {
+      if (t0 <= 0 && t0 + RUN > 0) first = 1u << (int)(-t0);
+      const int64_t d = p.total_T - 1 - t0;
+      if (d >= 0 && d < RUN) last = 1u << (int)d;
+      return;
+    }
+    if (lo < t0 && t0 + RUN < hi) return;
+    const int64_t t = t0 + lane;
+    int64_t l = 0, h = 0;
+    bool f = false, e = false;
+    if (lane < RUN && t >= 0 && t < p.total_T) {
+      seq = seq_at(p.cu_seqlens, p.n_seq, t);
+      l = __ldg(p.cu_seqlens + seq);
+      h = __ldg(p.cu_seqlens + seq + 1);
+      f = l == t;
+      e = h == t + 1;
+    }
+    first = __ballot_sync(0xffffffffu, f);
+    last = __ballot_sync(0xffffffffu, e);
+    lo = __shfl_sync(0xffffffffu, l, BACK ? 0 : RUN - 1);
+    hi = __shfl_sync(0xffffffffu, h, BACK ? 0 : RUN - 1);
+  }
+  __device__ __forceinline__ int seq_of(int i) const {
+    return __shfl_sync(0xffffffffu, seq, i);
+  }
 };
-template <int RUN>
-__device__ __forceinline__ Marks marks_of(const int32_t* cu, int n_seq, int64_t total_T,
-                                          int64_t t0, int lane) {
-  Marks m;
-  if (cu == nullptr) {
-    m.first = t0 == 0 ? 1u : 0u;
-    const int64_t d = total_T - 1 - t0;
-    m.last = d >= 0 && d < RUN ? 1u << (int)d : 0u;
-    return m;
-  }
-  bool f = false, l = false;
-  const int64_t t = t0 + lane;
-  if (lane < RUN && t >= 0 && t < total_T) {
-    const int s = seq_at(cu, n_seq, t);
-    f = __ldg(cu + s) == t;
-    l = __ldg(cu + s + 1) == t + 1;
-  }
-  m.first = __ballot_sync(0xffffffffu, f);
-  m.last = __ballot_sync(0xffffffffu, l);
-  return m;
-}
-__device__ __forceinline__ int64_t seq_of(const GlrArgs& p, int64_t t) {
-  return p.cu_seqlens == nullptr ? 0 : seq_at(p.cu_seqlens, p.n_seq, t);
-}
 
 // A composed run, two channels.
 struct __align__(16) Run {
@@ -184,20 +193,23 @@ struct Piece {
   }
 };
 
+// Stores a lane's two channels of a token row; `base` is the same for the whole
+// CTA, `off` the bytes from it to the row's channel 0.
 template <typename T, bool AL>
-__device__ __forceinline__ void put_out(T* row, const Chan<AL>& ch, f2 v) {
+__device__ __forceinline__ void put_out(char* base, uint32_t off, const Chan<AL>& ch, f2 v) {
   float v0, v1;
   f2_unpack(v, v0, v1);
+  T* q = reinterpret_cast<T*>(base + (off + (uint32_t)ch.c0 * (uint32_t)sizeof(T)));
   if (AL) {
     if (ch.ok0) {
       if (sizeof(T) == 2)
-        *reinterpret_cast<uint32_t*>(row + ch.c0) = sm100::pack_bf16(v0, v1);
+        *reinterpret_cast<uint32_t*>(q) = sm100::pack_bf16(v0, v1);
       else
-        *reinterpret_cast<f2*>(row + ch.c0) = v;
+        *reinterpret_cast<f2*>(q) = v;
     }
   } else {
-    if (ch.ok0) Elem<T>::store(row + ch.c0, v0);
-    if (ch.ok1) Elem<T>::store(row + ch.c1, v1);
+    if (ch.ok0) Elem<T>::store(q, v0);
+    if (ch.ok1) Elem<T>::store(q + 32, v1);
   }
 }
 
@@ -213,31 +225,56 @@ template <typename T, bool AL, int ROWS, int N>
 __device__ __forceinline__ void load_stage(uint32_t stage, const char* const (&src)[N], int64_t t0,
                                            int64_t total_T, int C, int cb) {
   using P = Piece<T, AL>;
-  const int64_t row_bytes = (int64_t)C * (int)sizeof(T);
-  const int64_t all = total_T * row_bytes;
-  for (int i = threadIdx.x; i < ROWS * P::kCopies; i += kThreads) {
-    const int r = i / P::kCopies, q = i % P::kCopies;
-    const int64_t t = t0 + r;
-    int64_t off = t * row_bytes + (int64_t)cb * (int)sizeof(T);
-    if (!AL) off &= ~(int64_t)15;
-    off += 16 * q;
-    int n = 0;
-    if (t >= 0 && t < total_T) {
-      if (AL)
-        n = cb * (int)sizeof(T) + 16 * q < row_bytes ? 16 : 0;
-      else
-        n = all - off >= 16 ? 16 : all - off > 0 ? (int)(all - off) : 0;
-    }
-    if (n == 0) off = 0;
+  const uint32_t row_bytes = (uint32_t)C * (uint32_t)sizeof(T);
+  if constexpr (AL) {
+    // a thread has one 16-byte column of every (kThreads / kCopies)th row
+    constexpr int kStep = kThreads / P::kCopies;
+    static_assert(kThreads % P::kCopies == 0 && ROWS % kStep == 0, "whole rounds");
+    const int q = (int)threadIdx.x % P::kCopies, r0 = (int)threadIdx.x / P::kCopies;
+    const uint32_t col = (uint32_t)cb * (uint32_t)sizeof(T) + 16u * q;
+    const bool ok = col < row_bytes;
+    uint32_t off = (uint32_t)r0 * row_bytes + col;
+    uint32_t dst = stage + r0 * P::kPitch + 16 * q;
+    const char* base[N];
+    const int64_t at = (t0 < 0 ? 0 : t0) * (int64_t)row_bytes;
 #pragma unroll
-    for (int k = 0; k < N; ++k)
-      copy16(stage + k * P::bytes(ROWS) + r * P::kPitch + 16 * q, src[k] + off, n);
+    for (int k = 0; k < N; ++k) base[k] = src[k] + at;
+    const bool whole = t0 >= 0 && t0 + ROWS <= total_T;
+#pragma unroll
+    for (int i = 0; i < ROWS / kStep; ++i) {
+      const int64_t t = t0 + r0 + i * kStep;
+      const bool in = ok && (whole || (t >= 0 && t < total_T));
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        copy16(dst + k * P::bytes(ROWS), base[k] + (in ? off : 0u), in ? 16 : 0);
+      off += kStep * row_bytes;
+      dst += kStep * P::kPitch;
+    }
+  } else {
+    const int64_t all = total_T * (int64_t)row_bytes;
+    for (int i = threadIdx.x; i < ROWS * P::kCopies; i += kThreads) {
+      const int r = i / P::kCopies, q = i % P::kCopies;
+      const int64_t t = t0 + r;
+      int64_t off = ((t * (int64_t)row_bytes + (int64_t)cb * (int)sizeof(T)) & ~(int64_t)15) +
+                    16 * q;
+      int n = 0;
+      if (t >= 0 && t < total_T) n = all - off >= 16 ? 16 : all - off > 0 ? (int)(all - off) : 0;
+      if (n == 0) off = 0;
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        copy16(stage + k * P::bytes(ROWS) + r * P::kPitch + 16 * q, src[k] + off, n);
+    }
   }
 }
 
-__device__ __forceinline__ void st_cluster_run(uint32_t addr, const Run& r) {
-  asm volatile("st.shared::cluster.v2.b64 [%0], {%1, %2};" ::"r"(addr), "l"(r.A), "l"(r.h)
-               : "memory");
+// A tile's run to one CTA of the cluster (its address there), counted on that
+// CTA's barrier.
+__device__ __forceinline__ void send_run(uint32_t addr, uint32_t bar, const Run& r) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];" ::
+          "r"(addr),
+      "l"(r.A), "l"(r.h), "r"(bar)
+      : "memory");
 }
 
 // One warp: turns the runs of a tile (in[w], in the order `first, first +
@@ -257,6 +294,55 @@ __device__ __forceinline__ Run fold_tile(Run (*runs)[32], int lane, bool backwar
   }
   return all;
 }
+
+// The cluster's exchange of tile runs.  In every step each CTA sends its tile's
+// run to all CTAs (itself too) and waits on its own barrier for theirs: the
+// stores carry the signal, so no fence waits for the outputs of the step
+// before.  Two buffers alternate: a CTA sends step s + 2 only after it has
+// everyone's step s + 1, which each sends after its reads of step s.
+constexpr uint32_t kWait = 1u << 24;
+struct Exchange {
+  Run (*tiles)[32];  // [2][kMaxCluster]
+  uint64_t* bar;     // [2]
+  int n_cta, rank;
+  bool ok = true;
+
+  // (by every thread, before the cluster's first barrier)
+  __device__ __forceinline__ void init() {
+    if (threadIdx.x == 0) {
+      sm100::mbar_init(&bar[0], 1);
+      sm100::mbar_init(&bar[1], 1);
+      sm100::fence_mbar_init();
+    }
+  }
+  // (by one warp)
+  __device__ __forceinline__ void send(int64_t step, int lane, const Run& all) {
+    const int b = (int)(step & 1);
+    if (lane == 0)
+      sm100::mbar_arrive_expect_tx(&bar[b], (uint32_t)n_cta * 32u * (uint32_t)sizeof(Run));
+    __syncwarp();
+    const uint32_t at = sm100::smem_u32(&tiles[b * kMaxCluster + rank][lane]);
+    const uint32_t on = sm100::smem_u32(&bar[b]);
+    for (int r = 0; r < n_cta; ++r)
+      send_run(sm100::mapa_shared(at, (uint32_t)r), sm100::mapa_shared(on, (uint32_t)r), all);
+  }
+  // Waits for the step's runs; h: the carry before this CTA's tile; carry
+  // moves on past the whole step.
+  __device__ __forceinline__ f2 receive(int64_t step, int lane, f2& carry, int* err) {
+    const int b = (int)(step & 1);
+    if (ok && !sm100::mbar_wait_cluster(&bar[b], (uint32_t)(step >> 1) & 1u, kWait)) {
+      ok = false;  // never waits again; every later step still sends
+      if (lane == 0) atomicOr(err, kErrTimeout);
+    }
+    f2 h = carry;
+#pragma unroll 4
+    for (int r = 0; r < n_cta; ++r) {
+      if (r == rank) h = carry;
+      carry = through(tiles[b * kMaxCluster + r][lane], carry);
+    }
+    return h;
+  }
+};
 
 // Sequences without tokens carry their state through: out[s] = in[s] (or 0).
 // Also reports a malformed cu_seqlens.  Rows are shared out over the
@@ -286,7 +372,7 @@ __device__ __forceinline__ void empty_sequences(const GlrArgs& p, const float* i
 template <typename T, bool AL>
 constexpr int scan_smem(int run, int tensors, int run_sets) {
   return run_sets * kWarps * 32 * (int)sizeof(Run) + 2 * kMaxCluster * 32 * (int)sizeof(Run) +
-         2 * tensors * Piece<T, AL>::bytes(kWarps * run);
+         128 + 2 * tensors * Piece<T, AL>::bytes(kWarps * run);
 }
 
 // Tokens of a thread's run.
@@ -303,18 +389,23 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(const GlrArgs p) {
   using P = Piece<T, AL>;
   extern __shared__ __align__(128) char smem[];
   Run(*runs)[32] = reinterpret_cast<Run(*)[32]>(smem);
-  Run(*tiles)[32] = runs + kWarps;  // [2][kMaxCluster]
-  char* stages = reinterpret_cast<char*>(tiles + 2 * kMaxCluster);
+  Exchange ex;
+  ex.tiles = runs + kWarps;
+  ex.bar = reinterpret_cast<uint64_t*>(ex.tiles + 2 * kMaxCluster);
+  char* stages = reinterpret_cast<char*>(ex.bar) + 128;
   const uint32_t stages_u = sm100::smem_u32(stages);
   constexpr int kStage = N * P::bytes(ROWS);
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n_cta = (int)gridDim.x, rank = (int)blockIdx.x;  // one cluster along x
+  ex.n_cta = n_cta;
+  ex.rank = rank;
   const int C = p.C, cb = (int)blockIdx.y * kChan;
   const Chan<AL> ch(cb, lane, C);
   const int64_t T_ = p.total_T;
   const int64_t n_tiles = (T_ + ROWS - 1) / ROWS;
   const int64_t n_steps = (n_tiles + n_cta - 1) / n_cta;
+  const uint32_t row_bytes = (uint32_t)C * (uint32_t)sizeof(T);
   const char* src[N];
   src[0] = static_cast<const char*>(p.x);
   src[1] = static_cast<const char*>(p.log_alpha);
@@ -327,94 +418,87 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(const GlrArgs p) {
   };
 
   f2 carry = both(0.f);  // state before this step's first tile
+  Marks<RUN, false> m;
   if (n_steps > 0) {
     load(0);
     load(1);
-    sm100::cluster_sync();  // every CTA runs before any writes into another's shared memory
+    ex.init();
+    sm100::cluster_sync();  // every CTA runs, its barriers set, before any sends
   }
   for (int64_t step = 0; step < n_steps; ++step) {
-    const int64_t t0 = (step * n_cta + rank) * ROWS + warp * RUN;
-    const Marks m = marks_of<RUN>(p.cu_seqlens, p.n_seq, T_, t0, lane);
+    const int64_t tile0 = (step * n_cta + rank) * ROWS, t0 = tile0 + warp * RUN;
+    m.look(p, t0, lane);
     sm100::cp_async_wait_group1();
     __syncthreads();
     f2 a[RUN], u[RUN];
+    Run run;
     {
       const char* st = stages + (int)(step & 1) * kStage + warp * RUN * P::kPitch;
-      const uint32_t inc = (uint32_t)C * (uint32_t)sizeof(T);
-      uint32_t rem = ((uint32_t)t0 * (uint32_t)C + (uint32_t)cb) * (uint32_t)sizeof(T);
+      const uint32_t rem = (uint32_t)t0 * row_bytes + (uint32_t)cb * (uint32_t)sizeof(T);
+      run.A = both(1.f);
+      run.h = both(0.f);
 #pragma unroll
       for (int i = 0; i < RUN; ++i) {
         const char* row = st + i * P::kPitch;
-        const int at = AL ? 0 : (int)(rem & 15u);
+        const int at = AL ? 0 : (int)((rem + (uint32_t)i * row_bytes) & 15u);
         const f2 x = P::get(row, at, lane);
         const f2 l = P::get(row + P::bytes(ROWS), at, lane);
         f2 b = 0, q = 0;
         if (GATE == kGateBeta) b = P::get(row + 2 * P::bytes(ROWS), at, lane);
         decay2<GATE>(l, a[i], q);
         u[i] = gated<GATE>(x, b, q);
-        rem += inc;
-      }
-    }
-    Run run;
-    if (m.first == 0) {
-      run.A = a[0];
-      run.h = u[0];
-#pragma unroll
-      for (int i = 1; i < RUN; ++i) {
         run.A = f2_mul(run.A, a[i]);
         run.h = f2_fma(a[i], run.h, u[i]);
       }
-    } else {
-      run.A = both(1.f);
-      run.h = both(0.f);
+    }
+    if (m.first != 0) {  // again, with the sequences' first tokens cut off
 #pragma unroll
       for (int i = 0; i < RUN; ++i) {
+        const int s = m.seq_of(i);
         if (m.first >> i & 1) {
           // (without a state, nothing: a_t = inf or NaN stays out of it)
           if (p.initial_state != nullptr)
-            u[i] = f2_fma(a[i], ch.get(p.initial_state, seq_of(p, t0 + i), C), u[i]);
-          a[i] = run.A = both(0.f);
+            u[i] = f2_fma(a[i], ch.get(p.initial_state, s, C), u[i]);
+          a[i] = both(0.f);
           run.h = u[i];
         } else {
-          run.A = f2_mul(run.A, a[i]);
-          run.h = f2_fma(a[i], run.h, u[i]);
+          run.h = i == 0 ? u[0] : f2_fma(a[i], run.h, u[i]);
         }
       }
+      run.A = both(0.f);
     }
     runs[warp][lane] = run;
     __syncthreads();  // the runs are complete, and this stage is read
     load(step + 2);
-    // The tile's run goes to every CTA of the cluster.  The two buffers
-    // alternate: a CTA writes step s + 2 only after the barrier of step s + 1,
-    // which every CTA reaches after its reads of step s.
-    Run(*tr)[32] = tiles + (int)(step & 1) * kMaxCluster;
-    if (warp == 0) {
-      const Run all = fold_tile(runs, lane, false);
-      const uint32_t mine = sm100::smem_u32(&tr[rank][lane]);
-      for (int r = 0; r < n_cta; ++r)
-        st_cluster_run(sm100::mapa_shared(mine, (uint32_t)r), all);
-    }
-    sm100::cluster_sync();
-    f2 h = carry;
-    for (int r = 0; r < n_cta; ++r) {
-      if (r == rank) h = carry;
-      carry = through(tr[r][lane], carry);
-    }
+    if (warp == 0) ex.send(step, lane, fold_tile(runs, lane, false));
+    __syncthreads();  // the fold is in shared memory
+    f2 h = ex.receive(step, lane, carry, p.err);
     h = through(runs[warp][lane], h);
     if (p.checkpoints != nullptr && warp % (kGlrTile / RUN) == 0 && t0 < T_)
       ch.put(p.checkpoints, t0 / kGlrTile, C, h);
     if (p.y == nullptr) continue;
-    T* y = static_cast<T*>(p.y) + t0 * C;
+    char* y = static_cast<char*>(p.y) + tile0 * row_bytes;
+    uint32_t off = (uint32_t)(warp * RUN) * row_bytes;
+    if ((m.first | m.last) == 0 && t0 + RUN <= T_) {
 #pragma unroll
-    for (int i = 0; i < RUN; ++i) {
-      // (a sequence's first token: a = 0, and whatever h was is dropped)
-      h = (m.first >> i & 1) ? u[i] : f2_fma(a[i], h, u[i]);
-      if (t0 + i < T_) put_out<T, AL>(y, ch, h);
-      y += C;
-      if ((m.last >> i & 1) && p.final_state != nullptr)
-        ch.put(p.final_state, seq_of(p, t0 + i), C, h);
+      for (int i = 0; i < RUN; ++i) {
+        h = f2_fma(a[i], h, u[i]);
+        put_out<T, AL>(y, off, ch, h);
+        off += row_bytes;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < RUN; ++i) {
+        const int s = m.seq_of(i);
+        // (a sequence's first token: a = 0, and whatever h was is dropped)
+        h = (m.first >> i & 1) ? u[i] : f2_fma(a[i], h, u[i]);
+        if (t0 + i < T_) put_out<T, AL>(y, off, ch, h);
+        off += row_bytes;
+        if ((m.last >> i & 1) && p.final_state != nullptr) ch.put(p.final_state, s, C, h);
+      }
     }
   }
+  if (n_steps > 0) sm100::cluster_sync();  // (a CTA that gave up waiting may still be sent to)
   empty_sequences<AL>(p, p.initial_state, p.final_state, ch, rank * kWarps + warp,
                       n_cta * kWarps, blockIdx.y == 0);
 }
@@ -437,18 +521,23 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(const GlrArgs p) {
   extern __shared__ __align__(128) char smem[];
   Run(*fwd_runs)[32] = reinterpret_cast<Run(*)[32]>(smem);
   Run(*rev_runs)[32] = fwd_runs + kWarps;
-  Run(*tiles)[32] = rev_runs + kWarps;
-  char* stages = reinterpret_cast<char*>(tiles + 2 * kMaxCluster);
+  Exchange ex;
+  ex.tiles = rev_runs + kWarps;
+  ex.bar = reinterpret_cast<uint64_t*>(ex.tiles + 2 * kMaxCluster);
+  char* stages = reinterpret_cast<char*>(ex.bar) + 128;
   const uint32_t stages_u = sm100::smem_u32(stages);
   constexpr int kStage = N * P::bytes(ROWS);
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n_cta = (int)gridDim.x, rank = (int)blockIdx.x;
+  ex.n_cta = n_cta;
+  ex.rank = rank;
   const int C = p.C, cb = (int)blockIdx.y * kChan;
   const Chan<AL> ch(cb, lane, C);
   const int64_t T_ = p.total_T;
   const int64_t n_tiles = (T_ + ROWS - 1) / ROWS;
   const int64_t n_steps = (n_tiles + n_cta - 1) / n_cta;
+  const uint32_t row_bytes = (uint32_t)C * (uint32_t)sizeof(T);
   const char* src[N];
   src[0] = static_cast<const char*>(p.x);
   src[1] = static_cast<const char*>(p.log_alpha);
@@ -464,32 +553,34 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(const GlrArgs p) {
   };
 
   f2 carry = both(0.f);  // e of the token behind this step's last tile
+  Marks<RUN, true> m;
   if (n_steps > 0) {
     load(0);
+    ex.init();
     sm100::cluster_sync();
   }
   for (int64_t step = 0; step < n_steps; ++step) {
     const int64_t tile = n_tiles - 1 - (step * n_cta + rank);
     const int64_t t0 = tile * ROWS + warp * RUN;
-    const Marks m = marks_of<RUN>(p.cu_seqlens, p.n_seq, T_, t0, lane);
+    m.look(p, t0, lane);
     f2 h = both(0.f);
     if (warp == 1 && tile >= 0) h = ch.get(p.checkpoints, tile, C);
     sm100::cp_async_wait_all();
     __syncthreads();  // this step's inputs have landed; the other stage is read
     load(step + 1);
     const char* st = stages + (int)(step & 1) * kStage + warp * RUN * P::kPitch;
-    const uint32_t inc = (uint32_t)C * (uint32_t)sizeof(T);
-    const uint32_t rem0 = ((uint32_t)t0 * (uint32_t)C + (uint32_t)cb) * (uint32_t)sizeof(T);
+    const uint32_t rem = (uint32_t)t0 * row_bytes + (uint32_t)cb * (uint32_t)sizeof(T);
     auto in = [&](int k, int i) {  // tensor k at token i of the run
       return P::get(st + k * P::bytes(ROWS) + i * P::kPitch,
-                    AL ? 0 : (int)((rem0 + (uint32_t)i * inc) & 15u), lane);
+                    AL ? 0 : (int)((rem + (uint32_t)i * row_bytes) & 15u), lane);
     };
     // dh_T joins its sequence's last dy; h_0 enters where a sequence begins
-    auto dy_at = [&](int i) {
-      f2 d = in(2, i);
-      if ((m.last >> i & 1) && p.d_final_state != nullptr)
-        d = f2_add(d, ch.get(p.d_final_state, seq_of(p, t0 + i), C));
-      return d;
+    // (i: a constant once the loops are unrolled)
+    auto dy_last = [&](int i, int s) {
+      const f2 d = in(2, i);
+      return (m.last >> i & 1) && p.d_final_state != nullptr
+                 ? f2_add(d, ch.get(p.d_final_state, s, C))
+                 : d;
     };
     f2 a[RUN], u[RUN], om[RUN];  // om: 1 - a
     Run fr, rr;
@@ -499,32 +590,38 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(const GlrArgs p) {
     for (int i = 0; i < RUN; ++i) {
       decay2<GATE>(in(1, i), a[i], om[i]);
       u[i] = gated<GATE>(in(0, i), GATE == kGateBeta ? in(N - 1, i) : 0, om[i]);
-      if (m.first >> i & 1) {
-        fr.h = ch.get(p.initial_state, seq_of(p, t0 + i), C);
-        fr.A = both(0.f);
-      }
       fr.A = f2_mul(fr.A, a[i]);
       fr.h = f2_fma(a[i], fr.h, u[i]);
     }
+    rr.A = fr.A;
+    const bool inside = (m.first | m.last) == 0;
+    if (inside) {
 #pragma unroll
-    for (int i = RUN - 1; i >= 0; --i) {
-      if (m.last >> i & 1) rr.A = rr.h = both(0.f);
-      rr.A = f2_mul(rr.A, a[i]);
-      rr.h = f2_mul(a[i], f2_add(dy_at(i), rr.h));
+      for (int i = RUN - 1; i >= 0; --i) rr.h = f2_mul(a[i], f2_add(in(2, i), rr.h));
+    } else {
+      // again, cut where sequences begin and end (a run with a first token
+      // forgets what was before it whatever its a are)
+      fr.h = both(0.f);
+#pragma unroll
+      for (int i = 0; i < RUN; ++i) {
+        const int s = m.seq_of(i);
+        if (m.first >> i & 1) fr.h = ch.get(p.initial_state, s, C);
+        fr.h = f2_fma(a[i], fr.h, u[i]);
+      }
+#pragma unroll
+      for (int i = RUN - 1; i >= 0; --i) {
+        const int s = m.seq_of(i);
+        if (m.last >> i & 1) rr.h = both(0.f);
+        rr.h = f2_mul(a[i], f2_add(dy_last(i, s), rr.h));
+      }
+      if (m.first != 0) fr.A = both(0.f);
+      if (m.last != 0) rr.A = both(0.f);
     }
-    // (a run with a first token forgets what was before it even where a is
-    // infinite or NaN)
-    if (m.first != 0) fr.A = both(0.f);
-    if (m.last != 0) rr.A = both(0.f);
     fwd_runs[warp][lane] = fr;
     rev_runs[warp][lane] = rr;
     __syncthreads();
-    Run(*tr)[32] = tiles + (int)(step & 1) * kMaxCluster;  // (two buffers: see the forward)
     if (warp == 0) {
-      const Run all = fold_tile(rev_runs, lane, true);
-      const uint32_t mine = sm100::smem_u32(&tr[rank][lane]);
-      for (int r = 0; r < n_cta; ++r)
-        st_cluster_run(sm100::mapa_shared(mine, (uint32_t)r), all);
+      ex.send(step, lane, fold_tile(rev_runs, lane, true));
     } else if (warp == 1) {  // the state before each run, left in its h
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
@@ -533,42 +630,58 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(const GlrArgs p) {
         h = through(r, h);
       }
     }
-    sm100::cluster_sync();
-    f2 e = carry;
-    for (int r = 0; r < n_cta; ++r) {
-      if (r == rank) e = carry;
-      carry = through(tr[r][lane], carry);
-    }
+    __syncthreads();  // both folds are in shared memory
+    f2 e = ex.receive(step, lane, carry, p.err);
     e = through(rev_runs[warp][lane], e);
     h = fwd_runs[warp][lane].h;
     // h_{t-1} of every token (into u), then the gradients from the last token back
-#pragma unroll
-    for (int i = 0; i < RUN; ++i) {
-      if (m.first >> i & 1) h = ch.get(p.initial_state, seq_of(p, t0 + i), C);
-      const f2 before = h;
-      h = f2_fma(a[i], h, u[i]);
-      u[i] = before;
-    }
-    const int64_t o0 = t0 * C;
-#pragma unroll
-    for (int i = RUN - 1; i >= 0; --i) {
+    char* dx = static_cast<char*>(p.dx) + tile * ROWS * row_bytes;
+    char* dl = static_cast<char*>(p.dlog_alpha) + tile * ROWS * row_bytes;
+    char* db = static_cast<char*>(p.dbeta) + tile * ROWS * row_bytes;
+    auto out = [&](int i, f2 dh) {  // token i's gradients
+      const uint32_t off = (uint32_t)(warp * RUN + i) * row_bytes;
       const f2 x = in(0, i);
-      f2 dh = dy_at(i);
-      if (!(m.last >> i & 1)) dh = f2_add(dh, e);
-      e = f2_mul(a[i], dh);
-      if (t0 + i >= 0 && t0 + i < T_) {
-        const int64_t o = o0 + (int64_t)i * C;
-        put_out<T, AL>(static_cast<T*>(p.dx) + o, ch,
-                       gated<GATE>(dh, GATE == kGateBeta ? in(N - 1, i) : 0, om[i]));
-        f2 hb = u[i];
-        if (GATE == kGateComp) hb = f2_fma(x, both(-1.f), hb);
-        put_out<T, AL>(static_cast<T*>(p.dlog_alpha) + o, ch, f2_mul(hb, e));
-        if (GATE == kGateBeta) put_out<T, AL>(static_cast<T*>(p.dbeta) + o, ch, f2_mul(x, dh));
+      put_out<T, AL>(dx, off, ch, gated<GATE>(dh, GATE == kGateBeta ? in(N - 1, i) : 0, om[i]));
+      f2 hb = u[i];
+      if (GATE == kGateComp) hb = f2_fma(x, both(-1.f), hb);
+      put_out<T, AL>(dl, off, ch, f2_mul(hb, e));
+      if (GATE == kGateBeta) put_out<T, AL>(db, off, ch, f2_mul(x, dh));
+    };
+    if (inside && t0 >= 0 && t0 + RUN <= T_) {
+#pragma unroll
+      for (int i = 0; i < RUN; ++i) {
+        const f2 before = h;
+        h = f2_fma(a[i], h, u[i]);
+        u[i] = before;
+      }
+#pragma unroll
+      for (int i = RUN - 1; i >= 0; --i) {
+        const f2 dh = f2_add(in(2, i), e);
+        e = f2_mul(a[i], dh);
+        out(i, dh);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < RUN; ++i) {
+        const int s = m.seq_of(i);
+        if (m.first >> i & 1) h = ch.get(p.initial_state, s, C);
+        const f2 before = h;
+        h = f2_fma(a[i], h, u[i]);
+        u[i] = before;
+      }
+#pragma unroll
+      for (int i = RUN - 1; i >= 0; --i) {
+        const int s = m.seq_of(i);
+        f2 dh = dy_last(i, s);
+        if (!(m.last >> i & 1)) dh = f2_add(dh, e);
+        e = f2_mul(a[i], dh);
+        if (t0 + i >= 0 && t0 + i < T_) out(i, dh);
         if ((m.first >> i & 1) && p.d_initial_state != nullptr)
-          ch.put(p.d_initial_state, seq_of(p, t0 + i), C, e);
+          ch.put(p.d_initial_state, s, C, e);
       }
     }
   }
+  if (n_steps > 0) sm100::cluster_sync();
   empty_sequences<AL>(p, p.d_final_state, p.d_initial_state, ch, rank * kWarps + warp,
                       n_cta * kWarps, blockIdx.y == 0);
 }
