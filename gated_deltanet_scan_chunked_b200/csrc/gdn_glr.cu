@@ -9,8 +9,8 @@
 // a_t h_0 to its input, so packed sequences need no other care.
 //
 // Layout.  A CTA of 8 warps owns a tile of 8 kRun tokens x 64 channels: warp w
-// has the run of kRun tokens from w kRun on, a lane two channels (which the
-// packed fp32 instructions take together).  The carry along the tokens passes
+// has the run of kRun tokens from w kRun on, a lane two channels (one 4-byte
+// word of bf16).  The carry along the tokens passes
 // three levels, each in a fixed order (results do not depend on timing): a
 // thread's run in registers, the 8 runs of a tile by one warp through shared
 // memory, and the CTAs of a cluster, which hold consecutive tiles of the same
@@ -18,12 +18,14 @@
 // tokens in steps of (cluster size) tiles, the carry kept in registers;
 // nothing is exchanged through global memory, so there is no workspace and no
 // flag to wait on.  Every input is read once and every output written once.
-// Inputs come by 16-byte asynchronous copies into two shared-memory stages,
-// so that the next steps' loads are in flight while this one is folded.
-//
-// Rows of C elements that are not a multiple of 16 bytes begin anywhere: then
-// a row's piece is copied from the 16-byte boundary below it, one copy more,
-// and read from its remainder on (kAl = false).
+// Inputs come into two shared-memory stages, so that the next steps' loads are
+// in flight while this one is folded: by TMA where rows of C elements are a
+// multiple of 16 bytes (AL), one box of 64 channels a tensor.  Other rows begin
+// anywhere: a row's piece is then copied from the 16-byte boundary below it
+// by 16-byte asynchronous copies, one more than it needs, and read from its
+// remainder on.
+#include <cuda.h>
+
 #include <atomic>
 
 #include "gdn_common.cuh"
@@ -33,49 +35,57 @@
 namespace gdn {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 8;  // (>= kMaxCluster)
 constexpr int kThreads = 32 * kWarps;
 constexpr int kChan = 64;  // channels of a CTA
 constexpr int kMaxCluster = 8;
+constexpr uint32_t kWait = 1u << 24;  // polls of a bounded wait
 
 enum : int { kGateNone = GDN_GLR_GATE_NONE, kGateBeta = GDN_GLR_GATE_BETA,
              kGateComp = GDN_GLR_GATE_COMPLEMENT };
 
-using f2 = uint64_t;  // two channels of a lane, fp32
+using f2 = float2;  // two channels of a lane
+
+__device__ __forceinline__ f2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  return make_float2(__fmul_rn(a.x, b.x), __fmul_rn(a.y, b.y));
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  return make_float2(__fmaf_rn(a.x, b.x, c.x), __fmaf_rn(a.y, b.y, c.y));
+}
 
 // a = exp(l) and 1 - a.  Channels that remember a thousand tokens have a
 // within 1e-3 of 1, where an error of exp in one direction adds up over all of
-// them.  So near 0, exp(l) - 1 is summed from its Taylor series (the first
-// term left out, l^7/5040, is below 2^-24 of the sum for |l| < 1/4) and a is
-// 1 + that, rounded once; further out the hardware 2^x, good to 2^-22,
-// serves, since such a channel forgets within a few tokens.
-__device__ __forceinline__ f2 both(float v) { return f2_pack(v, v); }
+// them.  So for |l| < 1/4, a = 1 + l q(l), rounded once, with
+//   q = 1 + l/2 + l^2 (r0 + r1 l + r2 l^2),
+// the first terms exact and the r fitted to (e^l - 1 - l - l^2/2) / l^3 so
+// that the largest relative error of l q over the range is least: 1.8e-7, at
+// its ends, falling with l^2 towards 0.  Further out the hardware 2^x, good to
+// 2^-22, serves, since such a channel forgets within a few tokens.
+template <int GATE>
+__device__ __forceinline__ void decay1(float l, float& a, float& one_minus_a) {
+  float q = __fmaf_rn(l, 0.008352220989763737f, 0.04174217954277992f);
+  q = __fmaf_rn(l, q, 0.16666626930236816f);
+  q = __fmaf_rn(l, q, 0.5f);
+  q = __fmaf_rn(l, q, 1.f);
+  const float e = sm100::ex2_approx(__fmul_rn(l, 1.4426950408889634f));
+  const bool near = fabsf(l) < 0.25f;
+  a = near ? __fmaf_rn(l, q, 1.f) : e;
+  if (GATE == kGateComp) one_minus_a = near ? __fmul_rn(-l, q) : __fadd_rn(1.f, -e);
+}
 template <int GATE>
 __device__ __forceinline__ void decay2(f2 l, f2& a, f2& one_minus_a) {
-  f2 p = f2_fma(l, both(1.f / 720.f), both(1.f / 120.f));
-  p = f2_fma(l, p, both(1.f / 24.f));
-  p = f2_fma(l, p, both(1.f / 6.f));
-  p = f2_fma(l, p, both(0.5f));
-  p = f2_fma(l, p, both(1.f));
-  p = f2_mul(l, p);
-  float l0, l1, z0, z1, n0, n1;
-  f2_unpack(l, l0, l1);
-  f2_unpack(f2_mul(l, both(1.4426950408889634f)), z0, z1);
-  f2_unpack(f2_add(p, both(1.f)), n0, n1);
-  const float e0 = sm100::ex2_approx(z0), e1 = sm100::ex2_approx(z1);
-  const bool s0 = fabsf(l0) < 0.25f, s1 = fabsf(l1) < 0.25f;
-  a = f2_pack(s0 ? n0 : e0, s1 ? n1 : e1);
-  if (GATE == kGateComp) {
-    float p0, p1;
-    f2_unpack(p, p0, p1);
-    one_minus_a = f2_pack(s0 ? -p0 : __fadd_rn(1.f, -e0), s1 ? -p1 : __fadd_rn(1.f, -e1));
-  }
+  decay1<GATE>(l.x, a.x, one_minus_a.x);
+  decay1<GATE>(l.y, a.y, one_minus_a.y);
 }
 
 // The input b x of two channels.
 template <int GATE>
 __device__ __forceinline__ f2 gated(f2 x, f2 beta, f2 one_minus_a) {
-  return GATE == kGateNone ? x : f2_mul(GATE == kGateBeta ? beta : one_minus_a, x);
+  return GATE == kGateNone ? x : mul2(GATE == kGateBeta ? beta : one_minus_a, x);
 }
 
 // Last sequence s with cu[s] <= t (so that empty sequences are passed over).
@@ -136,11 +146,8 @@ struct __align__(16) Run {
 // h behind a run that is entered with h.  A run whose A is 0 forgets what was
 // before it, even an infinity or NaN: those belong to another sequence.
 __device__ __forceinline__ f2 through(const Run& r, f2 h) {
-  float a0, a1, r0, r1, n0, n1;
-  f2_unpack(r.A, a0, a1);
-  f2_unpack(r.h, r0, r1);
-  f2_unpack(f2_fma(r.A, h, r.h), n0, n1);
-  return f2_pack(a0 == 0.f ? r0 : n0, a1 == 0.f ? r1 : n1);
+  const f2 n = fma2(r.A, h, r.h);
+  return make_float2(r.A.x == 0.f ? r.h.x : n.x, r.A.y == 0.f ? r.h.y : n.y);
 }
 
 // A lane's two channels: neighbours where rows are aligned, else 32 apart.
@@ -156,14 +163,12 @@ struct Chan {
   }
   // rows of a [.., C] fp32 array (nullptr: zeros)
   __device__ __forceinline__ f2 get(const float* p, int64_t row, int C) const {
-    return f2_pack(p != nullptr && ok0 ? p[row * C + c0] : 0.f,
+    return make_float2(p != nullptr && ok0 ? p[row * C + c0] : 0.f,
                    p != nullptr && ok1 ? p[row * C + c1] : 0.f);
   }
   __device__ __forceinline__ void put(float* p, int64_t row, int C, f2 v) const {
-    float v0, v1;
-    f2_unpack(v, v0, v1);
-    if (ok0) p[row * C + c0] = v0;
-    if (ok1) p[row * C + c1] = v1;
+    if (ok0) p[row * C + c0] = v.x;
+    if (ok1) p[row * C + c1] = v.y;
   }
 };
 
@@ -185,10 +190,10 @@ struct Piece {
         lo = (uint32_t) * reinterpret_cast<const unsigned short*>(row + rem + 2 * lane) << 16;
         hi = (uint32_t) * reinterpret_cast<const unsigned short*>(row + rem + 2 * lane + 64) << 16;
       }
-      return f2_pack(__uint_as_float(lo), __uint_as_float(hi));
+      return make_float2(__uint_as_float(lo), __uint_as_float(hi));
     }
     if (AL) return *reinterpret_cast<const f2*>(row + 8 * lane);
-    return f2_pack(*reinterpret_cast<const float*>(row + rem + 4 * lane),
+    return make_float2(*reinterpret_cast<const float*>(row + rem + 4 * lane),
                    *reinterpret_cast<const float*>(row + rem + 4 * lane + 128));
   }
 };
@@ -197,19 +202,17 @@ struct Piece {
 // CTA, `off` the bytes from it to the row's channel 0.
 template <typename T, bool AL>
 __device__ __forceinline__ void put_out(char* base, uint32_t off, const Chan<AL>& ch, f2 v) {
-  float v0, v1;
-  f2_unpack(v, v0, v1);
   T* q = reinterpret_cast<T*>(base + (off + (uint32_t)ch.c0 * (uint32_t)sizeof(T)));
   if (AL) {
     if (ch.ok0) {
       if (sizeof(T) == 2)
-        *reinterpret_cast<uint32_t*>(q) = sm100::pack_bf16(v0, v1);
+        *reinterpret_cast<uint32_t*>(q) = sm100::pack_bf16(v.x, v.y);
       else
         *reinterpret_cast<f2*>(q) = v;
     }
   } else {
-    if (ch.ok0) Elem<T>::store(q, v0);
-    if (ch.ok1) Elem<T>::store(q + 32, v1);
+    if (ch.ok0) Elem<T>::store(q, v.x);
+    if (ch.ok1) Elem<T>::store(q + 32, v.y);
   }
 }
 
@@ -219,80 +222,101 @@ __device__ __forceinline__ void copy16(uint32_t dst, const char* src, int n) {
                : "memory");
 }
 
-// Copies the tile's rows [t0, t0 + ROWS) of N tensors into a stage.  Tokens
-// outside [0, T) become zeros: a = exp(0) = 1 and x = 0 leave a state as it is.
+// TMA maps of the inputs (AL only): [total_T, C] with boxes of kChan channels x
+// a tile's tokens.
+struct ScanMaps {
+  CUtensorMap m[4];
+};
+
+// Two stages of N input tensors' tiles of ROWS tokens.  Tokens outside [0, T)
+// become zeros: a = exp(0) = 1 and x = 0 leave a state as it is.  Loads are
+// numbered by step; step s goes to stage s & 1.
 template <typename T, bool AL, int ROWS, int N>
-__device__ __forceinline__ void load_stage(uint32_t stage, const char* const (&src)[N], int64_t t0,
-                                           int64_t total_T, int C, int cb) {
+struct Stages {
   using P = Piece<T, AL>;
-  const uint32_t row_bytes = (uint32_t)C * (uint32_t)sizeof(T);
-  if constexpr (AL) {
-    // a thread has one 16-byte column of every (kThreads / kCopies)th row
-    constexpr int kStep = kThreads / P::kCopies;
-    static_assert(kThreads % P::kCopies == 0 && ROWS % kStep == 0, "whole rounds");
-    const int q = (int)threadIdx.x % P::kCopies, r0 = (int)threadIdx.x / P::kCopies;
-    const uint32_t col = (uint32_t)cb * (uint32_t)sizeof(T) + 16u * q;
-    const bool ok = col < row_bytes;
-    uint32_t off = (uint32_t)r0 * row_bytes + col;
-    uint32_t dst = stage + r0 * P::kPitch + 16 * q;
-    const char* base[N];
-    const int64_t at = (t0 < 0 ? 0 : t0) * (int64_t)row_bytes;
-#pragma unroll
-    for (int k = 0; k < N; ++k) base[k] = src[k] + at;
-    const bool whole = t0 >= 0 && t0 + ROWS <= total_T;
-#pragma unroll
-    for (int i = 0; i < ROWS / kStep; ++i) {
-      const int64_t t = t0 + r0 + i * kStep;
-      const bool in = ok && (whole || (t >= 0 && t < total_T));
-#pragma unroll
-      for (int k = 0; k < N; ++k)
-        copy16(dst + k * P::bytes(ROWS), base[k] + (in ? off : 0u), in ? 16 : 0);
-      off += kStep * row_bytes;
-      dst += kStep * P::kPitch;
-    }
-  } else {
-    const int64_t all = total_T * (int64_t)row_bytes;
-    for (int i = threadIdx.x; i < ROWS * P::kCopies; i += kThreads) {
-      const int r = i / P::kCopies, q = i % P::kCopies;
-      const int64_t t = t0 + r;
-      int64_t off = ((t * (int64_t)row_bytes + (int64_t)cb * (int)sizeof(T)) & ~(int64_t)15) +
-                    16 * q;
-      int n = 0;
-      if (t >= 0 && t < total_T) n = all - off >= 16 ? 16 : all - off > 0 ? (int)(all - off) : 0;
-      if (n == 0) off = 0;
-#pragma unroll
-      for (int k = 0; k < N; ++k)
-        copy16(stage + k * P::bytes(ROWS) + r * P::kPitch + 16 * q, src[k] + off, n);
+  static constexpr int kTensor = P::bytes(ROWS), kStage = N * kTensor;
+  char* at;
+  uint64_t* full;  // [2] (AL)
+
+  // (by every thread, before the block's first barrier)
+  __device__ __forceinline__ void init() {
+    if (AL && threadIdx.x == 0) {
+      sm100::mbar_init(&full[0], 1);
+      sm100::mbar_init(&full[1], 1);
+      sm100::fence_mbar_init();
     }
   }
-}
+  // (by every thread, after a barrier behind the last reads of the stage)
+  __device__ __forceinline__ void load(int64_t step, bool any, const char* const (&src)[N],
+                                       const ScanMaps& maps, int64_t t0, int64_t total_T, int C,
+                                       int cb) {
+    const uint32_t stage = sm100::smem_u32(at) + (uint32_t)(step & 1) * kStage;
+    if constexpr (AL) {
+      if (any && threadIdx.x == 0) {
+        uint64_t* bar = &full[step & 1];
+        sm100::mbar_arrive_expect_tx(bar, kStage);
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+          sm100::tma_load_2d(stage + k * kTensor, &maps.m[k], cb, (int)t0, bar);
+      }
+    } else {
+      if (any) {
+        const int64_t row_bytes = (int64_t)C * (int)sizeof(T), all = total_T * row_bytes;
+        for (int i = threadIdx.x; i < ROWS * P::kCopies; i += kThreads) {
+          const int r = i / P::kCopies, q = i % P::kCopies;
+          const int64_t t = t0 + r;
+          int64_t off = ((t * row_bytes + (int64_t)cb * (int)sizeof(T)) & ~(int64_t)15) + 16 * q;
+          int n = 0;
+          if (t >= 0 && t < total_T)
+            n = all - off >= 16 ? 16 : all - off > 0 ? (int)(all - off) : 0;
+          if (n == 0) off = 0;
+#pragma unroll
+          for (int k = 0; k < N; ++k)
+            copy16(stage + k * kTensor + r * P::kPitch + 16 * q, src[k] + off, n);
+        }
+      }
+      sm100::cp_async_commit();
+    }
+  }
+  // (by every thread) Waits for the step's inputs; AHEAD: a later step's loads
+  // are under way too.  ok: no bounded wait ran out yet (then none is made).
+  template <bool AHEAD>
+  __device__ __forceinline__ bool wait(int64_t step, bool ok) {
+    if constexpr (AL) {
+      return ok && sm100::mbar_wait(&full[step & 1], (uint32_t)(step >> 1) & 1u, kWait);
+    } else {
+      if (AHEAD) sm100::cp_async_wait_group1(); else sm100::cp_async_wait_all();
+      __syncthreads();
+      return ok;
+    }
+  }
+};
 
 // A tile's run to one CTA of the cluster (its address there), counted on that
 // CTA's barrier.
 __device__ __forceinline__ void send_run(uint32_t addr, uint32_t bar, const Run& r) {
   asm volatile(
-      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];" ::
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::
           "r"(addr),
-      "l"(r.A), "l"(r.h), "r"(bar)
+      "f"(r.A.x), "f"(r.A.y), "f"(r.h.x), "f"(r.h.y), "r"(bar)
       : "memory");
 }
 
-// One warp: turns the runs of a tile (in[w], in the order `first, first +
-// dir, ...`) into what lies before each (in place), and gives the whole.
-__device__ __forceinline__ Run fold_tile(Run (*runs)[32], int lane, bool backwards) {
-  Run r[kWarps];
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) r[w] = runs[backwards ? kWarps - 1 - w : w][lane];
-  Run all;
+// The runs of a tile's warps, in order or backwards: what lies before this
+// warp's run, and the whole.
+template <bool BACK>
+__device__ __forceinline__ void fold_tile(const Run (*runs)[32], int lane, int warp, Run& before,
+                                          Run& all) {
   all.A = both(1.f);
   all.h = both(0.f);
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    runs[backwards ? kWarps - 1 - w : w][lane] = all;
-    all.h = through(r[w], all.h);
-    all.A = f2_mul(all.A, r[w].A);
+  for (int k = 0; k < kWarps; ++k) {
+    const int w = BACK ? kWarps - 1 - k : k;
+    if (w == warp) before = all;
+    const Run r = runs[w][lane];
+    all.h = through(r, all.h);
+    all.A = mul2(all.A, r.A);
   }
-  return all;
 }
 
 // The cluster's exchange of tile runs.  In every step each CTA sends its tile's
@@ -300,7 +324,6 @@ __device__ __forceinline__ Run fold_tile(Run (*runs)[32], int lane, bool backwar
 // stores carry the signal, so no fence waits for the outputs of the step
 // before.  Two buffers alternate: a CTA sends step s + 2 only after it has
 // everyone's step s + 1, which each sends after its reads of step s.
-constexpr uint32_t kWait = 1u << 24;
 struct Exchange {
   Run (*tiles)[32];  // [2][kMaxCluster]
   uint64_t* bar;     // [2]
@@ -315,25 +338,22 @@ struct Exchange {
       sm100::fence_mbar_init();
     }
   }
-  // (by one warp)
-  __device__ __forceinline__ void send(int64_t step, int lane, const Run& all) {
+  // (by every warp: warp w sends to CTA w; kMaxCluster warps serve the largest cluster)
+  __device__ __forceinline__ void send(int64_t step, int lane, int warp, const Run& all) {
     const int b = (int)(step & 1);
-    if (lane == 0)
+    if (threadIdx.x == 0)
       sm100::mbar_arrive_expect_tx(&bar[b], (uint32_t)n_cta * 32u * (uint32_t)sizeof(Run));
-    __syncwarp();
-    const uint32_t at = sm100::smem_u32(&tiles[b * kMaxCluster + rank][lane]);
-    const uint32_t on = sm100::smem_u32(&bar[b]);
-    for (int r = 0; r < n_cta; ++r)
-      send_run(sm100::mapa_shared(at, (uint32_t)r), sm100::mapa_shared(on, (uint32_t)r), all);
+    if (warp < n_cta)
+      send_run(sm100::mapa_shared(sm100::smem_u32(&tiles[b * kMaxCluster + rank][lane]),
+                                  (uint32_t)warp),
+               sm100::mapa_shared(sm100::smem_u32(&bar[b]), (uint32_t)warp), all);
   }
   // Waits for the step's runs; h: the carry before this CTA's tile; carry
   // moves on past the whole step.
-  __device__ __forceinline__ f2 receive(int64_t step, int lane, f2& carry, int* err) {
+  __device__ __forceinline__ f2 receive(int64_t step, int lane, f2& carry) {
     const int b = (int)(step & 1);
-    if (ok && !sm100::mbar_wait_cluster(&bar[b], (uint32_t)(step >> 1) & 1u, kWait)) {
-      ok = false;  // never waits again; every later step still sends
-      if (lane == 0) atomicOr(err, kErrTimeout);
-    }
+    // (a thread that gave up never waits again, but still sends every step)
+    ok = ok && sm100::mbar_wait_cluster(&bar[b], (uint32_t)(step >> 1) & 1u, kWait);
     f2 h = carry;
 #pragma unroll 4
     for (int r = 0; r < n_cta; ++r) {
@@ -367,11 +387,11 @@ __device__ __forceinline__ void empty_sequences(const GlrArgs& p, const float* i
   }
 }
 
-// Shared memory of a CTA: the runs of a tile (RUNS sets), the cluster's tiles
-// (two buffers), two stages of inputs.
+// Shared memory of a CTA: the runs of a tile (`run_sets` arrays, two buffers
+// each), the cluster's tiles (two buffers), the barriers, two stages.
 template <typename T, bool AL>
 constexpr int scan_smem(int run, int tensors, int run_sets) {
-  return run_sets * kWarps * 32 * (int)sizeof(Run) + 2 * kMaxCluster * 32 * (int)sizeof(Run) +
+  return 2 * run_sets * kWarps * 32 * (int)sizeof(Run) + 2 * kMaxCluster * 32 * (int)sizeof(Run) +
          128 + 2 * tensors * Piece<T, AL>::bytes(kWarps * run);
 }
 
@@ -382,19 +402,20 @@ constexpr int kBwdRun = 8;
 static_assert(kBwdRun * kWarps == kGlrTile, "the backward starts each tile from a checkpoint");
 
 template <typename T, int GATE, bool AL>
-__global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(const GlrArgs p) {
+__global__ void __launch_bounds__(kThreads, 2)
+    glr_fwd_kernel(const GlrArgs p, const __grid_constant__ ScanMaps maps) {
   constexpr int RUN = fwd_run<T, AL>();
   constexpr int ROWS = kWarps * RUN;
   constexpr int N = GATE == kGateBeta ? 3 : 2;
   using P = Piece<T, AL>;
   extern __shared__ __align__(128) char smem[];
-  Run(*runs)[32] = reinterpret_cast<Run(*)[32]>(smem);
+  Run(*run_buf)[32] = reinterpret_cast<Run(*)[32]>(smem);  // [2][kWarps]
   Exchange ex;
-  ex.tiles = runs + kWarps;
+  ex.tiles = run_buf + 2 * kWarps;
   ex.bar = reinterpret_cast<uint64_t*>(ex.tiles + 2 * kMaxCluster);
-  char* stages = reinterpret_cast<char*>(ex.bar) + 128;
-  const uint32_t stages_u = sm100::smem_u32(stages);
-  constexpr int kStage = N * P::bytes(ROWS);
+  Stages<T, AL, ROWS, N> in;
+  in.full = ex.bar + 2;
+  in.at = reinterpret_cast<char*>(ex.bar) + 128;
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n_cta = (int)gridDim.x, rank = (int)blockIdx.x;  // one cluster along x
@@ -411,29 +432,26 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(const GlrArgs p) {
   src[1] = static_cast<const char*>(p.log_alpha);
   if (N == 3) src[N - 1] = static_cast<const char*>(p.beta);
   auto load = [&](int64_t step) {
-    if (step < n_steps)
-      load_stage<T, AL, ROWS, N>(stages_u + (int)(step & 1) * kStage, src,
-                                 (step * n_cta + rank) * ROWS, T_, C, cb);
-    sm100::cp_async_commit();
+    in.load(step, step < n_steps, src, maps, (step * n_cta + rank) * ROWS, T_, C, cb);
   };
 
   f2 carry = both(0.f);  // state before this step's first tile
   Marks<RUN, false> m;
   if (n_steps > 0) {
-    load(0);
-    load(1);
+    in.init();
     ex.init();
     sm100::cluster_sync();  // every CTA runs, its barriers set, before any sends
+    load(0);
+    load(1);
   }
   for (int64_t step = 0; step < n_steps; ++step) {
     const int64_t tile0 = (step * n_cta + rank) * ROWS, t0 = tile0 + warp * RUN;
     m.look(p, t0, lane);
-    sm100::cp_async_wait_group1();
-    __syncthreads();
+    ex.ok = in.template wait<true>(step, ex.ok);
     f2 a[RUN], u[RUN];
     Run run;
     {
-      const char* st = stages + (int)(step & 1) * kStage + warp * RUN * P::kPitch;
+      const char* st = in.at + (int)(step & 1) * in.kStage + warp * RUN * P::kPitch;
       const uint32_t rem = (uint32_t)t0 * row_bytes + (uint32_t)cb * (uint32_t)sizeof(T);
       run.A = both(1.f);
       run.h = both(0.f);
@@ -442,13 +460,13 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(const GlrArgs p) {
         const char* row = st + i * P::kPitch;
         const int at = AL ? 0 : (int)((rem + (uint32_t)i * row_bytes) & 15u);
         const f2 x = P::get(row, at, lane);
-        const f2 l = P::get(row + P::bytes(ROWS), at, lane);
-        f2 b = 0, q = 0;
-        if (GATE == kGateBeta) b = P::get(row + 2 * P::bytes(ROWS), at, lane);
+        const f2 l = P::get(row + in.kTensor, at, lane);
+        f2 b = both(0.f), q = both(0.f);
+        if (GATE == kGateBeta) b = P::get(row + 2 * in.kTensor, at, lane);
         decay2<GATE>(l, a[i], q);
         u[i] = gated<GATE>(x, b, q);
-        run.A = f2_mul(run.A, a[i]);
-        run.h = f2_fma(a[i], run.h, u[i]);
+        run.A = mul2(run.A, a[i]);
+        run.h = fma2(a[i], run.h, u[i]);
       }
     }
     if (m.first != 0) {  // again, with the sequences' first tokens cut off
@@ -458,22 +476,25 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(const GlrArgs p) {
         if (m.first >> i & 1) {
           // (without a state, nothing: a_t = inf or NaN stays out of it)
           if (p.initial_state != nullptr)
-            u[i] = f2_fma(a[i], ch.get(p.initial_state, s, C), u[i]);
+            u[i] = fma2(a[i], ch.get(p.initial_state, s, C), u[i]);
           a[i] = both(0.f);
           run.h = u[i];
         } else {
-          run.h = i == 0 ? u[0] : f2_fma(a[i], run.h, u[i]);
+          run.h = i == 0 ? u[0] : fma2(a[i], run.h, u[i]);
         }
       }
       run.A = both(0.f);
     }
+    // (two buffers: a warp may still fold this step's runs when others write
+    // the next one's)
+    Run(*runs)[32] = run_buf + (int)(step & 1) * kWarps;
     runs[warp][lane] = run;
     __syncthreads();  // the runs are complete, and this stage is read
     load(step + 2);
-    if (warp == 0) ex.send(step, lane, fold_tile(runs, lane, false));
-    __syncthreads();  // the fold is in shared memory
-    f2 h = ex.receive(step, lane, carry, p.err);
-    h = through(runs[warp][lane], h);
+    Run before, all;
+    fold_tile<false>(runs, lane, warp, before, all);
+    ex.send(step, lane, warp, all);
+    f2 h = through(before, ex.receive(step, lane, carry));
     if (p.checkpoints != nullptr && warp % (kGlrTile / RUN) == 0 && t0 < T_)
       ch.put(p.checkpoints, t0 / kGlrTile, C, h);
     if (p.y == nullptr) continue;
@@ -482,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(const GlrArgs p) {
     if ((m.first | m.last) == 0 && t0 + RUN <= T_) {
 #pragma unroll
       for (int i = 0; i < RUN; ++i) {
-        h = f2_fma(a[i], h, u[i]);
+        h = fma2(a[i], h, u[i]);
         put_out<T, AL>(y, off, ch, h);
         off += row_bytes;
       }
@@ -491,13 +512,14 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(const GlrArgs p) {
       for (int i = 0; i < RUN; ++i) {
         const int s = m.seq_of(i);
         // (a sequence's first token: a = 0, and whatever h was is dropped)
-        h = (m.first >> i & 1) ? u[i] : f2_fma(a[i], h, u[i]);
+        h = (m.first >> i & 1) ? u[i] : fma2(a[i], h, u[i]);
         if (t0 + i < T_) put_out<T, AL>(y, off, ch, h);
         off += row_bytes;
         if ((m.last >> i & 1) && p.final_state != nullptr) ch.put(p.final_state, s, C, h);
       }
     }
   }
+  if (!ex.ok) atomicOr(p.err, kErrTimeout);
   if (n_steps > 0) sm100::cluster_sync();  // (a CTA that gave up waiting may still be sent to)
   empty_sequences<AL>(p, p.initial_state, p.final_state, ch, rank * kWarps + warp,
                       n_cta * kWarps, blockIdx.y == 0);
@@ -513,20 +535,20 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(const GlrArgs p) {
 // from the tile's checkpoint (the state before it, from the forward), so the
 // forward carry needs the first two levels only.
 template <typename T, int GATE, bool AL>
-__global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(const GlrArgs p) {
+__global__ void __launch_bounds__(kThreads, 2)
+    glr_bwd_kernel(const GlrArgs p, const __grid_constant__ ScanMaps maps) {
   constexpr int RUN = kBwdRun;
   constexpr int ROWS = kWarps * RUN;
   constexpr int N = GATE == kGateBeta ? 4 : 3;  // x, log_alpha, dy, beta
   using P = Piece<T, AL>;
   extern __shared__ __align__(128) char smem[];
-  Run(*fwd_runs)[32] = reinterpret_cast<Run(*)[32]>(smem);
-  Run(*rev_runs)[32] = fwd_runs + kWarps;
+  Run(*run_buf)[32] = reinterpret_cast<Run(*)[32]>(smem);  // [2][forward, reverse][kWarps]
   Exchange ex;
-  ex.tiles = rev_runs + kWarps;
+  ex.tiles = run_buf + 4 * kWarps;
   ex.bar = reinterpret_cast<uint64_t*>(ex.tiles + 2 * kMaxCluster);
-  char* stages = reinterpret_cast<char*>(ex.bar) + 128;
-  const uint32_t stages_u = sm100::smem_u32(stages);
-  constexpr int kStage = N * P::bytes(ROWS);
+  Stages<T, AL, ROWS, N> stages;
+  stages.full = ex.bar + 2;
+  stages.at = reinterpret_cast<char*>(ex.bar) + 128;
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n_cta = (int)gridDim.x, rank = (int)blockIdx.x;
@@ -546,32 +568,29 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(const GlrArgs p) {
   // tiles in reverse: rank r of step s has tile n_tiles - 1 - (s n_cta + r),
   // negative (nothing to do, all neutral) behind the first tile
   auto load = [&](int64_t step) {
-    if (step < n_steps)
-      load_stage<T, AL, ROWS, N>(stages_u + (int)(step & 1) * kStage, src,
-                                 (n_tiles - 1 - (step * n_cta + rank)) * ROWS, T_, C, cb);
-    sm100::cp_async_commit();
+    stages.load(step, step < n_steps, src, maps, (n_tiles - 1 - (step * n_cta + rank)) * ROWS, T_,
+                C, cb);
   };
 
   f2 carry = both(0.f);  // e of the token behind this step's last tile
   Marks<RUN, true> m;
   if (n_steps > 0) {
-    load(0);
+    stages.init();
     ex.init();
     sm100::cluster_sync();
+    load(0);
   }
   for (int64_t step = 0; step < n_steps; ++step) {
     const int64_t tile = n_tiles - 1 - (step * n_cta + rank);
     const int64_t t0 = tile * ROWS + warp * RUN;
     m.look(p, t0, lane);
     f2 h = both(0.f);
-    if (warp == 1 && tile >= 0) h = ch.get(p.checkpoints, tile, C);
-    sm100::cp_async_wait_all();
-    __syncthreads();  // this step's inputs have landed; the other stage is read
-    load(step + 1);
-    const char* st = stages + (int)(step & 1) * kStage + warp * RUN * P::kPitch;
+    if (tile >= 0) h = ch.get(p.checkpoints, tile, C);
+    ex.ok = stages.template wait<false>(step, ex.ok);
+    const char* st = stages.at + (int)(step & 1) * stages.kStage + warp * RUN * P::kPitch;
     const uint32_t rem = (uint32_t)t0 * row_bytes + (uint32_t)cb * (uint32_t)sizeof(T);
     auto in = [&](int k, int i) {  // tensor k at token i of the run
-      return P::get(st + k * P::bytes(ROWS) + i * P::kPitch,
+      return P::get(st + k * stages.kTensor + i * P::kPitch,
                     AL ? 0 : (int)((rem + (uint32_t)i * row_bytes) & 15u), lane);
     };
     // dh_T joins its sequence's last dy; h_0 enters where a sequence begins
@@ -579,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(const GlrArgs p) {
     auto dy_last = [&](int i, int s) {
       const f2 d = in(2, i);
       return (m.last >> i & 1) && p.d_final_state != nullptr
-                 ? f2_add(d, ch.get(p.d_final_state, s, C))
+                 ? add2(d, ch.get(p.d_final_state, s, C))
                  : d;
     };
     f2 a[RUN], u[RUN], om[RUN];  // om: 1 - a
@@ -589,15 +608,15 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(const GlrArgs p) {
 #pragma unroll
     for (int i = 0; i < RUN; ++i) {
       decay2<GATE>(in(1, i), a[i], om[i]);
-      u[i] = gated<GATE>(in(0, i), GATE == kGateBeta ? in(N - 1, i) : 0, om[i]);
-      fr.A = f2_mul(fr.A, a[i]);
-      fr.h = f2_fma(a[i], fr.h, u[i]);
+      u[i] = gated<GATE>(in(0, i), GATE == kGateBeta ? in(N - 1, i) : both(0.f), om[i]);
+      fr.A = mul2(fr.A, a[i]);
+      fr.h = fma2(a[i], fr.h, u[i]);
     }
     rr.A = fr.A;
     const bool inside = (m.first | m.last) == 0;
     if (inside) {
 #pragma unroll
-      for (int i = RUN - 1; i >= 0; --i) rr.h = f2_mul(a[i], f2_add(in(2, i), rr.h));
+      for (int i = RUN - 1; i >= 0; --i) rr.h = mul2(a[i], add2(in(2, i), rr.h));
     } else {
       // again, cut where sequences begin and end (a run with a first token
       // forgets what was before it whatever its a are)
@@ -606,34 +625,28 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(const GlrArgs p) {
       for (int i = 0; i < RUN; ++i) {
         const int s = m.seq_of(i);
         if (m.first >> i & 1) fr.h = ch.get(p.initial_state, s, C);
-        fr.h = f2_fma(a[i], fr.h, u[i]);
+        fr.h = fma2(a[i], fr.h, u[i]);
       }
 #pragma unroll
       for (int i = RUN - 1; i >= 0; --i) {
         const int s = m.seq_of(i);
         if (m.last >> i & 1) rr.h = both(0.f);
-        rr.h = f2_mul(a[i], f2_add(dy_last(i, s), rr.h));
+        rr.h = mul2(a[i], add2(dy_last(i, s), rr.h));
       }
       if (m.first != 0) fr.A = both(0.f);
       if (m.last != 0) rr.A = both(0.f);
     }
+    Run(*fwd_runs)[32] = run_buf + (int)(step & 1) * 2 * kWarps;  // (two buffers: see the forward)
+    Run(*rev_runs)[32] = fwd_runs + kWarps;
     fwd_runs[warp][lane] = fr;
     rev_runs[warp][lane] = rr;
-    __syncthreads();
-    if (warp == 0) {
-      ex.send(step, lane, fold_tile(rev_runs, lane, true));
-    } else if (warp == 1) {  // the state before each run, left in its h
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const Run r = fwd_runs[w][lane];
-        fwd_runs[w][lane].h = h;
-        h = through(r, h);
-      }
-    }
-    __syncthreads();  // both folds are in shared memory
-    f2 e = ex.receive(step, lane, carry, p.err);
-    e = through(rev_runs[warp][lane], e);
-    h = fwd_runs[warp][lane].h;
+    __syncthreads();  // the runs are complete, and the other stage (the step before) is read
+    load(step + 1);
+    Run behind, all;
+    fold_tile<true>(rev_runs, lane, warp, behind, all);
+    ex.send(step, lane, warp, all);
+    for (int w = 0; w < warp; ++w) h = through(fwd_runs[w][lane], h);  // before this run
+    f2 e = through(behind, ex.receive(step, lane, carry));
     // h_{t-1} of every token (into u), then the gradients from the last token back
     char* dx = static_cast<char*>(p.dx) + tile * ROWS * row_bytes;
     char* dl = static_cast<char*>(p.dlog_alpha) + tile * ROWS * row_bytes;
@@ -641,23 +654,23 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(const GlrArgs p) {
     auto out = [&](int i, f2 dh) {  // token i's gradients
       const uint32_t off = (uint32_t)(warp * RUN + i) * row_bytes;
       const f2 x = in(0, i);
-      put_out<T, AL>(dx, off, ch, gated<GATE>(dh, GATE == kGateBeta ? in(N - 1, i) : 0, om[i]));
+      put_out<T, AL>(dx, off, ch, gated<GATE>(dh, GATE == kGateBeta ? in(N - 1, i) : both(0.f), om[i]));
       f2 hb = u[i];
-      if (GATE == kGateComp) hb = f2_fma(x, both(-1.f), hb);
-      put_out<T, AL>(dl, off, ch, f2_mul(hb, e));
-      if (GATE == kGateBeta) put_out<T, AL>(db, off, ch, f2_mul(x, dh));
+      if (GATE == kGateComp) hb = fma2(x, both(-1.f), hb);
+      put_out<T, AL>(dl, off, ch, mul2(hb, e));
+      if (GATE == kGateBeta) put_out<T, AL>(db, off, ch, mul2(x, dh));
     };
     if (inside && t0 >= 0 && t0 + RUN <= T_) {
 #pragma unroll
       for (int i = 0; i < RUN; ++i) {
         const f2 before = h;
-        h = f2_fma(a[i], h, u[i]);
+        h = fma2(a[i], h, u[i]);
         u[i] = before;
       }
 #pragma unroll
       for (int i = RUN - 1; i >= 0; --i) {
-        const f2 dh = f2_add(in(2, i), e);
-        e = f2_mul(a[i], dh);
+        const f2 dh = add2(in(2, i), e);
+        e = mul2(a[i], dh);
         out(i, dh);
       }
     } else {
@@ -666,21 +679,22 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(const GlrArgs p) {
         const int s = m.seq_of(i);
         if (m.first >> i & 1) h = ch.get(p.initial_state, s, C);
         const f2 before = h;
-        h = f2_fma(a[i], h, u[i]);
+        h = fma2(a[i], h, u[i]);
         u[i] = before;
       }
 #pragma unroll
       for (int i = RUN - 1; i >= 0; --i) {
         const int s = m.seq_of(i);
         f2 dh = dy_last(i, s);
-        if (!(m.last >> i & 1)) dh = f2_add(dh, e);
-        e = f2_mul(a[i], dh);
+        if (!(m.last >> i & 1)) dh = add2(dh, e);
+        e = mul2(a[i], dh);
         if (t0 + i >= 0 && t0 + i < T_) out(i, dh);
         if ((m.first >> i & 1) && p.d_initial_state != nullptr)
           ch.put(p.d_initial_state, s, C, e);
       }
     }
   }
+  if (!ex.ok) atomicOr(p.err, kErrTimeout);
   if (n_steps > 0) sm100::cluster_sync();
   empty_sequences<AL>(p, p.d_final_state, p.d_initial_state, ch, rank * kWarps + warp,
                       n_cta * kWarps, blockIdx.y == 0);
@@ -699,10 +713,12 @@ __global__ void __launch_bounds__(256) glr_step_kernel(const Tin* __restrict__ x
   if (i0 >= n) return;
   auto two = [&](float x0, float x1, float l0, float l1, float b0, float b1, float& h0,
                  float& h1) {
-    f2 a, q = 0;
-    decay2<GATE>(f2_pack(l0, l1), a, q);
-    const f2 u = gated<GATE>(f2_pack(x0, x1), f2_pack(b0, b1), q);
-    f2_unpack(f2_fma(a, f2_pack(h0, h1), u), h0, h1);
+    f2 a, q = both(0.f);
+    decay2<GATE>(make_float2(l0, l1), a, q);
+    const f2 u = gated<GATE>(make_float2(x0, x1), make_float2(b0, b1), q);
+    const f2 h = fma2(a, make_float2(h0, h1), u);
+    h0 = h.x;
+    h1 = h.y;
   };
   if (i0 + 8 <= n) {
 #pragma unroll
@@ -727,7 +743,7 @@ __global__ void __launch_bounds__(256) glr_step_kernel(const Tin* __restrict__ x
   }
 }
 
-using ScanKernel = void (*)(GlrArgs);
+using ScanKernel = void (*)(GlrArgs, ScanMaps);
 
 // One compiled scan: its kernel, shared memory and tokens per tile.
 struct Scan {
@@ -763,6 +779,38 @@ cudaLaunchConfig_t scan_config(const Scan& k, int cluster, int groups, cudaStrea
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cfg;
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_tiled() {
+  static const EncodeTiledFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    return cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) ==
+                       cudaSuccess &&
+                   q == cudaDriverEntryPointSuccess
+               ? reinterpret_cast<EncodeTiledFn>(f)
+               : nullptr;
+  }();
+  return fn;
+}
+
+bool encode_map(CUtensorMap* m, const GlrArgs& a, const void* base, int rows) {
+  const EncodeTiledFn fn = encode_tiled();
+  const bool bf16 = a.dtype == GDN_BF16;
+  const cuuint64_t dims[2] = {(cuuint64_t)a.C, (cuuint64_t)a.total_T};
+  const cuuint64_t strides[1] = {(cuuint64_t)a.C * (bf16 ? 2 : 4)};
+  const cuuint32_t box[2] = {(cuuint32_t)kChan, (cuuint32_t)rows};
+  const cuuint32_t one[2] = {1, 1};
+  return fn != nullptr &&
+         fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+            const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Clusters of each size that the device holds at once, per kernel (asked once
@@ -802,9 +850,17 @@ gdn_status launch_scan(const GlrArgs& a, bool bwd, cudaStream_t stream) {
   int cluster = (int)(n_tiles < kMaxCluster ? (n_tiles < 1 ? 1 : n_tiles) : kMaxCluster);
   while (cluster > 1 && clusters_that_fit(dev, variant, k, cluster) < groups) --cluster;
   if (clusters_that_fit(dev, variant, k, cluster) < 1) return GDN_ERR_CUDA;
+  ScanMaps maps = {};
+  if (al && a.total_T > 0) {
+    // (the order in which the kernels number their tensors)
+    const void* src[4] = {a.x, a.log_alpha, bwd ? a.dy : a.beta, a.beta};
+    const int n = 2 + (bwd ? 1 : 0) + (a.gate == kGateBeta ? 1 : 0);
+    for (int i = 0; i < n; ++i)
+      if (!encode_map(&maps.m[i], a, src[i], k.rows)) return GDN_ERR_CUDA;
+  }
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg = scan_config(k, cluster, groups, stream, &attr);
-  return cudaLaunchKernelEx(&cfg, k.kernel, a) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, k.kernel, a, maps) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 template <typename Tin>
