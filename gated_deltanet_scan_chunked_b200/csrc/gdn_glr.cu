@@ -8,22 +8,28 @@
 // (A1 A2, A2 h1 + h2).  A sequence's first token takes a = 0 and adds
 // a_t h_0 to its input, so packed sequences need no other care.
 //
-// Layout.  A CTA of 8 warps owns a tile of 8 kRun tokens x 64 channels: warp w
-// has the run of kRun tokens from w kRun on, a lane two channels (one 4-byte
-// word of bf16).  The carry along the tokens passes
-// three levels, each in a fixed order (results do not depend on timing): a
-// thread's run in registers, the 8 runs of a tile by one warp through shared
-// memory, and the CTAs of a cluster, which hold consecutive tiles of the same
-// channels, through distributed shared memory.  The cluster walks the packed
-// tokens in steps of (cluster size) tiles, the carry kept in registers;
+// Layout.  A CTA of W warps owns a tile of W kRun tokens x 64 channels: warp w
+// has the run of kRun tokens from w kRun on, a lane two channels.  The carry
+// along the tokens passes three levels, each in a fixed order (results do not
+// depend on timing): a thread's run in registers, the tile's runs through
+// shared memory, and the CTAs of a cluster, which hold consecutive tiles of
+// the same channels, through distributed shared memory.  The cluster walks the
+// packed tokens in steps of (cluster size) tiles, the carry kept in registers;
 // nothing is exchanged through global memory, so there is no workspace and no
-// flag to wait on.  Every input is read once and every output written once.
-// Inputs come into two shared-memory stages, so that the next steps' loads are
-// in flight while this one is folded: by TMA where rows of C elements are a
-// multiple of 16 bytes (AL), one box of 64 channels a tensor.  Other rows begin
-// anywhere: a row's piece is then copied from the 16-byte boundary below it
-// by 16-byte asynchronous copies, one more than it needs, and read from its
-// remainder on.
+// flag in it to wait on.  Every input is read once and every output written
+// once.
+//
+// Inputs come into two shared-memory stages, so that the next step's loads are
+// in flight while this one is folded, and outputs leave from the places of the
+// inputs that they replace: by TMA where rows of C elements are a multiple of
+// 16 bytes (AL), one box of 64 channels a tensor.  Other rows begin anywhere: a
+// row's piece is then copied from the 16-byte boundary below it by 16-byte
+// asynchronous copies, one more than it needs, and read from its remainder on;
+// outputs are stored from registers.
+//
+// Runs in which a sequence begins or ends take a path of their own, in rolled
+// loops that form a_t and b_t x_t again from the stage: few runs do, and
+// unrolled it would fill the instruction cache for all.
 #include <cuda.h>
 
 #include <atomic>
@@ -35,8 +41,6 @@
 namespace gdn {
 namespace {
 
-constexpr int kWarps = 8;  // (>= kMaxCluster)
-constexpr int kThreads = 32 * kWarps;
 constexpr int kChan = 64;  // channels of a CTA
 constexpr int kMaxCluster = 8;
 constexpr uint32_t kWait = 1u << 24;  // polls of a bounded wait
@@ -194,26 +198,24 @@ struct Piece {
     }
     if (AL) return *reinterpret_cast<const f2*>(row + 8 * lane);
     return make_float2(*reinterpret_cast<const float*>(row + rem + 4 * lane),
-                   *reinterpret_cast<const float*>(row + rem + 4 * lane + 128));
+                       *reinterpret_cast<const float*>(row + rem + 4 * lane + 128));
+  }
+  // Leaves an output in its input's place (AL).
+  static __device__ __forceinline__ void put(char* row, int lane, f2 v) {
+    if (sizeof(T) == 2)
+      *reinterpret_cast<uint32_t*>(row + 4 * lane) = sm100::pack_bf16(v.x, v.y);
+    else
+      *reinterpret_cast<f2*>(row + 8 * lane) = v;
   }
 };
 
-// Stores a lane's two channels of a token row; `base` is the same for the whole
-// CTA, `off` the bytes from it to the row's channel 0.
-template <typename T, bool AL>
-__device__ __forceinline__ void put_out(char* base, uint32_t off, const Chan<AL>& ch, f2 v) {
+// Stores a lane's two channels of a token row (unaligned rows); `base` is the
+// same for the whole CTA, `off` the bytes from it to the row's channel 0.
+template <typename T>
+__device__ __forceinline__ void put_out(char* base, uint32_t off, const Chan<false>& ch, f2 v) {
   T* q = reinterpret_cast<T*>(base + (off + (uint32_t)ch.c0 * (uint32_t)sizeof(T)));
-  if (AL) {
-    if (ch.ok0) {
-      if (sizeof(T) == 2)
-        *reinterpret_cast<uint32_t*>(q) = sm100::pack_bf16(v.x, v.y);
-      else
-        *reinterpret_cast<f2*>(q) = v;
-    }
-  } else {
-    if (ch.ok0) Elem<T>::store(q, v.x);
-    if (ch.ok1) Elem<T>::store(q + 32, v.y);
-  }
+  if (ch.ok0) Elem<T>::store(q, v.x);
+  if (ch.ok1) Elem<T>::store(q + 32, v.y);
 }
 
 // 16 bytes of which the first n (0 .. 16) are read, the rest zero filled.
@@ -222,16 +224,16 @@ __device__ __forceinline__ void copy16(uint32_t dst, const char* src, int n) {
                : "memory");
 }
 
-// TMA maps of the inputs (AL only): [total_T, C] with boxes of kChan channels x
-// a tile's tokens.
+// TMA maps of the inputs and outputs (AL only): [total_T, C] with boxes of kChan
+// channels x a tile's tokens.
 struct ScanMaps {
-  CUtensorMap m[4];
+  CUtensorMap in[4], out[3];
 };
 
 // Two stages of N input tensors' tiles of ROWS tokens.  Tokens outside [0, T)
 // become zeros: a = exp(0) = 1 and x = 0 leave a state as it is.  Loads are
 // numbered by step; step s goes to stage s & 1.
-template <typename T, bool AL, int ROWS, int N>
+template <typename T, bool AL, int ROWS, int N, int THREADS>
 struct Stages {
   using P = Piece<T, AL>;
   static constexpr int kTensor = P::bytes(ROWS), kStage = N * kTensor;
@@ -246,7 +248,8 @@ struct Stages {
       sm100::fence_mbar_init();
     }
   }
-  // (by every thread, after a barrier behind the last reads of the stage)
+  // (by every thread, after a barrier behind the last use of the stage; the
+  // outputs that leave from it are read before it is filled again)
   __device__ __forceinline__ void load(int64_t step, bool any, const char* const (&src)[N],
                                        const ScanMaps& maps, int64_t t0, int64_t total_T, int C,
                                        int cb) {
@@ -254,40 +257,53 @@ struct Stages {
     if constexpr (AL) {
       if (any && threadIdx.x == 0) {
         uint64_t* bar = &full[step & 1];
+        sm100::bulk_wait_read_all();
         sm100::mbar_arrive_expect_tx(bar, kStage);
 #pragma unroll
         for (int k = 0; k < N; ++k)
-          sm100::tma_load_2d(stage + k * kTensor, &maps.m[k], cb, (int)t0, bar);
+          sm100::tma_load_2d(stage + k * kTensor, &maps.in[k], cb, (int)t0, bar);
       }
-    } else {
-      if (any) {
-        const int64_t row_bytes = (int64_t)C * (int)sizeof(T), all = total_T * row_bytes;
-        for (int i = threadIdx.x; i < ROWS * P::kCopies; i += kThreads) {
-          const int r = i / P::kCopies, q = i % P::kCopies;
-          const int64_t t = t0 + r;
-          int64_t off = ((t * row_bytes + (int64_t)cb * (int)sizeof(T)) & ~(int64_t)15) + 16 * q;
-          int n = 0;
-          if (t >= 0 && t < total_T)
-            n = all - off >= 16 ? 16 : all - off > 0 ? (int)(all - off) : 0;
-          if (n == 0) off = 0;
+    } else if (any) {
+      const int64_t row_bytes = (int64_t)C * (int)sizeof(T), all = total_T * row_bytes;
+      for (int i = threadIdx.x; i < ROWS * P::kCopies; i += THREADS) {
+        const int r = i / P::kCopies, q = i % P::kCopies;
+        const int64_t t = t0 + r;
+        int64_t off = ((t * row_bytes + (int64_t)cb * (int)sizeof(T)) & ~(int64_t)15) + 16 * q;
+        int n = 0;
+        if (t >= 0 && t < total_T) n = all - off >= 16 ? 16 : all - off > 0 ? (int)(all - off) : 0;
+        if (n == 0) off = 0;
 #pragma unroll
-          for (int k = 0; k < N; ++k)
-            copy16(stage + k * kTensor + r * P::kPitch + 16 * q, src[k] + off, n);
-        }
+        for (int k = 0; k < N; ++k)
+          copy16(stage + k * kTensor + r * P::kPitch + 16 * q, src[k] + off, n);
       }
-      sm100::cp_async_commit();
     }
   }
-  // (by every thread) Waits for the step's inputs; AHEAD: a later step's loads
-  // are under way too.  ok: no bounded wait ran out yet (then none is made).
-  template <bool AHEAD>
+  // (by every thread) Waits for the step's inputs.  ok: no bounded wait ran out
+  // yet (then none is made).
   __device__ __forceinline__ bool wait(int64_t step, bool ok) {
     if constexpr (AL) {
       return ok && sm100::mbar_wait(&full[step & 1], (uint32_t)(step >> 1) & 1u, kWait);
     } else {
-      if (AHEAD) sm100::cp_async_wait_group1(); else sm100::cp_async_wait_all();
+      sm100::cp_async_wait_all();
       __syncthreads();
       return ok;
+    }
+  }
+  // (by every thread, its outputs in the places of the first `n` inputs; AL)
+  // Sends the tile of step `step` off.
+  __device__ __forceinline__ void store(int64_t step, int n, const ScanMaps& maps, int64_t t0,
+                                        int cb) {
+    sm100::fence_proxy_async();  // the outputs, before the copies read them
+    if (threadIdx.x >= 32) {
+      sm100::named_arrive(1, THREADS);
+      return;
+    }
+    sm100::named_sync(1, THREADS);
+    if (threadIdx.x == 0) {
+      const uint32_t stage = sm100::smem_u32(at) + (uint32_t)(step & 1) * kStage;
+      for (int k = 0; k < n; ++k)
+        sm100::tma_store_2d(&maps.out[k], cb, (int)t0, stage + k * kTensor);
+      sm100::bulk_commit();
     }
   }
 };
@@ -304,14 +320,14 @@ __device__ __forceinline__ void send_run(uint32_t addr, uint32_t bar, const Run&
 
 // The runs of a tile's warps, in order or backwards: what lies before this
 // warp's run, and the whole.
-template <bool BACK>
+template <int W, bool BACK>
 __device__ __forceinline__ void fold_tile(const Run (*runs)[32], int lane, int warp, Run& before,
                                           Run& all) {
   all.A = both(1.f);
   all.h = both(0.f);
 #pragma unroll
-  for (int k = 0; k < kWarps; ++k) {
-    const int w = BACK ? kWarps - 1 - k : k;
+  for (int k = 0; k < W; ++k) {
+    const int w = BACK ? W - 1 - k : k;
     if (w == warp) before = all;
     const Run r = runs[w][lane];
     all.h = through(r, all.h);
@@ -325,7 +341,7 @@ __device__ __forceinline__ void fold_tile(const Run (*runs)[32], int lane, int w
 // before.  Two buffers alternate: a CTA sends step s + 2 only after it has
 // everyone's step s + 1, which each sends after its reads of step s.
 struct Exchange {
-  Run (*tiles)[32];  // [2][kMaxCluster]
+  Run (*tiles)[32];  // [2][n_cta]
   uint64_t* bar;     // [2]
   int n_cta, rank;
   bool ok = true;
@@ -338,15 +354,16 @@ struct Exchange {
       sm100::fence_mbar_init();
     }
   }
-  // (by every warp: warp w sends to CTA w; kMaxCluster warps serve the largest cluster)
+  // (by every warp: warp w of W sends to CTAs w, w + W, ..)
+  template <int W>
   __device__ __forceinline__ void send(int64_t step, int lane, int warp, const Run& all) {
     const int b = (int)(step & 1);
     if (threadIdx.x == 0)
       sm100::mbar_arrive_expect_tx(&bar[b], (uint32_t)n_cta * 32u * (uint32_t)sizeof(Run));
-    if (warp < n_cta)
-      send_run(sm100::mapa_shared(sm100::smem_u32(&tiles[b * kMaxCluster + rank][lane]),
-                                  (uint32_t)warp),
-               sm100::mapa_shared(sm100::smem_u32(&bar[b]), (uint32_t)warp), all);
+    const uint32_t to = sm100::smem_u32(&tiles[b * n_cta + rank][lane]);
+    const uint32_t on = sm100::smem_u32(&bar[b]);
+    for (int r = warp; r < n_cta; r += W)
+      send_run(sm100::mapa_shared(to, (uint32_t)r), sm100::mapa_shared(on, (uint32_t)r), all);
   }
   // Waits for the step's runs; h: the carry before this CTA's tile; carry
   // moves on past the whole step.
@@ -358,7 +375,7 @@ struct Exchange {
 #pragma unroll 4
     for (int r = 0; r < n_cta; ++r) {
       if (r == rank) h = carry;
-      carry = through(tiles[b * kMaxCluster + r][lane], carry);
+      carry = through(tiles[b * n_cta + r][lane], carry);
     }
     return h;
   }
@@ -387,40 +404,44 @@ __device__ __forceinline__ void empty_sequences(const GlrArgs& p, const float* i
   }
 }
 
-// Shared memory of a CTA: the runs of a tile (`run_sets` arrays, two buffers
-// each), the cluster's tiles (two buffers), the barriers, two stages.
-template <typename T, bool AL>
-constexpr int scan_smem(int run, int tensors, int run_sets) {
-  return 2 * run_sets * kWarps * 32 * (int)sizeof(Run) + 2 * kMaxCluster * 32 * (int)sizeof(Run) +
-         128 + 2 * tensors * Piece<T, AL>::bytes(kWarps * run);
-}
+// Warps of a CTA and tokens of a thread's run.  The forward holds a and b x of
+// its run in registers (4 a token); more, smaller CTAs spread evenly over the
+// SMs.  The backward starts each tile from a checkpoint.
+template <typename T>
+struct FwdShape {
+  static constexpr int W = 4, RUN = sizeof(T) == 2 ? 16 : 8;
+};
+struct BwdShape {
+  static constexpr int W = 8, RUN = 8;
+};
+static_assert(BwdShape::W * BwdShape::RUN == kGlrTile, "a tile per checkpoint");
 
-// Tokens of a thread's run.
-template <typename T, bool AL>
-constexpr int fwd_run() { return sizeof(T) == 2 && AL ? 16 : 8; }
-constexpr int kBwdRun = 8;
-static_assert(kBwdRun * kWarps == kGlrTile, "the backward starts each tile from a checkpoint");
+// Shared memory of a CTA: the runs of a tile (`sets` arrays, two buffers each),
+// the cluster's tiles (two buffers), the barriers, two stages.
+constexpr int runs_bytes(int w, int sets) { return 2 * sets * w * 32 * (int)sizeof(Run); }
+constexpr int tiles_bytes(int cluster) { return 2 * cluster * 32 * (int)sizeof(Run); }
+constexpr int kBarBytes = 128;
+static_assert(runs_bytes(1, 1) % 128 == 0 && tiles_bytes(1) % 128 == 0, "stages on 128 bytes");
 
 template <typename T, int GATE, bool AL>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(32 * FwdShape<T>::W, 16 / FwdShape<T>::W)
     glr_fwd_kernel(const GlrArgs p, const __grid_constant__ ScanMaps maps) {
-  constexpr int RUN = fwd_run<T, AL>();
-  constexpr int ROWS = kWarps * RUN;
+  constexpr int RUN = FwdShape<T>::RUN, W = FwdShape<T>::W, ROWS = W * RUN;
   constexpr int N = GATE == kGateBeta ? 3 : 2;
   using P = Piece<T, AL>;
   extern __shared__ __align__(128) char smem[];
-  Run(*run_buf)[32] = reinterpret_cast<Run(*)[32]>(smem);  // [2][kWarps]
-  Exchange ex;
-  ex.tiles = run_buf + 2 * kWarps;
-  ex.bar = reinterpret_cast<uint64_t*>(ex.tiles + 2 * kMaxCluster);
-  Stages<T, AL, ROWS, N> in;
-  in.full = ex.bar + 2;
-  in.at = reinterpret_cast<char*>(ex.bar) + 128;
-
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n_cta = (int)gridDim.x, rank = (int)blockIdx.x;  // one cluster along x
+  Run(*run_buf)[32] = reinterpret_cast<Run(*)[32]>(smem);    // [2][W]
+  Exchange ex;
   ex.n_cta = n_cta;
   ex.rank = rank;
+  ex.tiles = run_buf + 2 * W;
+  ex.bar = reinterpret_cast<uint64_t*>(ex.tiles + 2 * n_cta);
+  Stages<T, AL, ROWS, N, 32 * W> stages;
+  stages.full = ex.bar + 2;
+  stages.at = reinterpret_cast<char*>(ex.bar) + kBarBytes;
+
   const int C = p.C, cb = (int)blockIdx.y * kChan;
   const Chan<AL> ch(cb, lane, C);
   const int64_t T_ = p.total_T;
@@ -432,13 +453,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   src[1] = static_cast<const char*>(p.log_alpha);
   if (N == 3) src[N - 1] = static_cast<const char*>(p.beta);
   auto load = [&](int64_t step) {
-    in.load(step, step < n_steps, src, maps, (step * n_cta + rank) * ROWS, T_, C, cb);
+    stages.load(step, step < n_steps, src, maps, (step * n_cta + rank) * ROWS, T_, C, cb);
   };
 
   f2 carry = both(0.f);  // state before this step's first tile
   Marks<RUN, false> m;
   if (n_steps > 0) {
-    in.init();
+    stages.init();
     ex.init();
     sm100::cluster_sync();  // every CTA runs, its barriers set, before any sends
     load(0);
@@ -447,82 +468,89 @@ __global__ void __launch_bounds__(kThreads, 2)
   for (int64_t step = 0; step < n_steps; ++step) {
     const int64_t tile0 = (step * n_cta + rank) * ROWS, t0 = tile0 + warp * RUN;
     m.look(p, t0, lane);
-    ex.ok = in.template wait<true>(step, ex.ok);
+    const bool inside = (m.first | m.last) == 0;
+    ex.ok = stages.wait(step, ex.ok);
+    char* st = stages.at + (int)(step & 1) * stages.kStage + warp * RUN * P::kPitch;
+    const uint32_t rem = (uint32_t)t0 * row_bytes + (uint32_t)cb * (uint32_t)sizeof(T);
+    auto in = [&](int k, int i) {  // tensor k at token i of the run
+      return P::get(st + k * stages.kTensor + i * P::kPitch,
+                    AL ? 0 : (int)((rem + (uint32_t)i * row_bytes) & 15u), lane);
+    };
+    auto form = [&](int i, f2& a, f2& u) {  // a_t and b_t x_t
+      f2 q;
+      decay2<GATE>(in(1, i), a, q);
+      u = gated<GATE>(in(0, i), GATE == kGateBeta ? in(N - 1, i) : both(0.f), q);
+    };
     f2 a[RUN], u[RUN];
     Run run;
-    {
-      const char* st = in.at + (int)(step & 1) * in.kStage + warp * RUN * P::kPitch;
-      const uint32_t rem = (uint32_t)t0 * row_bytes + (uint32_t)cb * (uint32_t)sizeof(T);
-      run.A = both(1.f);
-      run.h = both(0.f);
+    run.A = both(1.f);
+    run.h = both(0.f);
+    if (inside) {
 #pragma unroll
       for (int i = 0; i < RUN; ++i) {
-        const char* row = st + i * P::kPitch;
-        const int at = AL ? 0 : (int)((rem + (uint32_t)i * row_bytes) & 15u);
-        const f2 x = P::get(row, at, lane);
-        const f2 l = P::get(row + in.kTensor, at, lane);
-        f2 b = both(0.f), q = both(0.f);
-        if (GATE == kGateBeta) b = P::get(row + 2 * in.kTensor, at, lane);
-        decay2<GATE>(l, a[i], q);
-        u[i] = gated<GATE>(x, b, q);
+        form(i, a[i], u[i]);
         run.A = mul2(run.A, a[i]);
         run.h = fma2(a[i], run.h, u[i]);
       }
-    }
-    if (m.first != 0) {  // again, with the sequences' first tokens cut off
-#pragma unroll
+    } else {
+#pragma unroll 1
       for (int i = 0; i < RUN; ++i) {
         const int s = m.seq_of(i);
-        if (m.first >> i & 1) {
-          // (without a state, nothing: a_t = inf or NaN stays out of it)
-          if (p.initial_state != nullptr)
-            u[i] = fma2(a[i], ch.get(p.initial_state, s, C), u[i]);
-          a[i] = both(0.f);
-          run.h = u[i];
-        } else {
-          run.h = i == 0 ? u[0] : fma2(a[i], run.h, u[i]);
-        }
+        f2 ai, ui;
+        form(i, ai, ui);
+        if (m.first >> i & 1) run.h = ch.get(p.initial_state, s, C);
+        run.A = mul2(run.A, ai);
+        run.h = fma2(ai, run.h, ui);
       }
-      run.A = both(0.f);
+      // (a run with a first token forgets what was before, whatever its a are)
+      if (m.first != 0) run.A = both(0.f);
     }
     // (two buffers: a warp may still fold this step's runs when others write
     // the next one's)
-    Run(*runs)[32] = run_buf + (int)(step & 1) * kWarps;
+    Run(*runs)[32] = run_buf + (int)(step & 1) * W;
     runs[warp][lane] = run;
-    __syncthreads();  // the runs are complete, and this stage is read
-    load(step + 2);
+    __syncthreads();  // the runs are complete; the step before is done with its stage
+    if (step > 0) load(step + 1);
     Run before, all;
-    fold_tile<false>(runs, lane, warp, before, all);
-    ex.send(step, lane, warp, all);
+    fold_tile<W, false>(runs, lane, warp, before, all);
+    ex.template send<W>(step, lane, warp, all);
     f2 h = through(before, ex.receive(step, lane, carry));
-    if (p.checkpoints != nullptr && warp % (kGlrTile / RUN) == 0 && t0 < T_)
+    if (p.checkpoints != nullptr && t0 % kGlrTile == 0 && t0 < T_)
       ch.put(p.checkpoints, t0 / kGlrTile, C, h);
     if (p.y == nullptr) continue;
     char* y = static_cast<char*>(p.y) + tile0 * row_bytes;
-    uint32_t off = (uint32_t)(warp * RUN) * row_bytes;
-    if ((m.first | m.last) == 0 && t0 + RUN <= T_) {
+    auto out = [&](int i) {
+      if constexpr (AL) {
+        P::put(st + i * P::kPitch, lane, h);
+      } else {
+        if (t0 + i < T_) put_out<T>(y, (uint32_t)(warp * RUN + i) * row_bytes, ch, h);
+      }
+    };
+    if (inside) {
 #pragma unroll
       for (int i = 0; i < RUN; ++i) {
         h = fma2(a[i], h, u[i]);
-        put_out<T, AL>(y, off, ch, h);
-        off += row_bytes;
+        out(i);
       }
     } else {
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < RUN; ++i) {
         const int s = m.seq_of(i);
-        // (a sequence's first token: a = 0, and whatever h was is dropped)
-        h = (m.first >> i & 1) ? u[i] : fma2(a[i], h, u[i]);
-        if (t0 + i < T_) put_out<T, AL>(y, off, ch, h);
-        off += row_bytes;
+        f2 ai, ui;
+        form(i, ai, ui);
+        if (m.first >> i & 1) h = ch.get(p.initial_state, s, C);
+        h = fma2(ai, h, ui);
+        out(i);
         if ((m.last >> i & 1) && p.final_state != nullptr) ch.put(p.final_state, s, C, h);
       }
     }
+    if (AL && tile0 < T_) stages.store(step, 1, maps, tile0, cb);
   }
   if (!ex.ok) atomicOr(p.err, kErrTimeout);
+  if (AL && threadIdx.x == 0) sm100::bulk_wait_all();
   if (n_steps > 0) sm100::cluster_sync();  // (a CTA that gave up waiting may still be sent to)
-  empty_sequences<AL>(p, p.initial_state, p.final_state, ch, rank * kWarps + warp,
-                      n_cta * kWarps, blockIdx.y == 0);
+  empty_sequences<AL>(p, p.initial_state, p.final_state, ch, rank * W + warp, n_cta * W,
+                      blockIdx.y == 0);
 }
 
 // Backward.  With e_t = a_t dh_t (what token t hands to t - 1),
@@ -535,25 +563,25 @@ __global__ void __launch_bounds__(kThreads, 2)
 // from the tile's checkpoint (the state before it, from the forward), so the
 // forward carry needs the first two levels only.
 template <typename T, int GATE, bool AL>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(32 * BwdShape::W, 16 / BwdShape::W)
     glr_bwd_kernel(const GlrArgs p, const __grid_constant__ ScanMaps maps) {
-  constexpr int RUN = kBwdRun;
-  constexpr int ROWS = kWarps * RUN;
-  constexpr int N = GATE == kGateBeta ? 4 : 3;  // x, log_alpha, dy, beta
+  constexpr int RUN = BwdShape::RUN, W = BwdShape::W, ROWS = W * RUN;
+  constexpr int N = GATE == kGateBeta ? 4 : 3;  // x, log_alpha, [beta,] dy
+  constexpr int kBeta = 2, kDy = N - 1;
   using P = Piece<T, AL>;
   extern __shared__ __align__(128) char smem[];
-  Run(*run_buf)[32] = reinterpret_cast<Run(*)[32]>(smem);  // [2][forward, reverse][kWarps]
-  Exchange ex;
-  ex.tiles = run_buf + 4 * kWarps;
-  ex.bar = reinterpret_cast<uint64_t*>(ex.tiles + 2 * kMaxCluster);
-  Stages<T, AL, ROWS, N> stages;
-  stages.full = ex.bar + 2;
-  stages.at = reinterpret_cast<char*>(ex.bar) + 128;
-
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n_cta = (int)gridDim.x, rank = (int)blockIdx.x;
+  Run(*run_buf)[32] = reinterpret_cast<Run(*)[32]>(smem);  // [2][forward, reverse][W]
+  Exchange ex;
   ex.n_cta = n_cta;
   ex.rank = rank;
+  ex.tiles = run_buf + 4 * W;
+  ex.bar = reinterpret_cast<uint64_t*>(ex.tiles + 2 * n_cta);
+  Stages<T, AL, ROWS, N, 32 * W> stages;
+  stages.full = ex.bar + 2;
+  stages.at = reinterpret_cast<char*>(ex.bar) + kBarBytes;
+
   const int C = p.C, cb = (int)blockIdx.y * kChan;
   const Chan<AL> ch(cb, lane, C);
   const int64_t T_ = p.total_T;
@@ -563,8 +591,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   const char* src[N];
   src[0] = static_cast<const char*>(p.x);
   src[1] = static_cast<const char*>(p.log_alpha);
-  src[2] = static_cast<const char*>(p.dy);
-  if (N == 4) src[N - 1] = static_cast<const char*>(p.beta);
+  if (N == 4) src[kBeta] = static_cast<const char*>(p.beta);
+  src[kDy] = static_cast<const char*>(p.dy);
   // tiles in reverse: rank r of step s has tile n_tiles - 1 - (s n_cta + r),
   // negative (nothing to do, all neutral) behind the first tile
   auto load = [&](int64_t step) {
@@ -579,125 +607,141 @@ __global__ void __launch_bounds__(kThreads, 2)
     ex.init();
     sm100::cluster_sync();
     load(0);
+    load(1);
   }
   for (int64_t step = 0; step < n_steps; ++step) {
     const int64_t tile = n_tiles - 1 - (step * n_cta + rank);
     const int64_t t0 = tile * ROWS + warp * RUN;
     m.look(p, t0, lane);
+    const bool inside = (m.first | m.last) == 0;
     f2 h = both(0.f);
     if (tile >= 0) h = ch.get(p.checkpoints, tile, C);
-    ex.ok = stages.template wait<false>(step, ex.ok);
-    const char* st = stages.at + (int)(step & 1) * stages.kStage + warp * RUN * P::kPitch;
+    ex.ok = stages.wait(step, ex.ok);
+    char* st = stages.at + (int)(step & 1) * stages.kStage + warp * RUN * P::kPitch;
     const uint32_t rem = (uint32_t)t0 * row_bytes + (uint32_t)cb * (uint32_t)sizeof(T);
     auto in = [&](int k, int i) {  // tensor k at token i of the run
       return P::get(st + k * stages.kTensor + i * P::kPitch,
                     AL ? 0 : (int)((rem + (uint32_t)i * row_bytes) & 15u), lane);
     };
-    // dh_T joins its sequence's last dy; h_0 enters where a sequence begins
-    // (i: a constant once the loops are unrolled)
-    auto dy_last = [&](int i, int s) {
-      const f2 d = in(2, i);
+    auto form = [&](int i, f2& a, f2& u, f2& om) {  // a_t, b_t x_t, 1 - a_t
+      decay2<GATE>(in(1, i), a, om);
+      u = gated<GATE>(in(0, i), GATE == kGateBeta ? in(kBeta, i) : both(0.f), om);
+    };
+    // dy, to which dh_T joins at its sequence's last token
+    auto dy_at = [&](int i, int s) {
+      const f2 d = in(kDy, i);
       return (m.last >> i & 1) && p.d_final_state != nullptr
                  ? add2(d, ch.get(p.d_final_state, s, C))
                  : d;
     };
-    f2 a[RUN], u[RUN], om[RUN];  // om: 1 - a
+    f2 a[RUN], u[RUN], om[RUN];
     Run fr, rr;
     fr.A = rr.A = both(1.f);
     fr.h = rr.h = both(0.f);
-#pragma unroll
-    for (int i = 0; i < RUN; ++i) {
-      decay2<GATE>(in(1, i), a[i], om[i]);
-      u[i] = gated<GATE>(in(0, i), GATE == kGateBeta ? in(N - 1, i) : both(0.f), om[i]);
-      fr.A = mul2(fr.A, a[i]);
-      fr.h = fma2(a[i], fr.h, u[i]);
-    }
-    rr.A = fr.A;
-    const bool inside = (m.first | m.last) == 0;
     if (inside) {
 #pragma unroll
-      for (int i = RUN - 1; i >= 0; --i) rr.h = mul2(a[i], add2(in(2, i), rr.h));
-    } else {
-      // again, cut where sequences begin and end (a run with a first token
-      // forgets what was before it whatever its a are)
-      fr.h = both(0.f);
-#pragma unroll
       for (int i = 0; i < RUN; ++i) {
-        const int s = m.seq_of(i);
-        if (m.first >> i & 1) fr.h = ch.get(p.initial_state, s, C);
+        form(i, a[i], u[i], om[i]);
+        fr.A = mul2(fr.A, a[i]);
         fr.h = fma2(a[i], fr.h, u[i]);
       }
+      rr.A = fr.A;
 #pragma unroll
+      for (int i = RUN - 1; i >= 0; --i) rr.h = mul2(a[i], add2(in(kDy, i), rr.h));
+    } else {
+      f2 ai, ui, oi;
+#pragma unroll 1
+      for (int i = 0; i < RUN; ++i) {
+        const int s = m.seq_of(i);
+        form(i, ai, ui, oi);
+        if (m.first >> i & 1) fr.h = ch.get(p.initial_state, s, C);
+        fr.A = mul2(fr.A, ai);
+        fr.h = fma2(ai, fr.h, ui);
+      }
+      rr.A = fr.A;
+#pragma unroll 1
       for (int i = RUN - 1; i >= 0; --i) {
         const int s = m.seq_of(i);
+        form(i, ai, ui, oi);
         if (m.last >> i & 1) rr.h = both(0.f);
-        rr.h = mul2(a[i], add2(dy_last(i, s), rr.h));
+        rr.h = mul2(ai, add2(dy_at(i, s), rr.h));
       }
+      // (a run cut by a sequence's end forgets what is beyond it)
       if (m.first != 0) fr.A = both(0.f);
       if (m.last != 0) rr.A = both(0.f);
     }
-    Run(*fwd_runs)[32] = run_buf + (int)(step & 1) * 2 * kWarps;  // (two buffers: see the forward)
-    Run(*rev_runs)[32] = fwd_runs + kWarps;
+    Run(*fwd_runs)[32] = run_buf + (int)(step & 1) * 2 * W;  // (two buffers: see the forward)
+    Run(*rev_runs)[32] = fwd_runs + W;
     fwd_runs[warp][lane] = fr;
     rev_runs[warp][lane] = rr;
-    __syncthreads();  // the runs are complete, and the other stage (the step before) is read
-    load(step + 1);
+    __syncthreads();  // the runs are complete; the step before is done with its stage
+    if (step > 0) load(step + 1);
     Run behind, all;
-    fold_tile<true>(rev_runs, lane, warp, behind, all);
-    ex.send(step, lane, warp, all);
+    fold_tile<W, true>(rev_runs, lane, warp, behind, all);
+    ex.template send<W>(step, lane, warp, all);
     for (int w = 0; w < warp; ++w) h = through(fwd_runs[w][lane], h);  // before this run
     f2 e = through(behind, ex.receive(step, lane, carry));
-    // h_{t-1} of every token (into u), then the gradients from the last token back
-    char* dx = static_cast<char*>(p.dx) + tile * ROWS * row_bytes;
-    char* dl = static_cast<char*>(p.dlog_alpha) + tile * ROWS * row_bytes;
-    char* db = static_cast<char*>(p.dbeta) + tile * ROWS * row_bytes;
-    auto out = [&](int i, f2 dh) {  // token i's gradients
-      const uint32_t off = (uint32_t)(warp * RUN + i) * row_bytes;
+    // Token i's gradients, from its x, h_{t-1} (hb), dh, e and b's parts.
+    const int64_t o0 = tile * ROWS * row_bytes;
+    auto out = [&](int i, f2 dh, f2 hb, f2 om_i) {
       const f2 x = in(0, i);
-      put_out<T, AL>(dx, off, ch, gated<GATE>(dh, GATE == kGateBeta ? in(N - 1, i) : both(0.f), om[i]));
-      f2 hb = u[i];
+      const f2 dx = gated<GATE>(dh, GATE == kGateBeta ? in(kBeta, i) : both(0.f), om_i);
       if (GATE == kGateComp) hb = fma2(x, both(-1.f), hb);
-      put_out<T, AL>(dl, off, ch, mul2(hb, e));
-      if (GATE == kGateBeta) put_out<T, AL>(db, off, ch, mul2(x, dh));
+      const f2 dl = mul2(hb, e), db = mul2(x, dh);
+      if constexpr (AL) {
+        char* row = st + i * P::kPitch;
+        P::put(row, lane, dx);
+        P::put(row + stages.kTensor, lane, dl);
+        if (GATE == kGateBeta) P::put(row + kBeta * stages.kTensor, lane, db);
+      } else if (t0 + i >= 0 && t0 + i < T_) {
+        const uint32_t off = (uint32_t)(warp * RUN + i) * row_bytes;
+        put_out<T>(static_cast<char*>(p.dx) + o0, off, ch, dx);
+        put_out<T>(static_cast<char*>(p.dlog_alpha) + o0, off, ch, dl);
+        if (GATE == kGateBeta) put_out<T>(static_cast<char*>(p.dbeta) + o0, off, ch, db);
+      }
     };
-    if (inside && t0 >= 0 && t0 + RUN <= T_) {
+    if (inside) {
 #pragma unroll
-      for (int i = 0; i < RUN; ++i) {
-        const f2 before = h;
-        h = fma2(a[i], h, u[i]);
-        u[i] = before;
+      for (int i = 0; i < RUN; ++i) {  // h_{t-1} of every token, into u
+        const f2 next = fma2(a[i], h, u[i]);
+        u[i] = h;
+        h = next;
       }
 #pragma unroll
       for (int i = RUN - 1; i >= 0; --i) {
-        const f2 dh = add2(in(2, i), e);
+        const f2 dh = add2(in(kDy, i), e);
         e = mul2(a[i], dh);
-        out(i, dh);
+        out(i, dh, u[i], om[i]);
       }
     } else {
-#pragma unroll
+      f2 before[RUN], ai, ui, oi;  // (indexed: in local memory)
+#pragma unroll 1
       for (int i = 0; i < RUN; ++i) {
         const int s = m.seq_of(i);
+        form(i, ai, ui, oi);
         if (m.first >> i & 1) h = ch.get(p.initial_state, s, C);
-        const f2 before = h;
-        h = fma2(a[i], h, u[i]);
-        u[i] = before;
+        before[i] = h;
+        h = fma2(ai, h, ui);
       }
-#pragma unroll
+#pragma unroll 1
       for (int i = RUN - 1; i >= 0; --i) {
         const int s = m.seq_of(i);
-        f2 dh = dy_last(i, s);
+        form(i, ai, ui, oi);
+        f2 dh = dy_at(i, s);
         if (!(m.last >> i & 1)) dh = add2(dh, e);
-        e = mul2(a[i], dh);
-        if (t0 + i >= 0 && t0 + i < T_) out(i, dh);
+        e = mul2(ai, dh);
+        out(i, dh, before[i], oi);
         if ((m.first >> i & 1) && p.d_initial_state != nullptr)
           ch.put(p.d_initial_state, s, C, e);
       }
     }
+    if (AL && tile >= 0) stages.store(step, N - 1, maps, tile * ROWS, cb);
   }
   if (!ex.ok) atomicOr(p.err, kErrTimeout);
+  if (AL && threadIdx.x == 0) sm100::bulk_wait_all();
   if (n_steps > 0) sm100::cluster_sync();
-  empty_sequences<AL>(p, p.d_final_state, p.d_initial_state, ch, rank * kWarps + warp,
-                      n_cta * kWarps, blockIdx.y == 0);
+  empty_sequences<AL>(p, p.d_final_state, p.d_initial_state, ch, rank * W + warp, n_cta * W,
+                      blockIdx.y == 0);
 }
 
 // One token: [N, C] arrays, all dense and of one shape, so n = N C values in
@@ -745,18 +789,24 @@ __global__ void __launch_bounds__(256) glr_step_kernel(const Tin* __restrict__ x
 
 using ScanKernel = void (*)(GlrArgs, ScanMaps);
 
-// One compiled scan: its kernel, shared memory and tokens per tile.
+// One compiled scan: its kernel, threads, tokens per tile and shared memory
+// (apart from the cluster's part).
 struct Scan {
   ScanKernel kernel;
-  int smem, rows;
+  int threads, rows, smem;
 };
 
 template <typename T, bool AL, int GATE>
 Scan scan_of(bool bwd) {
-  constexpr int F = fwd_run<T, AL>(), G = GATE == kGateBeta ? 1 : 0;
-  return bwd ? Scan{glr_bwd_kernel<T, GATE, AL>, scan_smem<T, AL>(kBwdRun, 3 + G, 2),
-                    kWarps * kBwdRun}
-             : Scan{glr_fwd_kernel<T, GATE, AL>, scan_smem<T, AL>(F, 2 + G, 1), kWarps * F};
+  constexpr int G = GATE == kGateBeta ? 1 : 0;
+  if (bwd) {
+    constexpr int W = BwdShape::W, rows = W * BwdShape::RUN;
+    return {glr_bwd_kernel<T, GATE, AL>, 32 * W, rows,
+            runs_bytes(W, 2) + kBarBytes + 2 * (3 + G) * Piece<T, AL>::bytes(rows)};
+  }
+  constexpr int W = FwdShape<T>::W, rows = W * FwdShape<T>::RUN;
+  return {glr_fwd_kernel<T, GATE, AL>, 32 * W, rows,
+          runs_bytes(W, 1) + kBarBytes + 2 * (2 + G) * Piece<T, AL>::bytes(rows)};
 }
 template <typename T, bool AL>
 Scan scan_for(bool bwd, int gate) {
@@ -769,8 +819,8 @@ cudaLaunchConfig_t scan_config(const Scan& k, int cluster, int groups, cudaStrea
                                cudaLaunchAttribute* attr) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)cluster, (unsigned)groups);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = (size_t)k.smem;
+  cfg.blockDim = dim3((unsigned)k.threads);
+  cfg.dynamicSmemBytes = (size_t)(k.smem + tiles_bytes(cluster));
   cfg.stream = stream;
   attr->id = cudaLaunchAttributeClusterDimension;
   attr->val.clusterDim.x = (unsigned)cluster;
@@ -825,8 +875,8 @@ int clusters_that_fit(int dev, int variant, const Scan& k, int cluster) {
   if (n != 0) return n;
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg = scan_config(k, cluster, 1, nullptr, &attr);
-  if (cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem) !=
-          cudaSuccess ||
+  if (cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           k.smem + tiles_bytes(kMaxCluster)) != cudaSuccess ||
       cudaOccupancyMaxActiveClusters(&n, k.kernel, &cfg) != cudaSuccess || n < 1)
     return 0;
   slot.store(n, std::memory_order_relaxed);
@@ -853,10 +903,15 @@ gdn_status launch_scan(const GlrArgs& a, bool bwd, cudaStream_t stream) {
   ScanMaps maps = {};
   if (al && a.total_T > 0) {
     // (the order in which the kernels number their tensors)
-    const void* src[4] = {a.x, a.log_alpha, bwd ? a.dy : a.beta, a.beta};
-    const int n = 2 + (bwd ? 1 : 0) + (a.gate == kGateBeta ? 1 : 0);
-    for (int i = 0; i < n; ++i)
-      if (!encode_map(&maps.m[i], a, src[i], k.rows)) return GDN_ERR_CUDA;
+    const bool beta = a.gate == kGateBeta;
+    const void* in[4] = {a.x, a.log_alpha, beta ? a.beta : a.dy, a.dy};
+    const void* out[3] = {bwd ? a.dx : a.y, a.dlog_alpha, a.dbeta};
+    const int n_in = 2 + (beta ? 1 : 0) + (bwd ? 1 : 0);
+    const int n_out = bwd ? n_in - 1 : a.y != nullptr ? 1 : 0;
+    for (int i = 0; i < n_in; ++i)
+      if (!encode_map(&maps.in[i], a, in[i], k.rows)) return GDN_ERR_CUDA;
+    for (int i = 0; i < n_out; ++i)
+      if (!encode_map(&maps.out[i], a, out[i], k.rows)) return GDN_ERR_CUDA;
   }
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg = scan_config(k, cluster, groups, stream, &attr);

@@ -373,6 +373,10 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t saddr) {
 __device__ __forceinline__ void named_sync(uint32_t id, uint32_t nthreads) {
   asm volatile("barrier.sync.aligned %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
+// Arrive on a named barrier without waiting (others wait with named_sync).
+__device__ __forceinline__ void named_arrive(uint32_t id, uint32_t nthreads) {
+  asm volatile("barrier.arrive.aligned %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
 // Arrive once on a local mbarrier (release at CTA scope).
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -412,6 +416,13 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int 
       "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
       "l"(tmap), "r"(x), "r"(y), "r"(smem_u32(bar))
       : "memory");
+}
+// Tiled 2-D tensor store of one box from this CTA's shared memory (parts
+// outside the tensor are not written), in a bulk group of the issuing thread.
+__device__ __forceinline__ void tma_store_2d(const void* tmap, int x, int y, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
+               ::"l"(tmap), "r"(x), "r"(y), "r"(src)
+               : "memory");
 }
 // Prefetch a 3-D tile into L2 (no shared-memory destination, nothing to wait for).
 __device__ __forceinline__ void tma_prefetch_3d(const void* tmap, int x, int y, int z) {
