@@ -42,7 +42,7 @@ namespace gdn {
 namespace {
 
 constexpr int kChan = 64;  // channels of a CTA
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 8;  // the portable limit
 constexpr uint32_t kWait = 1u << 24;  // polls of a bounded wait
 
 enum : int { kGateNone = GDN_GLR_GATE_NONE, kGateBeta = GDN_GLR_GATE_BETA,
@@ -51,14 +51,20 @@ enum : int { kGateNone = GDN_GLR_GATE_NONE, kGateBeta = GDN_GLR_GATE_BETA,
 using f2 = float2;  // two channels of a lane
 
 __device__ __forceinline__ f2 both(float v) { return make_float2(v, v); }
+// (one packed instruction for both channels, each rounded as by itself)
+__device__ __forceinline__ f2 unpacked(uint64_t v) {
+  f2 r;
+  f2_unpack(v, r.x, r.y);
+  return r;
+}
 __device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-  return make_float2(__fmul_rn(a.x, b.x), __fmul_rn(a.y, b.y));
+  return unpacked(f2_mul(f2_pack(a.x, a.y), f2_pack(b.x, b.y)));
 }
 __device__ __forceinline__ f2 add2(f2 a, f2 b) {
-  return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
+  return unpacked(f2_add(f2_pack(a.x, a.y), f2_pack(b.x, b.y)));
 }
 __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-  return make_float2(__fmaf_rn(a.x, b.x, c.x), __fmaf_rn(a.y, b.y, c.y));
+  return unpacked(f2_fma(f2_pack(a.x, a.y), f2_pack(b.x, b.y), f2_pack(c.x, c.y)));
 }
 
 // a = exp(l) and 1 - a.  Channels that remember a thousand tokens have a
@@ -70,20 +76,20 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
 // its ends, falling with l^2 towards 0.  Further out the hardware 2^x, good to
 // 2^-22, serves, since such a channel forgets within a few tokens.
 template <int GATE>
-__device__ __forceinline__ void decay1(float l, float& a, float& one_minus_a) {
-  float q = __fmaf_rn(l, 0.008352220989763737f, 0.04174217954277992f);
-  q = __fmaf_rn(l, q, 0.16666626930236816f);
-  q = __fmaf_rn(l, q, 0.5f);
-  q = __fmaf_rn(l, q, 1.f);
-  const float e = sm100::ex2_approx(__fmul_rn(l, 1.4426950408889634f));
-  const bool near = fabsf(l) < 0.25f;
-  a = near ? __fmaf_rn(l, q, 1.f) : e;
-  if (GATE == kGateComp) one_minus_a = near ? __fmul_rn(-l, q) : __fadd_rn(1.f, -e);
-}
-template <int GATE>
 __device__ __forceinline__ void decay2(f2 l, f2& a, f2& one_minus_a) {
-  decay1<GATE>(l.x, a.x, one_minus_a.x);
-  decay1<GATE>(l.y, a.y, one_minus_a.y);
+  f2 q = fma2(l, both(0.008352220989763737f), both(0.04174217954277992f));
+  q = fma2(l, q, both(0.16666626930236816f));
+  q = fma2(l, q, both(0.5f));
+  q = fma2(l, q, both(1.f));
+  const f2 n = fma2(l, q, both(1.f)), z = mul2(l, both(1.4426950408889634f));
+  const float e0 = sm100::ex2_approx(z.x), e1 = sm100::ex2_approx(z.y);
+  const bool near0 = fabsf(l.x) < 0.25f, near1 = fabsf(l.y) < 0.25f;
+  a = make_float2(near0 ? n.x : e0, near1 ? n.y : e1);
+  if (GATE == kGateComp) {
+    const f2 lq = mul2(l, q);
+    one_minus_a = make_float2(near0 ? -lq.x : __fadd_rn(1.f, -e0),
+                              near1 ? -lq.y : __fadd_rn(1.f, -e1));
+  }
 }
 
 // The input b x of two channels.
@@ -147,10 +153,13 @@ struct __align__(16) Run {
   f2 A, h;
 };
 
-// h behind a run that is entered with h.  A run whose A is 0 forgets what was
-// before it, even an infinity or NaN: those belong to another sequence.
+// h behind a run that is entered with h.  CUT (a packed batch): a run whose A is
+// 0 forgets what was before it, even an infinity or NaN: those belong to
+// another sequence.
+template <bool CUT>
 __device__ __forceinline__ f2 through(const Run& r, f2 h) {
   const f2 n = fma2(r.A, h, r.h);
+  if (!CUT) return n;
   return make_float2(r.A.x == 0.f ? r.h.x : n.x, r.A.y == 0.f ? r.h.y : n.y);
 }
 
@@ -320,7 +329,7 @@ __device__ __forceinline__ void send_run(uint32_t addr, uint32_t bar, const Run&
 
 // The runs of a tile's warps, in order or backwards: what lies before this
 // warp's run, and the whole.
-template <int W, bool BACK>
+template <int W, bool BACK, bool CUT>
 __device__ __forceinline__ void fold_tile(const Run (*runs)[32], int lane, int warp, Run& before,
                                           Run& all) {
   all.A = both(1.f);
@@ -330,7 +339,7 @@ __device__ __forceinline__ void fold_tile(const Run (*runs)[32], int lane, int w
     const int w = BACK ? W - 1 - k : k;
     if (w == warp) before = all;
     const Run r = runs[w][lane];
-    all.h = through(r, all.h);
+    all.h = through<CUT>(r, all.h);
     all.A = mul2(all.A, r.A);
   }
 }
@@ -367,6 +376,7 @@ struct Exchange {
   }
   // Waits for the step's runs; h: the carry before this CTA's tile; carry
   // moves on past the whole step.
+  template <bool CUT>
   __device__ __forceinline__ f2 receive(int64_t step, int lane, f2& carry) {
     const int b = (int)(step & 1);
     // (a thread that gave up never waits again, but still sends every step)
@@ -375,9 +385,19 @@ struct Exchange {
 #pragma unroll 4
     for (int r = 0; r < n_cta; ++r) {
       if (r == rank) h = carry;
-      carry = through(tiles[b * n_cta + r][lane], carry);
+      carry = through<CUT>(tiles[b * n_cta + r][lane], carry);
     }
     return h;
+  }
+  // The tile's runs, as one to the cluster and, through the others' in return,
+  // h before this warp's run.
+  template <int W, bool BACK, bool CUT>
+  __device__ __forceinline__ f2 before(int64_t step, int lane, int warp, const Run (*runs)[32],
+                                       f2& carry) {
+    Run b, all;
+    fold_tile<W, BACK, CUT>(runs, lane, warp, b, all);
+    send<W>(step, lane, warp, all);
+    return through<CUT>(b, receive<CUT>(step, lane, carry));
   }
 };
 
@@ -404,13 +424,11 @@ __device__ __forceinline__ void empty_sequences(const GlrArgs& p, const float* i
   }
 }
 
-// Warps of a CTA and tokens of a thread's run.  The forward holds a and b x of
-// its run in registers (4 a token); more, smaller CTAs spread evenly over the
-// SMs.  The backward starts each tile from a checkpoint.
+// Tokens of a thread's run and warps of a CTA.  The forward holds a and b x of
+// its run in registers (4 a token) and comes with 4 and with 8 warps; the
+// backward starts each tile from a checkpoint.
 template <typename T>
-struct FwdShape {
-  static constexpr int W = 4, RUN = sizeof(T) == 2 ? 16 : 8;
-};
+constexpr int fwd_run() { return sizeof(T) == 2 ? 16 : 8; }
 struct BwdShape {
   static constexpr int W = 8, RUN = 8;
 };
@@ -423,10 +441,10 @@ constexpr int tiles_bytes(int cluster) { return 2 * cluster * 32 * (int)sizeof(R
 constexpr int kBarBytes = 128;
 static_assert(runs_bytes(1, 1) % 128 == 0 && tiles_bytes(1) % 128 == 0, "stages on 128 bytes");
 
-template <typename T, int GATE, bool AL>
-__global__ void __launch_bounds__(32 * FwdShape<T>::W, 16 / FwdShape<T>::W)
+template <typename T, int GATE, bool AL, int W>
+__global__ void __launch_bounds__(32 * W, 16 / W)
     glr_fwd_kernel(const GlrArgs p, const __grid_constant__ ScanMaps maps) {
-  constexpr int RUN = FwdShape<T>::RUN, W = FwdShape<T>::W, ROWS = W * RUN;
+  constexpr int RUN = fwd_run<T>(), ROWS = W * RUN;
   constexpr int N = GATE == kGateBeta ? 3 : 2;
   using P = Piece<T, AL>;
   extern __shared__ __align__(128) char smem[];
@@ -511,10 +529,9 @@ __global__ void __launch_bounds__(32 * FwdShape<T>::W, 16 / FwdShape<T>::W)
     runs[warp][lane] = run;
     __syncthreads();  // the runs are complete; the step before is done with its stage
     if (step > 0) load(step + 1);
-    Run before, all;
-    fold_tile<W, false>(runs, lane, warp, before, all);
-    ex.template send<W>(step, lane, warp, all);
-    f2 h = through(before, ex.receive(step, lane, carry));
+    f2 h = p.cu_seqlens == nullptr
+               ? ex.template before<W, false, false>(step, lane, warp, runs, carry)
+               : ex.template before<W, false, true>(step, lane, warp, runs, carry);
     if (p.checkpoints != nullptr && t0 % kGlrTile == 0 && t0 < T_)
       ch.put(p.checkpoints, t0 / kGlrTile, C, h);
     if (p.y == nullptr) continue;
@@ -676,11 +693,14 @@ __global__ void __launch_bounds__(32 * BwdShape::W, 16 / BwdShape::W)
     rev_runs[warp][lane] = rr;
     __syncthreads();  // the runs are complete; the step before is done with its stage
     if (step > 0) load(step + 1);
-    Run behind, all;
-    fold_tile<W, true>(rev_runs, lane, warp, behind, all);
-    ex.template send<W>(step, lane, warp, all);
-    for (int w = 0; w < warp; ++w) h = through(fwd_runs[w][lane], h);  // before this run
-    f2 e = through(behind, ex.receive(step, lane, carry));
+    f2 e;
+    if (p.cu_seqlens == nullptr) {
+      e = ex.template before<W, true, false>(step, lane, warp, rev_runs, carry);
+      for (int w = 0; w < warp; ++w) h = through<false>(fwd_runs[w][lane], h);
+    } else {
+      e = ex.template before<W, true, true>(step, lane, warp, rev_runs, carry);
+      for (int w = 0; w < warp; ++w) h = through<true>(fwd_runs[w][lane], h);
+    }
     // Token i's gradients, from its x, h_{t-1} (hb), dh, e and b's parts.
     const int64_t o0 = tile * ROWS * row_bytes;
     auto out = [&](int i, f2 dh, f2 hb, f2 om_i) {
@@ -796,23 +816,33 @@ struct Scan {
   int threads, rows, smem;
 };
 
+enum : int { kFwd8 = 0, kFwd4 = 1, kBwd = 2 };
+
+template <typename T, bool AL, int GATE, int W>
+Scan fwd_scan() {
+  constexpr int rows = W * fwd_run<T>(), n = GATE == kGateBeta ? 3 : 2;
+  return {glr_fwd_kernel<T, GATE, AL, W>, 32 * W, rows,
+          runs_bytes(W, 1) + kBarBytes + 2 * n * Piece<T, AL>::bytes(rows)};
+}
 template <typename T, bool AL, int GATE>
-Scan scan_of(bool bwd) {
-  constexpr int G = GATE == kGateBeta ? 1 : 0;
-  if (bwd) {
-    constexpr int W = BwdShape::W, rows = W * BwdShape::RUN;
-    return {glr_bwd_kernel<T, GATE, AL>, 32 * W, rows,
-            runs_bytes(W, 2) + kBarBytes + 2 * (3 + G) * Piece<T, AL>::bytes(rows)};
-  }
-  constexpr int W = FwdShape<T>::W, rows = W * FwdShape<T>::RUN;
-  return {glr_fwd_kernel<T, GATE, AL>, 32 * W, rows,
-          runs_bytes(W, 1) + kBarBytes + 2 * (2 + G) * Piece<T, AL>::bytes(rows)};
+Scan scan_of(int what) {
+  if (what == kFwd8) return fwd_scan<T, AL, GATE, 8>();
+  if (what == kFwd4) return fwd_scan<T, AL, GATE, 4>();
+  constexpr int W = BwdShape::W, rows = W * BwdShape::RUN, n = GATE == kGateBeta ? 4 : 3;
+  return {glr_bwd_kernel<T, GATE, AL>, 32 * W, rows,
+          runs_bytes(W, 2) + kBarBytes + 2 * n * Piece<T, AL>::bytes(rows)};
 }
 template <typename T, bool AL>
-Scan scan_for(bool bwd, int gate) {
-  return gate == kGateNone   ? scan_of<T, AL, kGateNone>(bwd)
-         : gate == kGateBeta ? scan_of<T, AL, kGateBeta>(bwd)
-                             : scan_of<T, AL, kGateComp>(bwd);
+Scan scan_gate(int what, int gate) {
+  return gate == kGateNone   ? scan_of<T, AL, kGateNone>(what)
+         : gate == kGateBeta ? scan_of<T, AL, kGateBeta>(what)
+                             : scan_of<T, AL, kGateComp>(what);
+}
+Scan scan_for(const GlrArgs& a, bool al, int what) {
+  if (a.dtype == GDN_BF16)
+    return al ? scan_gate<__nv_bfloat16, true>(what, a.gate)
+              : scan_gate<__nv_bfloat16, false>(what, a.gate);
+  return al ? scan_gate<float, true>(what, a.gate) : scan_gate<float, false>(what, a.gate);
 }
 
 cudaLaunchConfig_t scan_config(const Scan& k, int cluster, int groups, cudaStream_t stream,
@@ -863,11 +893,13 @@ bool encode_map(CUtensorMap* m, const GlrArgs& a, const void* base, int rows) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Clusters of each size that the device holds at once, per kernel (asked once
-// per device; the answers are the same whoever asks, so threads may race).
+// Clusters of each size that the device holds at once, per kernel, and its SMs
+// (asked once per device; the answers are the same whoever asks, so threads may
+// race).  -1: none of that size.
 constexpr int kMaxDevices = 64;
-constexpr int kVariants = 2 * 2 * 2 * 3;
+constexpr int kVariants = 2 * 2 * 3 * 3;
 std::atomic<int> g_fit[kMaxDevices][kVariants][kMaxCluster + 1];
+std::atomic<int> g_sms[kMaxDevices];
 
 int clusters_that_fit(int dev, int variant, const Scan& k, int cluster) {
   std::atomic<int>& slot = g_fit[dev][variant][cluster];
@@ -877,29 +909,72 @@ int clusters_that_fit(int dev, int variant, const Scan& k, int cluster) {
   const cudaLaunchConfig_t cfg = scan_config(k, cluster, 1, nullptr, &attr);
   if (cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            k.smem + tiles_bytes(kMaxCluster)) != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, k.kernel, &cfg) != cudaSuccess || n < 1)
-    return 0;
+      cudaFuncSetAttribute(k.kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+          cudaSuccess)
+    return -1;
+  if (cudaOccupancyMaxActiveClusters(&n, k.kernel, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();  // (a size that the device cannot hold)
+    n = -1;
+  }
   slot.store(n, std::memory_order_relaxed);
   return n;
+}
+
+// How a scan is cut: its kernel and cluster size, by the least estimated time.
+//   steps of a cluster  x  waves of clusters  x  a step's time,
+// the latter by how many CTAs share an SM.  Measured on a B200 (bf16, gate
+// beta, us a step): 8 warps 2.1 alone and 2.85 by twos, 4 warps (half the
+// tokens) 1.46, 1.87, 2.26 and 2.6; a further wave costs about a tenth.  What
+// this settles, C = 6144, T = 32768, forward: 8 warps in clusters of 2 (one
+// wave, a third of the SMs with two CTAs) 336 us, of 8 (three waves) 311, 4
+// warps in clusters of 4 289; C = 2560, T = 65536: 8 warps in clusters of 6
+// 250, 4 warps in clusters of 8 282; backward, C = 6144, T = 32768: clusters
+// of 2 641, of 5 (two waves) 569.
+struct Choice {
+  Scan scan;
+  int cluster;  // 0: none
+  double cost;
+};
+
+Choice choose(int dev, int sms, const GlrArgs& a, bool al, int what, int groups) {
+  static const double kStep8[] = {2.1, 2.85}, kStep4[] = {1.46, 1.87, 2.26, 2.6};
+  const Scan k = scan_for(a, al, what);
+  const int variant = (((a.dtype == GDN_BF16 ? 0 : 1) * 2 + (al ? 0 : 1)) * 3 + what) * 3 + a.gate;
+  const int64_t n_tiles = (a.total_T + k.rows - 1) / k.rows;
+  const int most = (int)(n_tiles < kMaxCluster ? (n_tiles < 1 ? 1 : n_tiles) : kMaxCluster);
+  Choice best = {k, 0, 0.0};
+  for (int r = 1; r <= most; ++r) {
+    const int fit = clusters_that_fit(dev, variant, k, r);
+    if (fit < 1) continue;
+    const int at_once = fit < groups ? fit : groups, waves = (groups + fit - 1) / fit;
+    int share = (at_once * r + sms - 1) / sms;
+    if (share > (what == kFwd4 ? 4 : 2)) share = what == kFwd4 ? 4 : 2;
+    const double cost = (double)((n_tiles + r - 1) / r) * waves * (1.0 + 0.1 * (waves - 1)) *
+                        (what == kFwd4 ? kStep4 : kStep8)[share - 1];
+    if (best.cluster == 0 || cost <= best.cost) best = {k, r, cost};
+  }
+  return best;
 }
 
 gdn_status launch_scan(const GlrArgs& a, bool bwd, cudaStream_t stream) {
   const bool bf16 = a.dtype == GDN_BF16;
   const bool al = (int64_t)a.C * (bf16 ? 2 : 4) % 16 == 0;
-  const Scan k = bf16 ? (al ? scan_for<__nv_bfloat16, true>(bwd, a.gate)
-                            : scan_for<__nv_bfloat16, false>(bwd, a.gate))
-                      : (al ? scan_for<float, true>(bwd, a.gate)
-                            : scan_for<float, false>(bwd, a.gate));
-  const int variant = ((bf16 ? 0 : 1) * 2 + (al ? 0 : 1)) * 6 + (bwd ? 3 : 0) + a.gate;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return GDN_ERR_CUDA;
+  int sms = g_sms[dev].load(std::memory_order_relaxed);
+  if (sms == 0) {
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return GDN_ERR_CUDA;
+    g_sms[dev].store(sms, std::memory_order_relaxed);
+  }
   const int groups = (a.C + kChan - 1) / kChan;
-  // The largest cluster (consecutive tiles in flight per channel group) at
-  // which all groups' clusters are on the device at once.
-  const int64_t n_tiles = (a.total_T + k.rows - 1) / k.rows;
-  int cluster = (int)(n_tiles < kMaxCluster ? (n_tiles < 1 ? 1 : n_tiles) : kMaxCluster);
-  while (cluster > 1 && clusters_that_fit(dev, variant, k, cluster) < groups) --cluster;
-  if (clusters_that_fit(dev, variant, k, cluster) < 1) return GDN_ERR_CUDA;
+  Choice c = choose(dev, sms, a, al, bwd ? kBwd : kFwd8, groups);
+  if (!bwd) {
+    const Choice small = choose(dev, sms, a, al, kFwd4, groups);
+    if (small.cluster != 0 && (c.cluster == 0 || small.cost < c.cost)) c = small;
+  }
+  if (c.cluster == 0) return GDN_ERR_CUDA;
+  const Scan& k = c.scan;
   ScanMaps maps = {};
   if (al && a.total_T > 0) {
     // (the order in which the kernels number their tensors)
@@ -914,7 +989,7 @@ gdn_status launch_scan(const GlrArgs& a, bool bwd, cudaStream_t stream) {
       if (!encode_map(&maps.out[i], a, out[i], k.rows)) return GDN_ERR_CUDA;
   }
   cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = scan_config(k, cluster, groups, stream, &attr);
+  const cudaLaunchConfig_t cfg = scan_config(k, c.cluster, groups, stream, &attr);
   return cudaLaunchKernelEx(&cfg, k.kernel, a, maps) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
