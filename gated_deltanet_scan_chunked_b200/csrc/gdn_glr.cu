@@ -27,9 +27,10 @@
 // asynchronous copies, one more than it needs, and read from its remainder on;
 // outputs are stored from registers.
 //
-// Runs in which a sequence begins or ends take a path of their own, in rolled
-// loops that form a_t and b_t x_t again from the stage: few runs do, and
-// unrolled it would fill the instruction cache for all.
+// Runs in which a sequence begins or ends take a path of their own behind the
+// common one: for each such token, in a loop over the marks, the states of
+// its sequence are fetched and added at that token (its index known only at run
+// time: a select over the run), then the run is folded again with its cuts.
 #include <cuda.h>
 
 #include <atomic>
@@ -147,6 +148,22 @@ struct Marks {
     return __shfl_sync(0xffffffffu, seq, i);
   }
 };
+
+// Value k (known at run time) of a run held in registers, and its replacement.
+template <int RUN>
+__device__ __forceinline__ f2 pick(const f2 (&v)[RUN], int k) {
+  f2 r = v[0];
+#pragma unroll
+  for (int i = 1; i < RUN; ++i)
+    if (i == k) r = v[i];
+  return r;
+}
+template <int RUN>
+__device__ __forceinline__ void replace(f2 (&v)[RUN], int k, f2 x) {
+#pragma unroll
+  for (int i = 0; i < RUN; ++i)
+    if (i == k) v[i] = x;
+}
 
 // A composed run, two channels.
 struct __align__(16) Run {
@@ -494,34 +511,28 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
       return P::get(st + k * stages.kTensor + i * P::kPitch,
                     AL ? 0 : (int)((rem + (uint32_t)i * row_bytes) & 15u), lane);
     };
-    auto form = [&](int i, f2& a, f2& u) {  // a_t and b_t x_t
-      f2 q;
-      decay2<GATE>(in(1, i), a, q);
-      u = gated<GATE>(in(0, i), GATE == kGateBeta ? in(N - 1, i) : both(0.f), q);
-    };
     f2 a[RUN], u[RUN];
     Run run;
     run.A = both(1.f);
     run.h = both(0.f);
-    if (inside) {
 #pragma unroll
-      for (int i = 0; i < RUN; ++i) {
-        form(i, a[i], u[i]);
-        run.A = mul2(run.A, a[i]);
-        run.h = fma2(a[i], run.h, u[i]);
+    for (int i = 0; i < RUN; ++i) {
+      f2 q;
+      decay2<GATE>(in(1, i), a[i], q);
+      u[i] = gated<GATE>(in(0, i), GATE == kGateBeta ? in(N - 1, i) : both(0.f), q);
+      run.A = mul2(run.A, a[i]);
+      run.h = fma2(a[i], run.h, u[i]);
+    }
+    if (m.first != 0) {  // h_0 joins at first tokens, which forget what was before them
+      for (uint32_t f = m.first; f != 0; f &= f - 1) {
+        const int k = __ffs((int)f) - 1;
+        const f2 h0 = ch.get(p.initial_state, m.seq_of(k), C);
+        replace(u, k, fma2(pick(a, k), h0, pick(u, k)));
       }
-    } else {
-#pragma unroll 1
-      for (int i = 0; i < RUN; ++i) {
-        const int s = m.seq_of(i);
-        f2 ai, ui;
-        form(i, ai, ui);
-        if (m.first >> i & 1) run.h = ch.get(p.initial_state, s, C);
-        run.A = mul2(run.A, ai);
-        run.h = fma2(ai, run.h, ui);
-      }
-      // (a run with a first token forgets what was before, whatever its a are)
-      if (m.first != 0) run.A = both(0.f);
+      run.A = both(0.f);
+#pragma unroll
+      for (int i = 0; i < RUN; ++i)
+        run.h = (m.first >> i & 1) ? u[i] : fma2(a[i], run.h, u[i]);
     }
     // (two buffers: a warp may still fold this step's runs when others write
     // the next one's)
@@ -550,16 +561,17 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
         out(i);
       }
     } else {
-#pragma unroll 1
+#pragma unroll
       for (int i = 0; i < RUN; ++i) {
-        const int s = m.seq_of(i);
-        f2 ai, ui;
-        form(i, ai, ui);
-        if (m.first >> i & 1) h = ch.get(p.initial_state, s, C);
-        h = fma2(ai, h, ui);
+        h = (m.first >> i & 1) ? u[i] : fma2(a[i], h, u[i]);
+        u[i] = h;
         out(i);
-        if ((m.last >> i & 1) && p.final_state != nullptr) ch.put(p.final_state, s, C, h);
       }
+      if (p.final_state != nullptr)
+        for (uint32_t f = m.last; f != 0; f &= f - 1) {
+          const int k = __ffs((int)f) - 1;
+          ch.put(p.final_state, m.seq_of(k), C, pick(u, k));
+        }
     }
     if (AL && tile0 < T_) stages.store(step, 1, maps, tile0, cb);
   }
@@ -640,52 +652,50 @@ __global__ void __launch_bounds__(32 * BwdShape::W, 16 / BwdShape::W)
       return P::get(st + k * stages.kTensor + i * P::kPitch,
                     AL ? 0 : (int)((rem + (uint32_t)i * row_bytes) & 15u), lane);
     };
-    auto form = [&](int i, f2& a, f2& u, f2& om) {  // a_t, b_t x_t, 1 - a_t
-      decay2<GATE>(in(1, i), a, om);
-      u = gated<GATE>(in(0, i), GATE == kGateBeta ? in(kBeta, i) : both(0.f), om);
+    // dy of the run; dh_T joins at its sequence's last token
+    auto all_dy = [&](f2(&d)[RUN]) {
+#pragma unroll
+      for (int i = 0; i < RUN; ++i) d[i] = in(kDy, i);
+      if (p.d_final_state != nullptr)
+        for (uint32_t f = m.last; f != 0; f &= f - 1) {
+          const int k = __ffs((int)f) - 1;
+          replace(d, k, add2(pick(d, k), ch.get(p.d_final_state, m.seq_of(k), C)));
+        }
     };
-    // dy, to which dh_T joins at its sequence's last token
-    auto dy_at = [&](int i, int s) {
-      const f2 d = in(kDy, i);
-      return (m.last >> i & 1) && p.d_final_state != nullptr
-                 ? add2(d, ch.get(p.d_final_state, s, C))
-                 : d;
-    };
-    f2 a[RUN], u[RUN], om[RUN];
+    f2 a[RUN], u[RUN], om[RUN];  // om: 1 - a
     Run fr, rr;
     fr.A = rr.A = both(1.f);
     fr.h = rr.h = both(0.f);
-    if (inside) {
 #pragma unroll
-      for (int i = 0; i < RUN; ++i) {
-        form(i, a[i], u[i], om[i]);
-        fr.A = mul2(fr.A, a[i]);
-        fr.h = fma2(a[i], fr.h, u[i]);
-      }
-      rr.A = fr.A;
+    for (int i = 0; i < RUN; ++i) {
+      decay2<GATE>(in(1, i), a[i], om[i]);
+      u[i] = gated<GATE>(in(0, i), GATE == kGateBeta ? in(kBeta, i) : both(0.f), om[i]);
+      fr.A = mul2(fr.A, a[i]);
+      fr.h = fma2(a[i], fr.h, u[i]);
+    }
+    rr.A = fr.A;
+    if (inside) {
 #pragma unroll
       for (int i = RUN - 1; i >= 0; --i) rr.h = mul2(a[i], add2(in(kDy, i), rr.h));
     } else {
-      f2 ai, ui, oi;
-#pragma unroll 1
-      for (int i = 0; i < RUN; ++i) {
-        const int s = m.seq_of(i);
-        form(i, ai, ui, oi);
-        if (m.first >> i & 1) fr.h = ch.get(p.initial_state, s, C);
-        fr.A = mul2(fr.A, ai);
-        fr.h = fma2(ai, fr.h, ui);
-      }
-      rr.A = fr.A;
-#pragma unroll 1
-      for (int i = RUN - 1; i >= 0; --i) {
-        const int s = m.seq_of(i);
-        form(i, ai, ui, oi);
-        if (m.last >> i & 1) rr.h = both(0.f);
-        rr.h = mul2(ai, add2(dy_at(i, s), rr.h));
-      }
       // (a run cut by a sequence's end forgets what is beyond it)
-      if (m.first != 0) fr.A = both(0.f);
+      f2 d[RUN];
+      all_dy(d);
+#pragma unroll
+      for (int i = RUN - 1; i >= 0; --i)
+        rr.h = mul2(a[i], (m.last >> i & 1) ? d[i] : add2(d[i], rr.h));
       if (m.last != 0) rr.A = both(0.f);
+      if (m.first != 0) {  // as in the forward
+        for (uint32_t f = m.first; f != 0; f &= f - 1) {
+          const int k = __ffs((int)f) - 1;
+          const f2 h0 = ch.get(p.initial_state, m.seq_of(k), C);
+          replace(u, k, fma2(pick(a, k), h0, pick(u, k)));
+        }
+        fr.A = both(0.f);
+#pragma unroll
+        for (int i = 0; i < RUN; ++i)
+          fr.h = (m.first >> i & 1) ? u[i] : fma2(a[i], fr.h, u[i]);
+      }
     }
     Run(*fwd_runs)[32] = run_buf + (int)(step & 1) * 2 * W;  // (two buffers: see the forward)
     Run(*rev_runs)[32] = fwd_runs + W;
@@ -734,26 +744,29 @@ __global__ void __launch_bounds__(32 * BwdShape::W, 16 / BwdShape::W)
         out(i, dh, u[i], om[i]);
       }
     } else {
-      f2 before[RUN], ai, ui, oi;  // (indexed: in local memory)
-#pragma unroll 1
+#pragma unroll
       for (int i = 0; i < RUN; ++i) {
-        const int s = m.seq_of(i);
-        form(i, ai, ui, oi);
-        if (m.first >> i & 1) h = ch.get(p.initial_state, s, C);
-        before[i] = h;
-        h = fma2(ai, h, ui);
+        const f2 next = (m.first >> i & 1) ? u[i] : fma2(a[i], h, u[i]);
+        u[i] = h;
+        h = next;
       }
-#pragma unroll 1
+      for (uint32_t f = m.first; f != 0; f &= f - 1) {  // before a first token: h_0
+        const int k = __ffs((int)f) - 1;
+        replace(u, k, ch.get(p.initial_state, m.seq_of(k), C));
+      }
+      f2 d[RUN];
+      all_dy(d);
+#pragma unroll
       for (int i = RUN - 1; i >= 0; --i) {
-        const int s = m.seq_of(i);
-        form(i, ai, ui, oi);
-        f2 dh = dy_at(i, s);
-        if (!(m.last >> i & 1)) dh = add2(dh, e);
-        e = mul2(ai, dh);
-        out(i, dh, before[i], oi);
-        if ((m.first >> i & 1) && p.d_initial_state != nullptr)
-          ch.put(p.d_initial_state, s, C, e);
+        const f2 dh = (m.last >> i & 1) ? d[i] : add2(d[i], e);
+        d[i] = e = mul2(a[i], dh);
+        out(i, dh, u[i], om[i]);
       }
+      if (p.d_initial_state != nullptr)
+        for (uint32_t f = m.first; f != 0; f &= f - 1) {
+          const int k = __ffs((int)f) - 1;
+          ch.put(p.d_initial_state, m.seq_of(k), C, pick(d, k));
+        }
     }
     if (AL && tile >= 0) stages.store(step, N - 1, maps, tile * ROWS, cb);
   }
