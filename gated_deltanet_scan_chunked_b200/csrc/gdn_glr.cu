@@ -290,17 +290,36 @@ struct Stages {
           sm100::tma_load_2d(stage + k * kTensor, &maps.in[k], cb, (int)t0, bar);
       }
     } else if (any) {
-      const int64_t row_bytes = (int64_t)C * (int)sizeof(T), all = total_T * row_bytes;
-      for (int i = threadIdx.x; i < ROWS * P::kCopies; i += THREADS) {
-        const int r = i / P::kCopies, q = i % P::kCopies;
-        const int64_t t = t0 + r;
-        int64_t off = ((t * row_bytes + (int64_t)cb * (int)sizeof(T)) & ~(int64_t)15) + 16 * q;
-        int n = 0;
-        if (t >= 0 && t < total_T) n = all - off >= 16 ? 16 : all - off > 0 ? (int)(all - off) : 0;
-        if (n == 0) off = 0;
+      // a thread has one 16-byte column of every kRows-th row
+      constexpr int kRows = THREADS / P::kCopies;
+      const int q = (int)threadIdx.x % P::kCopies, r0 = (int)threadIdx.x / P::kCopies;
+      if (r0 >= kRows) return;
+      const uint32_t row_bytes = (uint32_t)C * (uint32_t)sizeof(T);
+      // bytes of the tensors up to the tile, of which the last few not a
+      // multiple of 16 count with the rows
+      const int64_t before = (t0 < 0 ? 0 : t0) * (int64_t)row_bytes + (int64_t)cb * (int)sizeof(T);
+      const int64_t left = total_T * (int64_t)row_bytes - (before & ~(int64_t)15);
+      // (all of the tile's copies lie inside the tensors)
+      const bool whole =
+          t0 >= 0 && left >= (int64_t)(ROWS - 1) * row_bytes + 16 + P::kPitch;
+      const char* base[N];
 #pragma unroll
-        for (int k = 0; k < N; ++k)
-          copy16(stage + k * kTensor + r * P::kPitch + 16 * q, src[k] + off, n);
+      for (int k = 0; k < N; ++k) base[k] = src[k] + (before & ~(int64_t)15);
+      uint32_t row = (uint32_t)(before & 15) + (uint32_t)r0 * row_bytes;
+      uint32_t dst = stage + r0 * P::kPitch + 16 * q;
+#pragma unroll 4
+      for (int r = r0; r < ROWS; r += kRows) {
+        uint32_t off = (row & ~15u) + 16u * q;
+        int n = 16;
+        if (!whole) {
+          const bool in = t0 + r >= 0 && t0 + r < total_T && (int64_t)off < left;
+          n = !in ? 0 : left - off >= 16 ? 16 : (int)(left - off);
+          if (n == 0) off = 0;
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k) copy16(dst + k * kTensor, base[k] + off, n);
+        row += kRows * row_bytes;
+        dst += kRows * P::kPitch;
       }
     }
   }
