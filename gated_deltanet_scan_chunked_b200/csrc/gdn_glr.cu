@@ -43,7 +43,7 @@ namespace gdn {
 namespace {
 
 constexpr int kChan = 64;  // channels of a CTA
-constexpr int kMaxCluster = 8;  // the portable limit
+constexpr int kMaxCluster = 16;  // (more than 8: by leave of cudaFuncSetAttribute)
 constexpr uint32_t kWait = 1u << 24;  // polls of a bounded wait
 
 enum : int { kGateNone = GDN_GLR_GATE_NONE, kGateBeta = GDN_GLR_GATE_BETA,
@@ -979,7 +979,10 @@ Choice choose(int dev, int sms, const GlrArgs& a, bool al, int what, int groups)
     const int fit = clusters_that_fit(dev, variant, k, r);
     if (fit < 1) continue;
     const int at_once = fit < groups ? fit : groups, waves = (groups + fit - 1) / fit;
-    int share = (at_once * r + sms - 1) / sms;
+    // CTAs of an SM: of the `per` that it holds, the part of the clusters that
+    // fit (clusters lie within a GPC, so not all of its SMs' places are taken)
+    const int per = (clusters_that_fit(dev, variant, k, 1) + sms - 1) / sms;
+    int share = (at_once * per + fit - 1) / fit;
     if (share > (what == kFwd4 ? 4 : 2)) share = what == kFwd4 ? 4 : 2;
     const double cost = (double)((n_tiles + r - 1) / r) * waves * (1.0 + 0.1 * (waves - 1)) *
                         (what == kFwd4 ? kStep4 : kStep8)[share - 1];
