@@ -981,7 +981,7 @@ Choice choose(int dev, int sms, const GlrArgs& a, bool al, int what, int groups)
     const int at_once = fit < groups ? fit : groups, waves = (groups + fit - 1) / fit;
     // CTAs of an SM: of the `per` that it holds, the part of the clusters that
     // fit (clusters lie within a GPC, so not all of its SMs' places are taken)
-    const int per = (clusters_that_fit(dev, variant, k, 1) + sms - 1) / sms;
+    const int per = (fit * r + sms - 1) / sms;
     int share = (at_once * per + fit - 1) / fit;
     if (share > (what == kFwd4 ? 4 : 2)) share = what == kFwd4 ? 4 : 2;
     const double cost = (double)((n_tiles + r - 1) / r) * waves * (1.0 + 0.1 * (waves - 1)) *
