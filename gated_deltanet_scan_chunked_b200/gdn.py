@@ -597,78 +597,70 @@ GLR_TILE = 64  # tokens between two checkpoints
 _GATE_NONE, _GATE_BETA, _GATE_COMPLEMENT = 0, 1, 2
 
 
-class _on:
-    """The device of a call's tensors made current, and the stream that it runs
-    on: the given one, or that device's current one."""
+# These calls may be as short as a few microseconds, so the binding asks torch
+# for the device and the stream by its cheapest ways.
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+_CODES = {torch.bfloat16: GDN_BF16, torch.float32: GDN_FP32}
 
-    def __init__(self, dev, stream):
-        self._back = None
-        now = torch.cuda.current_device()
-        if dev.index != now:
-            self._back = now
-            torch.cuda.set_device(dev)
-        self.given = stream
-        if stream is None:
-            self.handle = torch.cuda.current_stream(dev).cuda_stream
-        else:
-            self.handle = stream.cuda_stream
 
-    def __enter__(self):
-        return self
+def _device_of(t: torch.Tensor, name: str) -> int:
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor (libgdn has no CPU path)" % name)
+    return t.get_device()
 
-    def __exit__(self, *exc):
-        if self._back is not None:
-            torch.cuda.set_device(self._back)
 
-    def keep(self, *tensors):
-        """Memory made here (on torch's current stream) is used on a given
-        stream: it must not go to others before that use is over."""
-        if self.given is not None:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(self.given)
+def _on(i: int, stream):
+    """Handle of the stream that a call on device i runs on: the given one, or
+    the device's current one."""
+    return _current_stream(i) if stream is None else stream.cuda_stream
+
+
+def _keep(stream, *tensors):
+    """Memory made here (on torch's current stream) is used on a given stream: it
+    must not go to others before that use is over."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
 
 
 def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _need(t: Optional[torch.Tensor], name: str, dtype, shape, dev):
-    """t (if given) is a dense CUDA tensor on dev of that type and shape."""
-    if t is None:
-        return
-    if t.device != dev or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-        _check(t, name, dtype, dev)
+def _need(t: torch.Tensor, name: str, dtype, shape, i: int):
+    """t is a dense CUDA tensor on device i of that type and shape."""
+    if not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == i):
+        _check(t, name, dtype, torch.device("cuda", i))
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
 
 
-def _glr_gate(beta):
+def _glr_inputs(x, log_alpha, beta, i):
+    """(dtype code, gate code, beta tensor) of a call on x's device i."""
+    dtype, shape = x.dtype, x.shape
+    dt = _CODES.get(dtype)
+    if dt is None:
+        raise TypeError("x must be bfloat16 or float32, got %s" % dtype)
+    if len(shape) != 2 or not x.is_contiguous():
+        raise ValueError("x must be contiguous [tokens, channels], got %s" % (tuple(shape),))
+    _need(log_alpha, "log_alpha", dtype, shape, i)
+    if beta is None:
+        return dt, _GATE_NONE, None
     if isinstance(beta, str):
         if beta != "complement":
             raise ValueError("beta must be a tensor, None or 'complement'")
-        return _GATE_COMPLEMENT, None
-    return (_GATE_NONE, None) if beta is None else (_GATE_BETA, beta)
+        return dt, _GATE_COMPLEMENT, None
+    _need(beta, "beta", dtype, shape, i)
+    return dt, _GATE_BETA, beta
 
 
-def _glr_inputs(x, log_alpha, beta):
-    """(device, dtype code, shape, gate code, beta tensor) of a call."""
-    dev = x.device
-    _check(x, "x")
-    dt = _dtype_code(x)
-    if x.dim() != 2:
-        raise ValueError("x must be [tokens, channels], got %s" % (tuple(x.shape),))
-    gate, beta = _glr_gate(beta)
-    _need(log_alpha, "log_alpha", x.dtype, x.shape, dev)
-    _need(beta, "beta", x.dtype, x.shape, dev)
-    return dev, dt, x.shape, gate, beta
-
-
-def _glr_sequences(cu_seqlens, dev):
+def _glr_sequences(cu_seqlens, i):
     if cu_seqlens is None:
         return 1
-    _check(cu_seqlens, "cu_seqlens", torch.int32, dev)
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
         raise ValueError("cu_seqlens must be [n_seq + 1]")
+    _need(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, i)
     return cu_seqlens.shape[0] - 1
 
 
@@ -691,29 +683,34 @@ def gdn_glr_fwd(x, log_alpha, beta=None, initial_state=None, cu_seqlens=None, y=
     glr_checkpoint_shape(T, C) fp32, for gdn_glr_bwd.
     """
     lib = _lib or load()
-    dev, dt, shape, gate, beta = _glr_inputs(x, log_alpha, beta)
-    T, C = shape
-    n_seq = _glr_sequences(cu_seqlens, dev)
-    with _on(dev, stream) as on:
-        _need(initial_state, "initial_state", torch.float32, (n_seq, C), dev)
-        if y is None:
-            y = torch.empty_like(x)
-            on.keep(y)
-        else:
-            _need(y, "y", x.dtype, shape, dev)
-        if final_state is not None:
-            _need(final_state, "final_state", torch.float32, (n_seq, C), dev)
-        elif output_final_state:
-            final_state = torch.empty((n_seq, C), dtype=torch.float32, device=dev)
-            on.keep(final_state)
-        if checkpoints is True:
-            checkpoints = torch.empty(glr_checkpoint_shape(T, C), dtype=torch.float32, device=dev)
-            on.keep(checkpoints)
-        else:
-            _need(checkpoints, "checkpoints", torch.float32, glr_checkpoint_shape(T, C), dev)
-        st = lib.gdn_glr_fwd(_addr(x), _addr(log_alpha), _addr(beta), gate, _addr(initial_state),
-                             _addr(cu_seqlens), n_seq, T, C, dt, _addr(y), _addr(final_state),
-                             _addr(checkpoints), on.handle)
+    i = _device_of(x, "x")
+    if i != _current_device():
+        with torch.cuda.device(i):
+            return gdn_glr_fwd(x, log_alpha, beta, initial_state, cu_seqlens, y, final_state,
+                               output_final_state, checkpoints, stream)
+    dt, gate, beta = _glr_inputs(x, log_alpha, beta, i)
+    T, C = x.shape
+    n_seq = _glr_sequences(cu_seqlens, i)
+    if initial_state is not None:
+        _need(initial_state, "initial_state", torch.float32, (n_seq, C), i)
+    if y is None:
+        y = torch.empty_like(x)
+        _keep(stream, y)
+    else:
+        _need(y, "y", x.dtype, x.shape, i)
+    if final_state is not None:
+        _need(final_state, "final_state", torch.float32, (n_seq, C), i)
+    elif output_final_state:
+        final_state = x.new_empty((n_seq, C), dtype=torch.float32)
+        _keep(stream, final_state)
+    if checkpoints is True:
+        checkpoints = x.new_empty(glr_checkpoint_shape(T, C), dtype=torch.float32)
+        _keep(stream, checkpoints)
+    elif checkpoints is not None:
+        _need(checkpoints, "checkpoints", torch.float32, glr_checkpoint_shape(T, C), i)
+    st = lib.gdn_glr_fwd(x.data_ptr(), log_alpha.data_ptr(), _addr(beta), gate,
+                         _addr(initial_state), _addr(cu_seqlens), n_seq, T, C, dt, y.data_ptr(),
+                         _addr(final_state), _addr(checkpoints), _on(i, stream))
     if st != GDN_OK:
         raise GdnError(st, "gdn_glr_fwd")
     return y, final_state, checkpoints
@@ -734,32 +731,39 @@ def gdn_glr_bwd(x, log_alpha, dy, beta=None, initial_state=None, d_final_state=N
     computed again into ``workspace`` (a uint8 CUDA tensor of at least
     glr_bwd_workspace_size(T, C) bytes, or None: allocated here)."""
     lib = _lib or load()
-    dev, dt, shape, gate, beta = _glr_inputs(x, log_alpha, beta)
-    T, C = shape
-    n_seq = _glr_sequences(cu_seqlens, dev)
-    _check(dy, "dy")
-    _need(dy, "dy", x.dtype, shape, dev)
-    for name, t in (("initial_state", initial_state), ("d_final_state", d_final_state)):
-        _need(t, name, torch.float32, (n_seq, C), dev)
-    _need(checkpoints, "checkpoints", torch.float32, glr_checkpoint_shape(T, C), dev)
-    _check(workspace, "workspace", torch.uint8, dev)
-    with _on(dev, stream) as on:
-        out = dict(dx=torch.empty_like(x), dlog_alpha=torch.empty_like(x))
-        if gate == _GATE_BETA:
-            out["dbeta"] = torch.empty_like(x)
-        if want_d_initial_state:
-            out["d_initial_state"] = torch.empty((n_seq, C), dtype=torch.float32, device=dev)
-        on.keep(*out.values())
-        if checkpoints is None and workspace is None:
-            workspace = torch.empty(max(int(lib.gdn_glr_bwd_workspace_size(T, C)), 1),
-                                    dtype=torch.uint8, device=dev)
-            on.keep(workspace)
-        st = lib.gdn_glr_bwd(_addr(x), _addr(log_alpha), _addr(beta), gate, _addr(initial_state),
-                             _addr(cu_seqlens), n_seq, T, C, dt, _addr(dy), _addr(d_final_state),
-                             _addr(checkpoints), _addr(out["dx"]), _addr(out["dlog_alpha"]),
-                             _addr(out.get("dbeta")), _addr(out.get("d_initial_state")),
-                             _addr(workspace), 0 if workspace is None else workspace.numel(),
-                             on.handle)
+    i = _device_of(x, "x")
+    if i != _current_device():
+        with torch.cuda.device(i):
+            return gdn_glr_bwd(x, log_alpha, dy, beta, initial_state, d_final_state, cu_seqlens,
+                               checkpoints, want_d_initial_state, workspace, stream)
+    dt, gate, beta = _glr_inputs(x, log_alpha, beta, i)
+    T, C = x.shape
+    n_seq = _glr_sequences(cu_seqlens, i)
+    _need(dy, "dy", x.dtype, x.shape, i)
+    if initial_state is not None:
+        _need(initial_state, "initial_state", torch.float32, (n_seq, C), i)
+    if d_final_state is not None:
+        _need(d_final_state, "d_final_state", torch.float32, (n_seq, C), i)
+    if checkpoints is not None:
+        _need(checkpoints, "checkpoints", torch.float32, glr_checkpoint_shape(T, C), i)
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8, workspace.shape, i)
+    elif checkpoints is None:
+        workspace = x.new_empty(max(int(lib.gdn_glr_bwd_workspace_size(T, C)), 1),
+                                dtype=torch.uint8)
+        _keep(stream, workspace)
+    out = dict(dx=torch.empty_like(x), dlog_alpha=torch.empty_like(x))
+    if gate == _GATE_BETA:
+        out["dbeta"] = torch.empty_like(x)
+    if want_d_initial_state:
+        out["d_initial_state"] = x.new_empty((n_seq, C), dtype=torch.float32)
+    _keep(stream, *out.values())
+    st = lib.gdn_glr_bwd(x.data_ptr(), log_alpha.data_ptr(), _addr(beta), gate,
+                         _addr(initial_state), _addr(cu_seqlens), n_seq, T, C, dt, dy.data_ptr(),
+                         _addr(d_final_state), _addr(checkpoints), out["dx"].data_ptr(),
+                         out["dlog_alpha"].data_ptr(), _addr(out.get("dbeta")),
+                         _addr(out.get("d_initial_state")), _addr(workspace),
+                         0 if workspace is None else workspace.numel(), _on(i, stream))
     if st != GDN_OK:
         raise GdnError(st, "gdn_glr_bwd")
     return out
@@ -770,17 +774,21 @@ def gdn_glr_step(x, log_alpha, state, beta=None, y=None, stream=None) -> torch.T
     C]; beta as for gdn_glr_fwd; ``state`` [N, C] fp32 is updated in place.
     Returns y [N, C]."""
     lib = _lib or load()
-    dev, dt, shape, gate, beta = _glr_inputs(x, log_alpha, beta)
-    _check(state, "state")
-    _need(state, "state", torch.float32, shape, dev)
-    with _on(dev, stream) as on:
-        if y is None:
-            y = torch.empty_like(x)
-            on.keep(y)
-        else:
-            _need(y, "y", x.dtype, shape, dev)
-        st = lib.gdn_glr_step(_addr(x), _addr(log_alpha), _addr(beta), gate, _addr(state),
-                              shape[0], shape[1], dt, _addr(y), on.handle)
+    i = _device_of(x, "x")
+    if i != _current_device():
+        with torch.cuda.device(i):
+            return gdn_glr_step(x, log_alpha, state, beta, y, stream)
+    dt, gate, beta = _glr_inputs(x, log_alpha, beta, i)
+    shape = x.shape
+    _need(state, "state", torch.float32, shape, i)
+    if y is None:
+        y = torch.empty_like(x)
+        _keep(stream, y)
+    else:
+        _need(y, "y", x.dtype, shape, i)
+    st = lib.gdn_glr_step(x.data_ptr(), log_alpha.data_ptr(), _addr(beta), gate,
+                          state.data_ptr(), shape[0], shape[1], dt, y.data_ptr(),
+                          _on(i, stream))
     if st != GDN_OK:
         raise GdnError(st, "gdn_glr_step")
     return y
@@ -808,10 +816,14 @@ def gdn_beam_select(logits, scores, n_candidates, finished=None, end_token=-1, o
     out[3] finished).  ``workspace``: a uint8 CUDA tensor of at least
     beam_workspace_size(...) bytes, or None (allocated here)."""
     lib = _lib or load()
-    dev = logits.device
-    if not logits.is_cuda:
-        raise ValueError("logits must be a CUDA tensor (libgdn has no CPU path)")
-    dt = _dtype_code_of(logits.dtype)
+    i = _device_of(logits, "logits")
+    if i != _current_device():
+        with torch.cuda.device(i):
+            return gdn_beam_select(logits, scores, n_candidates, finished, end_token, out,
+                                   workspace, stream)
+    dt = _CODES.get(logits.dtype)
+    if dt is None:
+        raise TypeError("logits must be bfloat16 or float32, got %s" % logits.dtype)
     if logits.dim() != 3:
         raise ValueError("logits must be [groups, beams, vocabulary], got %s"
                          % (tuple(logits.shape),))
@@ -825,37 +837,34 @@ def gdn_beam_select(logits, scores, n_candidates, finished=None, end_token=-1, o
     if (V > 1 and sv != 1) or (G > 1 and sg != K * ld):
         raise ValueError("logits must have a contiguous vocabulary and equally spaced rows, got "
                          "strides %s" % (logits.stride(),))
-    _check(scores, "scores")
-    _need(scores, "scores", torch.float32, (G, K), dev)
+    _need(scores, "scores", torch.float32, (G, K), i)
     if finished is not None:
-        if finished.dtype == torch.bool:
+        if finished.dtype is torch.bool:
             finished = finished.view(torch.uint8)
-        _need(finished, "finished", torch.uint8, (G, K), dev)
-    _check(workspace, "workspace", torch.uint8, dev)
-    with _on(dev, stream) as on:
-        if out is None:
-            out = (torch.empty((G, M), dtype=torch.float32, device=dev),
-                   torch.empty((G, M), dtype=torch.int32, device=dev),
-                   torch.empty((G, M), dtype=torch.int32, device=dev),
-                   torch.empty((G, M), dtype=torch.uint8, device=dev))
-            on.keep(*out)
-        else:
-            for t, name, dtype in zip(out, ("out scores", "out parents", "out tokens",
-                                            "out finished"),
-                                      (torch.float32, torch.int32, torch.int32, torch.uint8)):
-                _check(t, name)
-                _need(t, name, dtype, (G, M), dev)
-        if workspace is None:
-            n = int(lib.gdn_beam_select_workspace_size(G, K, V, M, dt))
-            workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
-            on.keep(workspace)
-        st = lib.gdn_beam_select(_addr(logits), ld, _addr(scores), _addr(finished),
-                                 int(end_token), G, K, V, M, dt, _addr(out[0]), _addr(out[1]),
-                                 _addr(out[2]), _addr(out[3]), _addr(workspace),
-                                 workspace.numel(), on.handle)
+        _need(finished, "finished", torch.uint8, (G, K), i)
+    if out is None:
+        out = (scores.new_empty((G, M)), scores.new_empty((G, M), dtype=torch.int32),
+               scores.new_empty((G, M), dtype=torch.int32),
+               scores.new_empty((G, M), dtype=torch.uint8))
+        _keep(stream, *out)
+    else:
+        out = tuple(out)
+        for t, name, dtype in zip(out, ("out scores", "out parents", "out tokens", "out finished"),
+                                  (torch.float32, torch.int32, torch.int32, torch.uint8)):
+            _need(t, name, dtype, (G, M), i)
+    if workspace is None:
+        n = int(lib.gdn_beam_select_workspace_size(G, K, V, M, dt))
+        workspace = scores.new_empty(max(n, 1), dtype=torch.uint8)
+        _keep(stream, workspace)
+    else:
+        _need(workspace, "workspace", torch.uint8, workspace.shape, i)
+    st = lib.gdn_beam_select(logits.data_ptr(), ld, scores.data_ptr(), _addr(finished),
+                             int(end_token), G, K, V, M, dt, out[0].data_ptr(),
+                             out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(),
+                             workspace.data_ptr(), workspace.numel(), _on(i, stream))
     if st != GDN_OK:
         raise GdnError(st, "gdn_beam_select")
-    return tuple(out)
+    return out
 
 
 def gdn_state_reorder(states, parents, stream=None):
@@ -864,23 +873,27 @@ def gdn_state_reorder(states, parents, stream=None):
     ``states``: a tensor or a list of up to 16, each contiguous with G * K rows
     (recurrent states, conv states, token histories; any type)."""
     lib = _lib or load()
-    many = [states] if isinstance(states, torch.Tensor) else list(states)
-    dev = parents.device
-    _check(parents, "parents", torch.int32)
-    if parents.dim() != 2 or not many:
-        raise ValueError("parents must be [groups, beams], and there must be a state")
+    i = _device_of(parents, "parents")
+    if i != _current_device():
+        with torch.cuda.device(i):
+            return gdn_state_reorder(states, parents, stream)
+    if parents.dim() != 2:
+        raise ValueError("parents must be [groups, beams], got %s" % (tuple(parents.shape),))
+    _need(parents, "parents", torch.int32, parents.shape, i)
+    many = [states] if isinstance(states, torch.Tensor) else states
     G, K = parents.shape
-    n = len(many)
+    rows, n = G * K, len(many)
+    if n == 0:
+        raise ValueError("there must be a state to reorder")
     ptrs, sizes = (ctypes.c_void_p * n)(), (ctypes.c_size_t * n)()
-    for i, t in enumerate(many):
-        if t.device != dev or not t.is_contiguous():
-            _check(t, "states[%d]" % i, None, dev)
-        if t.dim() < 1 or t.shape[0] != G * K:
-            raise ValueError("states[%d] must have %d rows, got %s" % (i, G * K, tuple(t.shape)))
-        ptrs[i] = t.data_ptr()
-        sizes[i] = t.nbytes // (G * K) if G * K else 0
-    with _on(dev, stream) as on:
-        st = lib.gdn_state_reorder(ptrs, sizes, n, _addr(parents), G, K, on.handle)
+    for j, t in enumerate(many):
+        if t.get_device() != i or not t.is_contiguous():
+            _check(t, "states[%d]" % j, None, parents.device)
+        if t.dim() < 1 or t.shape[0] != rows:
+            raise ValueError("states[%d] must have %d rows, got %s" % (j, rows, tuple(t.shape)))
+        ptrs[j] = t.data_ptr()
+        sizes[j] = t.nbytes // rows if rows else 0
+    st = lib.gdn_state_reorder(ptrs, sizes, n, parents.data_ptr(), G, K, _on(i, stream))
     if st != GDN_OK:
         raise GdnError(st, "gdn_state_reorder")
     return states
