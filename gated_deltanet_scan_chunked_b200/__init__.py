@@ -4,7 +4,7 @@ The computation lives in libgdn.so (CUDA kernels behind the C ABI in
 include/gdn.h).  ``gdn`` is a thin ctypes binding; ``inputs`` holds the
 seeded synthetic workloads; ``build`` compiles the library.
 """
-from .gdn import (GdnError, beam_workspace_size, bwd_workspace_size,  # noqa: F401
+from .gdn import (GdnError, bwd_workspace_size,  # noqa: F401
                   conv_workspace_size, gdn_beam_select,
                   gdn_check_device_error, gdn_chunk_bwd, gdn_chunk_fwd, gdn_chunk_fwd_conv,
                   gdn_conv_frontend, gdn_decode_conv, gdn_decode_multi, gdn_decode_step,
@@ -16,5 +16,5 @@ __all__ = ["gdn_chunk_fwd", "gdn_chunk_bwd", "gdn_decode_step", "gdn_decode_mult
            "gdn_check_device_error", "gdn_conv_frontend", "gdn_chunk_fwd_conv", "gdn_decode_conv", "gdn_gr_read",
            "gdn_gr_write", "gdn_glr_fwd", "gdn_glr_bwd", "gdn_glr_step", "GdnError", "load",
            "glr_bwd_workspace_size", "glr_checkpoint_shape", "gdn_beam_select",
-           "gdn_state_reorder", "beam_workspace_size",
+           "gdn_state_reorder",
            "workspace_size", "bwd_workspace_size", "conv_workspace_size"]

@@ -643,7 +643,7 @@ gdn_status beam_check(int32_t n_groups, int32_t K, int32_t V, int32_t M, gdn_dty
   if (dt != GDN_BF16 && dt != GDN_FP32) return GDN_ERR_UNSUPPORTED;
   if (K > kMaxBeams || M > kMaxBeamCandidates || (int64_t)K * V > 0x7fffffffLL)
     return GDN_ERR_UNSUPPORTED;
-  if ((int64_t)n_groups * K > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
+  if (n_groups > 65535) return GDN_ERR_UNSUPPORTED;  // a cluster each, along the grid's y
   return GDN_OK;
 }
 
@@ -651,19 +651,12 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 
 }  // namespace
 
-extern "C" size_t gdn_beam_select_workspace_size(int32_t n_groups, int32_t K, int32_t V,
-                                                 int32_t M, gdn_dtype in_dtype) {
-  if (beam_check(n_groups, K, V, M, in_dtype) != GDN_OK || n_groups == 0) return 0;
-  return beam_plan((int64_t)n_groups * K, K, V, M, in_dtype).bytes;
-}
-
 extern "C" gdn_status gdn_beam_select(const void* logits, int64_t ld, const float* scores,
                                       const uint8_t* finished, int32_t end_token,
                                       int32_t n_groups, int32_t K, int32_t V, int32_t M,
                                       gdn_dtype in_dtype, float* out_scores,
                                       int32_t* out_parents, int32_t* out_tokens,
-                                      uint8_t* out_finished, void* workspace,
-                                      size_t workspace_bytes, gdn_stream_t stream) {
+                                      uint8_t* out_finished, gdn_stream_t stream) {
   gdn_status st = beam_check(n_groups, K, V, M, in_dtype);
   if (st != GDN_OK) return st;
   if (ld < V || end_token < -1 || end_token >= V) return GDN_ERR_INVALID_ARG;
@@ -676,9 +669,6 @@ extern "C" gdn_status gdn_beam_select(const void* logits, int64_t ld, const floa
     return GDN_ERR_INVALID_ARG;
   const int64_t rows = (int64_t)n_groups * K;
   if (ld > 0x7fffffffffffffffLL / 4 / rows) return GDN_ERR_INVALID_ARG;
-  if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
-      workspace_bytes < beam_plan(rows, K, V, M, in_dtype).bytes)
-    return GDN_ERR_INVALID_ARG;
   // In place (exactly, with M = K) is allowed for the scores and the flags:
   // they are then listed as outputs only.
   const bool same = M == K;
@@ -687,14 +677,14 @@ extern "C" gdn_status gdn_beam_select(const void* logits, int64_t ld, const floa
                      {same && scores == out_scores ? nullptr : scores, (size_t)rows * 4},
                      {same && finished == out_finished ? nullptr : finished, (size_t)rows}};
   const Span out[] = {{out_scores, n * 4}, {out_parents, n * 4}, {out_tokens, n * 4},
-                      {out_finished, n}, {workspace, workspace_bytes}};
-  if (!disjoint(in, 3, out, 5)) return GDN_ERR_INVALID_ARG;
+                      {out_finished, n}};
+  if (!disjoint(in, 3, out, 4)) return GDN_ERR_INVALID_ARG;
   BeamArgs a = {};
   a.logits = logits; a.ld = ld; a.scores = scores; a.finished = finished;
   a.end_token = end_token; a.n_groups = n_groups; a.K = K; a.V = V; a.M = M; a.dtype = in_dtype;
   a.out_scores = out_scores; a.out_parents = out_parents; a.out_tokens = out_tokens;
   a.out_finished = out_finished;
-  return launch_beam_select(a, workspace, reinterpret_cast<cudaStream_t>(stream));
+  return launch_beam_select(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" gdn_status gdn_state_reorder(void* const* states, const size_t* row_bytes,

@@ -6,16 +6,20 @@
 //   c = score_k + logit_kv - log sum_v' exp(logit_kv').
 // Within a beam the order by c is the order by logit, so each row's best M are
 // found from the logits alone while its sum is still being formed, and the
-// logits are read once.  Two kernels:
-//   1. beam_scan_kernel, a CTA per segment of a row: the segment's maximum and
-//      sum of exponentials, and its best M as 64-bit keys (ordered value, then
-//      the complement of the index: keys are distinct, and the lower index
-//      wins a tie), largest first;
-//   2. beam_merge_kernel, a CTA per group: the rows' log sums, then one warp
-//      merges the K x segments lists by score (64-bit floating point, ties to
-//      the lowest k V + v).
+// logits are read once.  One kernel, a cluster of CTAs per group: the group's
+// K rows, cut into S segments each, are dealt to the cluster's CTAs.  A CTA
+// forms a segment's maximum and sum of exponentials and its best M as 64-bit
+// keys (ordered value, then the complement of the index: keys are distinct, and
+// the lower index wins a tie), and leaves them in the first CTA's shared
+// memory, which then forms the rows' log sums and merges the K S lists by score
+// (64-bit floating point, ties to the lowest k V + v).
 // Work is cut by element index, never by address, so rows with equal logits
 // get equal sums bit for bit, wherever they lie.
+//
+// The best M of n values, by 256 threads, without sorting them: each thread's
+// largest; of those, the largest of each of g >= M groups of threads; the
+// least of these g has at least M values at or above it.  What lies at or above
+// it, about g ln g values of random data, is collected and ranked by counting.
 #include <float.h>
 
 #include <atomic>
@@ -124,10 +128,6 @@ struct Row {
   }
 };
 
-__device__ __forceinline__ u64 shfl_u64(u64 v, int src) {
-  return __shfl_sync(0xffffffffu, v, src);
-}
-
 // How a beam takes part: read its logits, or only its end token (finished), or
 // not at all (its score is -inf or not a number).
 enum : int { kLive = 0, kDone = 1, kDead = 2 };
@@ -137,27 +137,53 @@ __device__ __forceinline__ int beam_kind(const BeamArgs& a, int64_t row) {
   return a.finished != nullptr && a.finished[row] != 0 ? kDone : kLive;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) beam_scan_kernel(const BeamArgs a) {
+// The least of the g largest-of-group values (see above): `mine` is a thread's
+// largest key (0: none), g a power of two, 1 .. 64, a thread's group its
+// index modulo g.  All threads; a barrier inside.
+__device__ __forceinline__ u64 least_of_groups(u64 mine, int g, u64 (*best)[32]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  best[warp][lane] = mine;
+  __syncthreads();
+  u64 even = 0, odd = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; w += 2) {
+    const u64 x = best[w][lane], y = best[w + 1][lane];
+    even = x > even ? x : even;
+    odd = y > odd ? y : odd;
+  }
+  u64 v = g == 64 ? (even < odd ? even : odd) : (even > odd ? even : odd);
+  for (int o = 16; o > 0; o >>= 1) {
+    const u64 x = __shfl_xor_sync(0xffffffffu, v, o);
+    v = (o >= g) == (x > v) ? x : v;  // the larger within a group, the lesser of groups
+  }
+  return v;
+}
+
+// Shared memory of a CTA besides the merge's lists.
+struct BeamShared {
+  u64 best[kWarps][32];
+  u64 cand[kCap];
+  u64 red_k[kWarps];
+  int winner[kThreads];
+  float red_m[kWarps], red_s[kWarps];
+  int n_cand, n_win;
+  // the merge
+  double score[kMaxBeams], log_sum[kMaxBeams];  // score -inf: no finite candidate
+  float top[kMaxBeams];
+  unsigned char done[kMaxBeams];
+};
+
+// One segment of a row: its best M keys, largest first (0: none), put(r, key),
+// and its maximum and sum of exp(x - maximum), sums(m, s).  All threads.
+template <typename T, typename Put, typename Sums>
+__device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, int64_t row,
+                                             int seg, Put put, Sums sums) {
   constexpr int E = Vec<T>::n;
   constexpr int U = 4;  // vectors of a thread in flight
-  __shared__ u64 sorted[kWarps][32];
-  __shared__ u64 cand[kCap];
-  __shared__ float red_m[kWarps], red_s[kWarps];
-  __shared__ u64 red_k[kWarps];
-  __shared__ int winner[kMaxBeamCandidates];
-  __shared__ u64 tau;
-  __shared__ int n_cand;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t row = blockIdx.x / a.n_seg;
-  const int seg = (int)(blockIdx.x % a.n_seg);
   const int M = a.M;
   const int64_t e0 = (int64_t)seg * a.seg_len;
   const int64_t e1 = e0 + a.seg_len < a.V ? e0 + a.seg_len : (int64_t)a.V;
-  u64* out = a.keys + ((int64_t)row * a.n_seg + seg) * M;
-  float2* out_sum = a.sums + (int64_t)row * a.n_seg + seg;
-  sm100::launch_dependents();
-
   const int kind = beam_kind(a, row);
   if (kind != kLive) {
     // every token -inf, in index order, but a finished beam's end token 0
@@ -172,18 +198,15 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const BeamArgs a) {
         if (has_end && v >= end) ++v;
         if (v < e1) k = key_of(-INFINITY, (uint32_t)v);
       }
-      out[r] = k;
+      put(r, k);
     }
-    if (tid == 0) *out_sum = make_float2(0.f, 1.f);
+    if (tid == 0) sums(0.f, 1.f);
     return;
   }
 
   const Row<T> x(static_cast<const T*>(a.logits) + row * a.ld, a.V);
-  const int n_vec = (int)((e1 - e0 + E - 1) / E);
-  if (tid == 0) {
-    tau = 1;  // every key
-    n_cand = 0;
-  }
+  const int n_vec = e1 > e0 ? (int)((e1 - e0 + E - 1) / E) : 0;
+  if (tid == 0) sh.n_cand = sh.n_win = 0;
   // One pass: running maximum m and sum s of exp(x - m); the thread's best
   // element.  m starts at the lowest finite value, not -inf, so that m - m is
   // a number in rows of -inf.
@@ -233,61 +256,34 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const BeamArgs a) {
       s += sum;
     }
   }
-  // the segment's maximum and sum
   float wm = m;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, o));
   const float ws = warp_sum(s * sm100::ex2_approx(__fmul_rn(__fadd_rn(m, -wm), kLog2e)));
   if (lane == 0) {
-    red_m[warp] = wm;
-    red_s[warp] = ws;
+    sh.red_m[warp] = wm;
+    sh.red_s[warp] = ws;
   }
-  // The threads' best elements, ranked: the warp sorts its 32 keys, then each
-  // key's rank is its place here plus the larger keys of the other warps.
   const u64 mine = tid < n_vec ? key_of(best, best_at) : 0;
-  int place = 0;
-#pragma unroll 8
-  for (int i = 0; i < 32; ++i) {
-    const u64 k = shfl_u64(mine, i);
-    place += (k > mine || (k == mine && i < lane)) ? 1 : 0;
-  }
-  sorted[warp][place] = mine;
-  __syncthreads();
+  int g = 1;
+  while (g < M) g *= 2;
+  const u64 lim = least_of_groups(mine, g, sh.best);  // (0: fewer vectors than groups)
   if (tid == 0) {
-    float bm = red_m[0];
-    for (int w = 1; w < kWarps; ++w) bm = fmaxf(bm, red_m[w]);
+    float bm = sh.red_m[0];
+    for (int w = 1; w < kWarps; ++w) bm = fmaxf(bm, sh.red_m[w]);
     float bs = 0.f;
     for (int w = 0; w < kWarps; ++w)
-      bs += red_s[w] * sm100::ex2_approx(__fmul_rn(__fadd_rn(red_m[w], -bm), kLog2e));
-    *out_sum = make_float2(bm, bs);
+      bs += sh.red_s[w] * sm100::ex2_approx(__fmul_rn(__fadd_rn(sh.red_m[w], -bm), kLog2e));
+    sums(bm, bs);
   }
-  const int n_own = n_vec < kThreads ? n_vec : kThreads;  // threads with elements
-  const int n_win = n_own < M ? n_own : M;
-  if (place < M && mine != 0) {
-    int rank = place;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w == warp) continue;
-      int lo = 0, hi = 32;  // keys larger than mine in sorted[w]
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (sorted[w][mid] > mine) lo = mid + 1; else hi = mid;
-      }
-      rank += lo;
-    }
-    if (rank < M) {
-      winner[rank] = tid;
-      if (rank == M - 1) tau = mine;
-    }
-  }
+  if (mine >= lim && mine != 0) sh.winner[atomicAdd(&sh.n_win, 1)] = tid;
   __syncthreads();
-  // The segment's best M are >= tau, the M-th best of the threads' best
-  // elements, and lie with the threads whose best is >= tau.  Those threads'
-  // vectors (from the caches) give the candidates: M and a few more.
-  const u64 lim = tau;
-  const float lim_x = lim == 1 ? -INFINITY : unordered((uint32_t)(lim >> 32));
-  const int per = (n_vec + kThreads - 1) / kThreads;
+  // What is at or above the limit lies with the threads whose best is: their
+  // vectors again (from the caches), shared out over all threads.
+  const float lim_x = lim == 0 ? -INFINITY : unordered((uint32_t)(lim >> 32));
+  const int n_win = sh.n_win, per = (n_vec + kThreads - 1) / kThreads;
   for (int i = tid; i < n_win * per; i += kThreads) {
-    const int v = winner[i % n_win] + (i / n_win) * kThreads;
+    const int v = sh.winner[i % n_win] + (i / n_win) * kThreads;
     if (v >= n_vec) continue;
     const int64_t at = e0 + (int64_t)v * E;
     float f[E];
@@ -298,22 +294,23 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const BeamArgs a) {
       if (z >= lim_x && at + j < e1) {
         const u64 k = key_of(z, (uint32_t)(at + j));
         if (k >= lim) {
-          const int c = atomicAdd(&n_cand, 1);
-          if (c < kCap) cand[c] = k;
+          const int c = atomicAdd(&sh.n_cand, 1);
+          if (c < kCap) sh.cand[c] = k;
         }
       }
     }
   }
   __syncthreads();
-  const int n = n_cand;
+  const int n = sh.n_cand;
   if (n <= kCap) {
     for (int c = tid; c < n; c += kThreads) {
-      const u64 k = cand[c];
+      const u64 k = sh.cand[c];
       int rank = 0;
-      for (int d = 0; d < n; ++d) rank += cand[d] > k ? 1 : 0;
-      if (rank < M) out[rank] = k;
+#pragma unroll 4
+      for (int d = 0; d < n; ++d) rank += sh.cand[d] > k ? 1 : 0;
+      if (rank < M) put(rank, k);
     }
-    for (int r = n + tid; r < M; r += kThreads) out[r] = 0;
+    for (int r = n + tid; r < M; r += kThreads) put(r, (u64)0);
     return;
   }
   // More than kCap: a few threads hold a great many of the largest elements
@@ -337,11 +334,11 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const BeamArgs a) {
       const u64 q = __shfl_xor_sync(0xffffffffu, k, o);
       k = q > k ? q : k;
     }
-    if (lane == 0) red_k[warp] = k;
+    if (lane == 0) sh.red_k[warp] = k;
     __syncthreads();
-    for (int w = 0; w < kWarps; ++w) k = red_k[w] > k ? red_k[w] : k;
+    for (int w = 0; w < kWarps; ++w) k = sh.red_k[w] > k ? sh.red_k[w] : k;
     __syncthreads();
-    if (tid == 0) out[r] = k;
+    if (tid == 0) put(r, k);
     last = k;
   }
 }
@@ -356,94 +353,110 @@ __device__ __forceinline__ double unordered64(u64 o) {
   return __longlong_as_double((long long)(o ^ ((o >> 63) ? 1ull << 63 : ~0ull)));
 }
 
-__global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a) {
+template <typename T>
+__global__ void __launch_bounds__(kThreads) beam_select_kernel(const BeamArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
-  // c = score + ((x - top) - log_sum), the difference of the logits first: x and
-  // top may be as large as the type allows
-  __shared__ double score[kMaxBeams], log_sum[kMaxBeams];  // score -inf: no finite candidate
-  __shared__ float top[kMaxBeams];
-  __shared__ unsigned char done[kMaxBeams];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = blockIdx.x, K = a.K, M = a.M, S = a.n_seg;
-  const int lists = K * S, n_keys = lists * M;
-  u64* keys = reinterpret_cast<u64*>(smem);                            // [lists][M]
-  unsigned char* used = reinterpret_cast<unsigned char*>(keys + n_keys);  // [lists]
-  sm100::dependency_wait();  // the scan's results are in memory
+  __shared__ BeamShared sh;
+  const int tid = threadIdx.x;
+  const int n_cta = (int)gridDim.x, rank = (int)blockIdx.x;  // one cluster along x
+  const int64_t g = blockIdx.y;
+  const int K = a.K, M = a.M, S = a.n_seg, lists = K * S, N = lists * M;
+  // (used in the first CTA) keys [M][lists]: list u = k S + segment; then the
+  // merge's candidates; then the segments' sums
+  u64* keys = reinterpret_cast<u64*>(smem);
+  u64* cand_o = keys + N;
+  uint32_t* cand_f = reinterpret_cast<uint32_t*>(cand_o + N);
+  float2* sums = reinterpret_cast<float2*>(cand_f + ((N + 1) & ~1));
+  const uint32_t keys0 = sm100::mapa_shared(sm100::smem_u32(keys), 0);
+  const uint32_t sums0 = sm100::mapa_shared(sm100::smem_u32(sums), 0);
+  if (n_cta > 1) sm100::cluster_sync();  // the first CTA runs before any writes into it
 
-  const u64* src = a.keys + (int64_t)g * n_keys;
-  for (int i = tid; i < n_keys; i += kThreads) keys[i] = src[i];
-  for (int i = tid; i < lists; i += kThreads) used[i] = 0;
-  for (int k = warp; k < K; k += kWarps) {
-    const int64_t row = (int64_t)g * K + k;
-    float m = -FLT_MAX;
-    for (int i = lane; i < S; i += 32) m = fmaxf(m, a.sums[row * S + i].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    double s = 0.0;
-    for (int i = lane; i < S; i += 32) {
-      const float2 p = a.sums[row * S + i];
-      s += (double)p.y * exp((double)p.x - (double)m);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) {
-      const int kind = beam_kind(a, row);
-      // (a row of -inf has s = 0: it takes part like a dead beam; a finished
-      // beam's sums are maximum 0, sum 1)
-      const bool some = kind != kDead && s > 0.0;
-      score[k] = some ? (double)a.scores[row] : -INFINITY;
-      log_sum[k] = some && kind == kLive ? log(s) : 0.0;
-      top[k] = some && kind == kLive ? m : 0.f;
-      done[k] = a.finished != nullptr && a.finished[row] != 0;
-    }
+  for (int u = rank; u < lists; u += n_cta) {
+    scan_segment<T>(
+        a, sh, g * K + u / S, u % S,
+        [&](int r, u64 key) {
+          asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(keys0 + 8u * (r * lists + u)),
+                       "l"(key)
+                       : "memory");
+        },
+        [&](float m, float s) {
+          asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(sums0 + 8u * u), "f"(m),
+                       "f"(s)
+                       : "memory");
+        });
+    __syncthreads();  // before the next segment uses the shared memory again
   }
-  __syncthreads();
-  if (warp != 0) return;
+  if (n_cta > 1) sm100::cluster_sync();
+  if (rank != 0) return;
 
-  // One warp: a lane has the lists lane, lane + 32, ...; each round takes the
-  // best head of all and moves that list on.
-  u64 best = 0;
-  uint32_t best_flat = 0xffffffffu;
-  int best_list = -1;
-  auto pick = [&]() {  // the best head among this lane's lists
-    best = 0;
-    best_flat = 0xffffffffu;
-    best_list = -1;
-    for (int l = lane; l < lists; l += 32) {
-      const int u = used[l];
-      const u64 key = u < M ? keys[l * M + u] : 0;
-      if (key == 0) continue;
-      const int k = l / S;
-      const uint32_t v = ~(uint32_t)key;
-      const float x = unordered((uint32_t)(key >> 32));
-      const u64 o = ordered64(score[k] + (((double)x - (double)top[k]) - log_sum[k]));
-      const uint32_t flat = (uint32_t)k * (uint32_t)a.V + v;
-      if (best_list < 0 || o > best || (o == best && flat < best_flat)) {
-        best = o;
-        best_flat = flat;
-        best_list = l;
+  // The rows: c = score + ((x - top) - log_sum), the difference of the logits
+  // first, since x and top may be as large as the type allows.
+  if (tid < K) {
+    const int64_t row = g * K + tid;
+    const int kind = beam_kind(a, row);
+    float m = -FLT_MAX;
+    for (int i = 0; i < S; ++i) m = fmaxf(m, sums[tid * S + i].x);
+    double s = 0.0;
+    for (int i = 0; i < S; ++i) {
+      const float2 p = sums[tid * S + i];
+      s += (double)(p.y * sm100::ex2_approx(__fmul_rn(__fadd_rn(p.x, -m), kLog2e)));
+    }
+    // (a row of -inf has s = 0: it takes part like a dead beam)
+    const bool some = kind != kDead && s > 0.0, live = some && kind == kLive;
+    sh.score[tid] = some ? (double)a.scores[row] : -INFINITY;
+    sh.log_sum[tid] = live ? log(s) : 0.0;
+    sh.top[tid] = live ? m : 0.f;
+    sh.done[tid] = a.finished != nullptr && a.finished[row] != 0;
+  }
+  if (tid == 0) sh.n_cand = 0;
+  __syncthreads();
+  auto candidate = [&](int i, u64& o, uint32_t& flat) {  // (o = 0: none)
+    const u64 key = keys[i];
+    const int k = (i % lists) / S;
+    const float x = unordered((uint32_t)(key >> 32));
+    o = key == 0 ? 0 : ordered64(sh.score[k] + (((double)x - (double)sh.top[k]) - sh.log_sum[k]));
+    flat = (uint32_t)k * (uint32_t)a.V + ~(uint32_t)key;
+  };
+  // The best M by (score, then the lowest flat index): those at or above the
+  // limit, ranked by counting.  (Equal scores may put more there than ranks
+  // need, never fewer.)
+  u64 mine = 0;
+  for (int i = tid; i < N; i += kThreads) {
+    u64 o;
+    uint32_t flat;
+    candidate(i, o, flat);
+    mine = o > mine ? o : mine;
+  }
+  int groups = 1;
+  while (groups < M) groups *= 2;
+  const u64 lim = least_of_groups(mine, groups, sh.best);
+  if (mine >= lim)
+    for (int i = tid; i < N; i += kThreads) {
+      u64 o;
+      uint32_t flat;
+      candidate(i, o, flat);
+      if (o != 0 && o >= lim) {
+        const int c = atomicAdd(&sh.n_cand, 1);
+        cand_o[c] = o;
+        cand_f[c] = flat;
       }
     }
-  };
-  pick();
-  for (int r = 0; r < M; ++r) {
-    const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32));
-    bool in = (uint32_t)(best >> 32) == hi;
-    const uint32_t lo = __reduce_max_sync(0xffffffffu, in ? (uint32_t)best : 0u);
-    in = in && (uint32_t)best == lo;
-    const uint32_t flat = __reduce_min_sync(0xffffffffu, in ? best_flat : 0xffffffffu);
-    if (in && best_flat == flat && best_list >= 0) {
-      const int k = best_list / S;
-      const int token = (int)(flat - (uint32_t)k * (uint32_t)a.V);
-      const int64_t o = (int64_t)g * M + r;
-      a.out_scores[o] = (float)unordered64(best);
-      a.out_parents[o] = k;
-      a.out_tokens[o] = token;
-      if (a.out_finished != nullptr) a.out_finished[o] = done[k] || token == a.end_token;
-      ++used[best_list];
-      pick();
-    }
-    __syncwarp();
+  __syncthreads();
+  const int n = sh.n_cand;
+  for (int c = tid; c < n; c += kThreads) {
+    const u64 o = cand_o[c];
+    const uint32_t flat = cand_f[c];
+    int r = 0;
+#pragma unroll 4
+    for (int d = 0; d < n; ++d)
+      r += cand_o[d] > o || (cand_o[d] == o && cand_f[d] < flat) ? 1 : 0;
+    if (r >= M) continue;
+    const int k = (int)(flat / (uint32_t)a.V), token = (int)(flat % (uint32_t)a.V);
+    const int64_t at = g * M + r;
+    a.out_scores[at] = (float)unordered64(o);
+    a.out_parents[at] = k;
+    a.out_tokens[at] = token;
+    if (a.out_finished != nullptr) a.out_finished[at] = sh.done[k] || token == a.end_token;
   }
 }
 
@@ -491,66 +504,61 @@ __global__ void __launch_bounds__(kThreads) state_reorder_kernel(const ReorderAr
 
 }  // namespace
 
-// How a call is cut: enough segments that the device has several CTAs per SM
-// (148 SMs), none shorter than one vector a thread, and no more lists than
-// the merge holds in shared memory.
-BeamPlan beam_plan(int64_t rows, int32_t K, int32_t V, int32_t M, gdn_dtype dtype) {
-  const int64_t step = (int64_t)kThreads * (dtype == GDN_BF16 ? 8 : 4);
-  const int64_t target = 4 * 148;
-  int64_t n = (target + rows - 1) / rows;
-  const int64_t most = (V + step - 1) / step;
-  if (n > most) n = most;
-  const int64_t hold = kBeamMergeKeys / ((int64_t)K * M);
-  if (n > hold) n = hold;
-  if (n < 1) n = 1;
-  const int64_t len = ((V + n - 1) / n + step - 1) / step * step;
-  BeamPlan p;
-  p.seg_len = len;
-  p.n_seg = (int32_t)((V + len - 1) / len);
-  p.sum_bytes = ((size_t)rows * p.n_seg * sizeof(float2) + 255) & ~(size_t)255;
-  p.bytes = p.sum_bytes + (((size_t)rows * p.n_seg * M * sizeof(u64) + 255) & ~(size_t)255);
-  return p;
-}
+// How a call is cut.  CTAs of a group's cluster: enough that the device's 148
+// SMs have two each, none with less than a vector a thread; a power of two, at
+// most 16 (more than the portable 8 by leave of cudaFuncSetAttribute).
+constexpr int kMaxCluster = 16;
 
-gdn_status launch_beam_select(BeamArgs a, void* ws, cudaStream_t stream) {
-  const int64_t rows = (int64_t)a.n_groups * a.K;
-  const BeamPlan p = beam_plan(rows, a.K, a.V, a.M, a.dtype);
-  if (rows * p.n_seg > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
-  a.n_seg = p.n_seg;
-  a.seg_len = p.seg_len;
-  a.sums = static_cast<float2*>(ws);
-  a.keys = reinterpret_cast<u64*>(static_cast<char*>(ws) + p.sum_bytes);
-  const unsigned blocks = (unsigned)(rows * p.n_seg);
-  if (a.dtype == GDN_BF16)
-    beam_scan_kernel<__nv_bfloat16><<<blocks, kThreads, 0, stream>>>(a);
-  else
-    beam_scan_kernel<float><<<blocks, kThreads, 0, stream>>>(a);
-  if (cudaPeekAtLastError() != cudaSuccess) return GDN_ERR_CUDA;
-  const size_t smem = (size_t)a.K * p.n_seg * (a.M * sizeof(u64) + 1);
-  static std::atomic<bool> attr_set[64];  // per device; setting it twice does no harm
+gdn_status launch_beam_select(BeamArgs a, cudaStream_t stream) {
+  const int64_t step = (int64_t)kThreads * (a.dtype == GDN_BF16 ? 8 : 4);
+  const int64_t vectors = a.K * ((a.V + step - 1) / step);
+  int cluster = 1;
+  while (cluster < kMaxCluster && (int64_t)cluster * a.n_groups < 2 * 148 && cluster < vectors)
+    cluster *= 2;
+  // Segments of a row: the least time of the busiest CTA, whose every list
+  // costs its elements and about as much as 8192 more for the choice among them.
+  const int hold = kBeamMergeKeys / (a.K * a.M);
+  int segs = 1;
+  double least = 0.0;
+  for (int s = 1; s <= cluster && s <= hold; ++s) {
+    const double cost = ((a.K * s + cluster - 1) / cluster) * ((double)a.V / s + 8192.0);
+    if (s == 1 || cost < least) {
+      least = cost;
+      segs = s;
+    }
+  }
+  a.seg_len = ((a.V + segs - 1) / segs + step - 1) / step * step;
+  a.n_seg = (int)((a.V + a.seg_len - 1) / a.seg_len);
+
+  void (*kernel)(BeamArgs) = a.dtype == GDN_BF16 ? beam_select_kernel<__nv_bfloat16>
+                                                 : beam_select_kernel<float>;
+  const int lists = a.K * a.n_seg;
+  const size_t smem = (size_t)lists * a.M * 20 + 8 + (size_t)lists * sizeof(float2);
+  static std::atomic<bool> attr_set[64][2];  // per device; setting it twice does no harm
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return GDN_ERR_CUDA;
-  if (!attr_set[dev].load(std::memory_order_relaxed)) {
-    if (cudaFuncSetAttribute(beam_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kBeamMergeSmem) != cudaSuccess)
+  std::atomic<bool>& set = attr_set[dev][a.dtype == GDN_BF16 ? 0 : 1];
+  if (!set.load(std::memory_order_relaxed)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kBeamMergeKeys * 28 + 8) != cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+            cudaSuccess)
       return GDN_ERR_CUDA;
-    attr_set[dev].store(true, std::memory_order_relaxed);
+    set.store(true, std::memory_order_relaxed);
   }
-  // the merge may be scheduled while the scan still runs; it waits for the
-  // scan's end before it reads
   cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)cluster;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.n_groups);
+  cfg.gridDim = dim3((unsigned)cluster, (unsigned)a.n_groups);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, beam_merge_kernel, (const BeamArgs)a) == cudaSuccess
-             ? GDN_OK
-             : GDN_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 gdn_status launch_state_reorder(ReorderArgs a, cudaStream_t stream) {

@@ -196,8 +196,7 @@ gdn_status launch_glr_step(const GlrArgs& a, cudaStream_t stream);
 constexpr int kMaxBeams = 32;           // beams of a group
 constexpr int kMaxBeamCandidates = 64;  // candidates chosen per group
 constexpr int kMaxReorderStates = 16;   // state tensors of one reordering
-constexpr int kBeamMergeKeys = 8192;    // candidates that the merge holds in shared memory
-constexpr int kBeamMergeSmem = kBeamMergeKeys * 9;
+constexpr int kBeamMergeKeys = kMaxBeams * kMaxBeamCandidates;  // of a group's lists
 
 struct BeamArgs {
   const void* logits;         // [n_groups * K] rows of V, ld elements apart
@@ -211,20 +210,11 @@ struct BeamArgs {
   int32_t* out_parents;
   int32_t* out_tokens;
   uint8_t* out_finished;      // or nullptr
-  // set by the launcher: the cut, and the workspace's parts
-  int32_t n_seg;
-  int64_t seg_len;            // elements per segment
-  float2* sums;               // [rows, n_seg]: maximum, sum of exp(x - maximum)
-  unsigned long long* keys;   // [rows, n_seg, M], largest first, 0: none
-};
-
-struct BeamPlan {
+  // set by the launcher: segments of a row, and their elements
   int32_t n_seg;
   int64_t seg_len;
-  size_t sum_bytes, bytes;    // of the sums; of the whole workspace
 };
-BeamPlan beam_plan(int64_t rows, int32_t K, int32_t V, int32_t M, gdn_dtype dtype);
-gdn_status launch_beam_select(BeamArgs a, void* ws, cudaStream_t stream);
+gdn_status launch_beam_select(BeamArgs a, cudaStream_t stream);
 
 struct ReorderArgs {
   void* states[kMaxReorderStates];         // [n_groups * K] rows each

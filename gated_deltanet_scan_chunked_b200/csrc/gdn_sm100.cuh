@@ -314,16 +314,6 @@ __device__ __forceinline__ void bulk_store_s2g(void* dst, uint32_t src_smem, uin
                : "memory");
 }
 
-// ---- programmatic dependent launch --------------------------------------------
-// Let the next kernel of the stream (launched with programmatic serialisation)
-// be scheduled; and, in that kernel, wait until this one has ended.
-__device__ __forceinline__ void launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void dependency_wait() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 // Prefetch the 128-byte line holding `p` into L2.
 __device__ __forceinline__ void prefetch_l2(const void* p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));

@@ -123,13 +123,10 @@ def load(path: str = LIB_PATH):
     f.restype = ctypes.c_int
     f.argtypes = [_vp] * 3 + [ctypes.c_int, _vp, ctypes.c_int32, ctypes.c_int32, ctypes.c_int,
                               _vp, _vp]
-    f = lib.gdn_beam_select_workspace_size
-    f.restype = ctypes.c_size_t
-    f.argtypes = [ctypes.c_int32] * 4 + [ctypes.c_int]
     f = lib.gdn_beam_select
     f.restype = ctypes.c_int
     f.argtypes = [_vp, ctypes.c_int64, _vp, _vp] + [ctypes.c_int32] * 5 + [ctypes.c_int] + [
-        _vp] * 5 + [ctypes.c_size_t, _vp]
+        _vp] * 5
     f = lib.gdn_state_reorder
     f.restype = ctypes.c_int
     f.argtypes = [_vp, _vp, ctypes.c_int32, _vp, ctypes.c_int32, ctypes.c_int32, _vp]
@@ -794,15 +791,8 @@ def gdn_glr_step(x, log_alpha, state, beta=None, y=None, stream=None) -> torch.T
     return y
 
 
-def beam_workspace_size(n_groups: int, K: int, V: int, n_candidates: int,
-                        dtype=torch.bfloat16) -> int:
-    """Bytes of workspace gdn_beam_select needs (0: never accepted)."""
-    return int(load().gdn_beam_select_workspace_size(n_groups, K, V, n_candidates,
-                                                     _dtype_code_of(dtype)))
-
-
 def gdn_beam_select(logits, scores, n_candidates, finished=None, end_token=-1, out=None,
-                    workspace=None, stream=None):
+                    stream=None):
     """Beam search's choice: the ``n_candidates`` (M) best continuations of each
     group over its K beams and the vocabulary, by scores[g, k] + log softmax of
     logits[g, k], best first; ties go to the lowest k V + v.
@@ -813,14 +803,13 @@ def gdn_beam_select(logits, scores, n_candidates, finished=None, end_token=-1, o
     continued by ``end_token`` alone, at their own score.  Returns (scores,
     parents, tokens, finished), [G, M] fp32, int32, int32 and uint8, or writes
     them into ``out``, four such tensors (with M = K, out[0] may be scores and
-    out[3] finished).  ``workspace``: a uint8 CUDA tensor of at least
-    beam_workspace_size(...) bytes, or None (allocated here)."""
+    out[3] finished)."""
     lib = _lib or load()
     i = _device_of(logits, "logits")
     if i != _current_device():
         with torch.cuda.device(i):
             return gdn_beam_select(logits, scores, n_candidates, finished, end_token, out,
-                                   workspace, stream)
+                                   stream)
     dt = _CODES.get(logits.dtype)
     if dt is None:
         raise TypeError("logits must be bfloat16 or float32, got %s" % logits.dtype)
@@ -852,16 +841,10 @@ def gdn_beam_select(logits, scores, n_candidates, finished=None, end_token=-1, o
         for t, name, dtype in zip(out, ("out scores", "out parents", "out tokens", "out finished"),
                                   (torch.float32, torch.int32, torch.int32, torch.uint8)):
             _need(t, name, dtype, (G, M), i)
-    if workspace is None:
-        n = int(lib.gdn_beam_select_workspace_size(G, K, V, M, dt))
-        workspace = scores.new_empty(max(n, 1), dtype=torch.uint8)
-        _keep(stream, workspace)
-    else:
-        _need(workspace, "workspace", torch.uint8, workspace.shape, i)
     st = lib.gdn_beam_select(logits.data_ptr(), ld, scores.data_ptr(), _addr(finished),
                              int(end_token), G, K, V, M, dt, out[0].data_ptr(),
                              out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(),
-                             workspace.data_ptr(), workspace.numel(), _on(i, stream))
+                             _on(i, stream))
     if st != GDN_OK:
         raise GdnError(st, "gdn_beam_select")
     return out

@@ -566,10 +566,6 @@ gdn_status gdn_glr_step(const void* x, const void* log_alpha, const void* beta,
  * themselves move.
  */
 
-/* Workspace bytes gdn_beam_select needs (0 for arguments it never accepts). */
-size_t gdn_beam_select_workspace_size(int32_t n_groups, int32_t K, int32_t V, int32_t M,
-                                      gdn_dtype in_dtype);
-
 /*
  * gdn_beam_select -- the M best continuations of every group.
  *
@@ -591,6 +587,7 @@ size_t gdn_beam_select_workspace_size(int32_t n_groups, int32_t K, int32_t V, in
  *   finished       [n_groups, K] bytes (non-zero: finished) or NULL (none)
  *   end_token      in [0, V), or -1: no token ends a beam (finished must
  *                  then be NULL)
+ *   n_groups       0 .. 65535
  *   K              beams per group, 1 .. 32
  *   V              vocabulary; K V < 2^31
  *   M              candidates chosen per group, 1 .. 64, at most K V
@@ -599,18 +596,16 @@ size_t gdn_beam_select_workspace_size(int32_t n_groups, int32_t K, int32_t V, in
  *   out_tokens     [n_groups, M] int32, v
  *   out_finished   [n_groups, M] bytes or NULL: 1 if the parent was finished
  *                  or the token is end_token
- *   workspace      256-byte aligned, gdn_beam_select_workspace_size bytes;
- *                  calls that may overlap must not share one
  * With M = K, out_scores may be scores and out_finished may be finished (in
  * place, for a loop without copies); otherwise outputs must not overlap
- * inputs or each other.  The logits are read once.  Two kernels.
+ * inputs or each other.  The logits are read once.  One kernel, no
+ * workspace.
  */
 gdn_status gdn_beam_select(const void* logits, int64_t ld, const float* scores,
                            const uint8_t* finished, int32_t end_token, int32_t n_groups,
                            int32_t K, int32_t V, int32_t M, gdn_dtype in_dtype,
                            float* out_scores, int32_t* out_parents, int32_t* out_tokens,
-                           uint8_t* out_finished, void* workspace, size_t workspace_bytes,
-                           gdn_stream_t stream);
+                           uint8_t* out_finished, gdn_stream_t stream);
 
 /*
  * gdn_state_reorder -- the states of the chosen beams, in place: row g K + j

@@ -1,7 +1,6 @@
 """Host-side refusals of the beam-search entry points, and pins of their
 numpy oracle (CPU)."""
 import ctypes
-import itertools
 
 import numpy as np
 import pytest
@@ -27,11 +26,10 @@ def at(i):
 
 def _select(lib, **kw):
     a = dict(x=at(1), ld=1000, s=at(2), f=at(3), end=7, G=2, K=4, V=1000, M=8, dt=0, os=at(4),
-             op=at(5), ot=at(6), of=at(7), ws=at(8), wsb=64 * MB)
+             op=at(5), ot=at(6), of=at(7))
     a.update(kw)
     return lib.gdn_beam_select(a["x"], a["ld"], a["s"], a["f"], a["end"], a["G"], a["K"], a["V"],
-                               a["M"], a["dt"], a["os"], a["op"], a["ot"], a["of"], a["ws"],
-                               a["wsb"], None)
+                               a["M"], a["dt"], a["os"], a["op"], a["ot"], a["of"], None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -44,26 +42,15 @@ def _select(lib, **kw):
     (dict(V=1, ld=1, end=0, M=5), BAD),                    # fewer candidates than asked for
     (dict(K=33), UNSUP), (dict(M=65), UNSUP), (dict(dt=2), UNSUP),
     (dict(K=32, V=1 << 26, ld=1 << 26), UNSUP),            # K V = 2^31
-    (dict(ws=None), BAD), (dict(ws=at(8) + 16), BAD), (dict(wsb=100), BAD),
+    (dict(G=65536), UNSUP),
     (dict(os=at(2)), BAD),                                 # in place needs M = K
     (dict(of=at(3)), BAD), (dict(op=at(4)), BAD), (dict(os=at(1) + 64), BAD),
     (dict(M=4, os=at(2) + 4), BAD),                        # a partial overlap
-    (dict(M=4, op=at(2)), BAD), (dict(ws=at(1)), BAD),
-    (dict(G=0, x=None, s=None, os=None, ws=None), OK),
+    (dict(M=4, op=at(2)), BAD),
+    (dict(G=0, x=None, s=None, os=None), OK),
 ])
 def test_select_rejects(lib, kw, code):
     assert _select(lib, **kw) == code
-
-
-def test_workspace_size(lib):
-    n = gdn.beam_workspace_size(2, 4, 1000, 8)
-    assert 0 < n < MB and n % 256 == 0
-    assert gdn.beam_workspace_size(0, 4, 1000, 8) == 0
-    assert gdn.beam_workspace_size(2, 33, 1000, 8) == 0
-    assert gdn.beam_workspace_size(2, 4, 1, 8) == 0
-    # the lists of the largest K and M fit the merge
-    for K, M, V, G in itertools.product((1, 32), (1, 64), (70, 260000), (1, 40)):
-        assert gdn.beam_workspace_size(G, K, V, M) > 0
 
 
 def _reorder(lib, ptrs=(at(1),), sizes=(64,), parents=at(9), G=2, K=4, n=None):

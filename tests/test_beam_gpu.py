@@ -190,17 +190,14 @@ def test_select_when_a_few_threads_hold_the_largest_values(M, dtype):
     check(x, s, M, groups=[0, 3, 149])
 
 
-def test_select_in_place_out_and_workspace():
+def test_select_in_place():
     G, K, V = 3, 6, 3000
     x, s = rows(9, G, K, V, F32)
     fin = torch.zeros(G, K, dtype=torch.uint8, device="cuda")
     fin[1, 2] = 1
     want = lib.gdn_beam_select(x, s, K, finished=fin, end_token=1)
-    ws = torch.full((gdn.beam_workspace_size(G, K, V, K, F32),), 255, dtype=torch.uint8,
-                    device="cuda")
     pa, to = (torch.empty(G, K, dtype=torch.int32, device="cuda") for _ in range(2))
-    out = lib.gdn_beam_select(x, s, K, finished=fin, end_token=1, out=(s, pa, to, fin),
-                              workspace=ws)
+    out = lib.gdn_beam_select(x, s, K, finished=fin, end_token=1, out=(s, pa, to, fin))
     assert out[0] is s and all(torch.equal(a, b) for a, b in zip(out, want))
 
 
@@ -226,8 +223,6 @@ def test_binding_refuses_mismatches():
            lambda: lib.gdn_beam_select(x, s, 2, end_token=100),
            lambda: lib.gdn_beam_select(x, s, 2, finished=ok["finished"]),   # no end token
            lambda: lib.gdn_beam_select(x, s, 2, finished=s, end_token=1),
-           lambda: lib.gdn_beam_select(x, s, 2, workspace=torch.empty(16, dtype=torch.uint8,
-                                                                      device="cuda")),
            lambda: lib.gdn_beam_select(x, s, 2, out=(s, s, s, s)),
            lambda: lib.gdn_state_reorder(torch.zeros(5, 2, device="cuda"),
                                          torch.zeros(2, 3, dtype=torch.int32, device="cuda")),
@@ -339,8 +334,7 @@ def search_step(m, b):
     z = lib.gdn_glr_step(m.x[t], m.lc[t], b["h"], m.bc[t])
     logits = torch.cat([y.flatten(1), z], 1) @ m.w
     lib.gdn_beam_select(logits.view(G, K, V), b["scores"], K, finished=b["finished"], end_token=0,
-                        out=(b["scores"], b["parents"], b["token"], b["finished"]),
-                        workspace=b["ws"])
+                        out=(b["scores"], b["parents"], b["token"], b["finished"]))
     lib.gdn_state_reorder([b["S"], b["h"], b["history"]], b["parents"])
     b["history"].scatter_(1, b["at"].expand(G * K, 1), b["token"].reshape(-1, 1))
     b["at"] += 1
@@ -355,9 +349,7 @@ def buffers(m):
                 finished=torch.zeros(G, K, dtype=torch.uint8, device="cuda"),
                 token=torch.tensor([[5] * K, [9] * K], **i32), parents=torch.zeros(G, K, **i32),
                 history=torch.full((G * K, STEPS), -1, **i32),
-                at=torch.zeros(1, dtype=torch.int64, device="cuda"),
-                ws=torch.empty(gdn.beam_workspace_size(G, K, V, K, F32), dtype=torch.uint8,
-                               device="cuda"))
+                at=torch.zeros(1, dtype=torch.int64, device="cuda"))
 
 
 def test_a_search_keeps_states_histories_and_scores_together():
