@@ -18,8 +18,8 @@
 //
 // The best M of n values, by 256 threads, without sorting them: each thread's
 // largest; of those, the largest of each of g >= M groups of threads; the
-// least of these g has at least M values at or above it.  What lies at or above
-// it, about g ln g values of random data, is collected and ranked by counting.
+// least of these g has at least M values at or above it, and in random data
+// about g ln g.  These are collected and ranked by counting.
 #include <float.h>
 
 #include <atomic>
@@ -60,6 +60,11 @@ template <>
 struct Vec<float> {
   static constexpr int n = 4;
   static constexpr uint32_t kNegInf = 0xff800000u;
+  // the largest (of numbers, where there are any)
+  static __device__ __forceinline__ float top(const uint4& r) {
+    return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)),
+                 fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+  }
   static __device__ __forceinline__ void get(const uint4& r, float* f) {
     f[0] = __uint_as_float(r.x); f[1] = __uint_as_float(r.y);
     f[2] = __uint_as_float(r.z); f[3] = __uint_as_float(r.w);
@@ -69,6 +74,11 @@ template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int n = 8;
   static constexpr uint32_t kNegInf = 0xff80ff80u;
+  static __device__ __forceinline__ float top(const uint4& r) {
+    auto p = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+    const __nv_bfloat162 m = __hmax2(__hmax2(p(r.x), p(r.y)), __hmax2(p(r.z), p(r.w)));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
   static __device__ __forceinline__ void get(const uint4& r, float* f) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -159,12 +169,30 @@ __device__ __forceinline__ u64 least_of_groups(u64 mine, int g, u64 (*best)[32])
   return v;
 }
 
+// For every c in [0, n): use(c, r), once, r the number of d with before(c, d).
+// All threads, several to a c where there are enough.
+template <typename Before, typename Use>
+__device__ __forceinline__ void rank_by_count(int n, Before before, Use use) {
+  int team = 1;  // threads to a c, in one warp
+  while (team < 32 && 2 * team * n <= kThreads) team *= 2;
+  const int me = threadIdx.x % team, c0 = threadIdx.x / team;
+  for (int c = c0; c < ((n + kThreads - 1) / kThreads) * kThreads; c += kThreads / team) {
+    int r = 0;
+    if (c < n)
+      for (int d = me; d < n; d += team) r += before(c, d) ? 1 : 0;
+    for (int o = team / 2; o > 0; o /= 2) r += __shfl_xor_sync(0xffffffffu, r, o);
+    if (c < n && me == 0) use(c, r);
+    if (team > 1) break;  // (every c has had its team)
+  }
+}
+
 // Shared memory of a CTA besides the merge's lists.
 struct BeamShared {
   u64 best[kWarps][32];
   u64 cand[kCap];
   u64 red_k[kWarps];
-  int winner[kThreads];
+  u64 win_key[kThreads], lim;
+  int winner[kThreads], chosen[kMaxBeamCandidates];
   float red_m[kWarps], red_s[kWarps];
   int n_cand, n_win;
   // the merge
@@ -207,11 +235,15 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
   const Row<T> x(static_cast<const T*>(a.logits) + row * a.ld, a.V);
   const int n_vec = e1 > e0 ? (int)((e1 - e0 + E - 1) / E) : 0;
   if (tid == 0) sh.n_cand = sh.n_win = 0;
-  // One pass: running maximum m and sum s of exp(x - m); the thread's best
-  // element.  m starts at the lowest finite value, not -inf, so that m - m is
-  // a number in rows of -inf.
-  float m = -FLT_MAX, s = 0.f, best = -INFINITY;
-  uint32_t best_at = (uint32_t)(e0 + (int64_t)tid * E);
+  // One pass: the sum s of exp(x - m), and the thread's best vector (its largest
+  // value, the first vector that has it).  m need not be the maximum: it is
+  // the first vector's and moves only when exp(x - m) would grow past e^40,
+  // so that most vectors cost no rescaling.  With c = fl(m log2 e), the
+  // exponent is x log2 e - c, one instruction; what c is off by is a factor
+  // common to the thread's terms, put right at the end.  Values beyond 1e30 and
+  // vectors with NaN take the long way.
+  float m = -FLT_MAX, c = 0.f, s = 0.f, best = -INFINITY;
+  uint32_t best_v = (uint32_t)tid;
   for (int v0 = tid; v0 < n_vec; v0 += U * kThreads) {
     uint4 r[U];
 #pragma unroll
@@ -223,39 +255,34 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
     }
 #pragma unroll
     for (int q = 0; q < U; ++q) {
+      const float top = tame(Vec<T>::top(r[q]));
+      if (top > best) {
+        best = top;
+        best_v = (uint32_t)(v0 + q * kThreads);
+      }
+      if (top > m + 40.f) {  // (-FLT_MAX + 40 is -FLT_MAX; nothing is summed yet or it vanishes)
+        s *= sm100::ex2_approx(__fmul_rn(__fadd_rn(m, -top), kLog2e));
+        m = top;
+        c = fabsf(m) < 1e30f ? __fmul_rn(m, kLog2e) : 0.f;
+      }
       float f[E];
       Vec<T>::get(r[q], f);
-      float top = f[0];
-#pragma unroll
-      for (int j = 1; j < E; ++j) top = fmaxf(top, f[j]);
-      if (top > best) {
-        top = tame(top);
-        int at = 0;
-#pragma unroll
-        for (int j = E - 1; j >= 0; --j)
-          if (tame(f[j]) == top) at = j;
-        if (top > best) {
-          best = top;
-          best_at = (uint32_t)(e0 + (int64_t)(v0 + q * kThreads) * E + at);
-        }
-        if (top > m) {
-          s *= sm100::ex2_approx(__fmul_rn(__fadd_rn(m, -top), kLog2e));
-          m = top;
-        }
-      }
       float sum = 0.f;
 #pragma unroll
-      for (int j = 0; j < E; ++j)
-        sum += sm100::ex2_approx(__fmul_rn(__fadd_rn(f[j], -m), kLog2e));
-      if (!(sum <= FLT_MAX)) {  // a NaN or +inf among them
+      for (int j = 0; j < E; ++j) sum += sm100::ex2_approx(__fmaf_rn(f[j], kLog2e, -c));
+      // (m <= 1e30 unless a value is beyond)
+      if (!(sum <= FLT_MAX) || !(fabsf(m) < 1e30f)) {
+        const float c_off = fabsf(m) < 1e30f ? __fmaf_rn(m, kLog2e, -c) : 0.f;
         sum = 0.f;
 #pragma unroll
         for (int j = 0; j < E; ++j)
-          sum += sm100::ex2_approx(__fmul_rn(__fadd_rn(tame(f[j]), -m), kLog2e));
+          sum += sm100::ex2_approx(__fmaf_rn(__fadd_rn(tame(f[j]), -m), kLog2e, c_off));
       }
       s += sum;
     }
   }
+  if (fabsf(m) < 1e30f)  // 2^(c - m log2 e)
+    s = __fmaf_rn(s, -0.6931471805599453f * __fmaf_rn(m, kLog2e, -c), s);
   float wm = m;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, o));
@@ -264,10 +291,11 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
     sh.red_m[warp] = wm;
     sh.red_s[warp] = ws;
   }
-  const u64 mine = tid < n_vec ? key_of(best, best_at) : 0;
+  // (a thread's key here: its best value, then its vector)
+  const u64 mine = tid < n_vec ? key_of(best, best_v) : 0;
   int g = 1;
   while (g < M) g *= 2;
-  const u64 lim = least_of_groups(mine, g, sh.best);  // (0: fewer vectors than groups)
+  u64 lim = least_of_groups(mine, g, sh.best);  // (0: fewer vectors than groups)
   if (tid == 0) {
     float bm = sh.red_m[0];
     for (int w = 1; w < kWarps; ++w) bm = fmaxf(bm, sh.red_m[w]);
@@ -276,14 +304,34 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
       bs += sh.red_s[w] * sm100::ex2_approx(__fmul_rn(__fadd_rn(sh.red_m[w], -bm), kLog2e));
     sums(bm, bs);
   }
-  if (mine >= lim && mine != 0) sh.winner[atomicAdd(&sh.n_win, 1)] = tid;
+  if (mine >= lim && mine != 0) {
+    const int w = atomicAdd(&sh.n_win, 1);
+    sh.winner[w] = tid;
+    sh.win_key[w] = mine;
+  }
   __syncthreads();
   // What is at or above the limit lies with the threads whose best is: their
-  // vectors again (from the caches), shared out over all threads.
+  // vectors again (from the caches), shared out over all threads.  Where that
+  // is more than a vector each, the limit is first raised to the M-th best of
+  // the threads' best.
+  const int per = (n_vec + kThreads - 1) / kThreads;
+  int n_win = sh.n_win;
+  const int* winner = sh.winner;
+  if (n_win > M && n_win * per > kThreads) {
+    rank_by_count(n_win, [&](int c, int d) { return sh.win_key[d] > sh.win_key[c]; },
+                  [&](int c, int r) {
+                    if (r < M) sh.chosen[r] = sh.winner[c];
+                    if (r == M - 1) sh.lim = sh.win_key[c];
+                  });
+    __syncthreads();
+    n_win = M;
+    winner = sh.chosen;
+    lim = sh.lim;
+  }
   const float lim_x = lim == 0 ? -INFINITY : unordered((uint32_t)(lim >> 32));
-  const int n_win = sh.n_win, per = (n_vec + kThreads - 1) / kThreads;
+  const uint32_t lim_v = ~(uint32_t)lim;
   for (int i = tid; i < n_win * per; i += kThreads) {
-    const int v = sh.winner[i % n_win] + (i / n_win) * kThreads;
+    const int v = winner[i % n_win] + (i / n_win) * kThreads;
     if (v >= n_vec) continue;
     const int64_t at = e0 + (int64_t)v * E;
     float f[E];
@@ -291,25 +339,19 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
 #pragma unroll
     for (int j = 0; j < E; ++j) {
       const float z = tame(f[j]);
-      if (z >= lim_x && at + j < e1) {
-        const u64 k = key_of(z, (uint32_t)(at + j));
-        if (k >= lim) {
-          const int c = atomicAdd(&sh.n_cand, 1);
-          if (c < kCap) sh.cand[c] = k;
-        }
+      if ((z > lim_x || (z == lim_x && (uint32_t)v <= lim_v)) && at + j < e1) {
+        const int c = atomicAdd(&sh.n_cand, 1);
+        if (c < kCap) sh.cand[c] = key_of(z, (uint32_t)(at + j));
       }
     }
   }
   __syncthreads();
   const int n = sh.n_cand;
   if (n <= kCap) {
-    for (int c = tid; c < n; c += kThreads) {
-      const u64 k = sh.cand[c];
-      int rank = 0;
-#pragma unroll 4
-      for (int d = 0; d < n; ++d) rank += sh.cand[d] > k ? 1 : 0;
-      if (rank < M) put(rank, k);
-    }
+    rank_by_count(n, [&](int c, int d) { return sh.cand[d] > sh.cand[c]; },
+                  [&](int c, int r) {
+                    if (r < M) put(r, sh.cand[c]);
+                  });
     for (int r = n + tid; r < M; r += kThreads) put(r, (u64)0);
     return;
   }
@@ -443,21 +485,21 @@ __global__ void __launch_bounds__(kThreads) beam_select_kernel(const BeamArgs a)
     }
   __syncthreads();
   const int n = sh.n_cand;
-  for (int c = tid; c < n; c += kThreads) {
-    const u64 o = cand_o[c];
-    const uint32_t flat = cand_f[c];
-    int r = 0;
-#pragma unroll 4
-    for (int d = 0; d < n; ++d)
-      r += cand_o[d] > o || (cand_o[d] == o && cand_f[d] < flat) ? 1 : 0;
-    if (r >= M) continue;
-    const int k = (int)(flat / (uint32_t)a.V), token = (int)(flat % (uint32_t)a.V);
-    const int64_t at = g * M + r;
-    a.out_scores[at] = (float)unordered64(o);
-    a.out_parents[at] = k;
-    a.out_tokens[at] = token;
-    if (a.out_finished != nullptr) a.out_finished[at] = sh.done[k] || token == a.end_token;
-  }
+  rank_by_count(
+      n,
+      [&](int c, int d) {
+        return cand_o[d] > cand_o[c] || (cand_o[d] == cand_o[c] && cand_f[d] < cand_f[c]);
+      },
+      [&](int c, int r) {
+        if (r >= M) return;
+        const uint32_t flat = cand_f[c];
+        const int k = (int)(flat / (uint32_t)a.V), token = (int)(flat % (uint32_t)a.V);
+        const int64_t at = g * M + r;
+        a.out_scores[at] = (float)unordered64(cand_o[c]);
+        a.out_parents[at] = k;
+        a.out_tokens[at] = token;
+        if (a.out_finished != nullptr) a.out_finished[at] = sh.done[k] || token == a.end_token;
+      });
 }
 
 // In-place reordering.  A thread owns one W-wide column of a group's K rows of
