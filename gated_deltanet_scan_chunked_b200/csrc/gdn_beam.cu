@@ -175,14 +175,16 @@ template <typename Before, typename Use>
 __device__ __forceinline__ void rank_by_count(int n, Before before, Use use) {
   int team = 1;  // threads to a c, in one warp
   while (team < 32 && 2 * team * n <= kThreads) team *= 2;
-  const int me = threadIdx.x % team, c0 = threadIdx.x / team;
-  for (int c = c0; c < ((n + kThreads - 1) / kThreads) * kThreads; c += kThreads / team) {
+  const int me = threadIdx.x & (team - 1);
+  for (int c = threadIdx.x / team; c < ((n + kThreads - 1) & ~(kThreads - 1));
+       c += team > 1 ? 2 * kThreads : kThreads) {  // (teams of several: once is enough)
     int r = 0;
-    if (c < n)
+    if (c < n) {
+#pragma unroll 8
       for (int d = me; d < n; d += team) r += before(c, d) ? 1 : 0;
+    }
     for (int o = team / 2; o > 0; o /= 2) r += __shfl_xor_sync(0xffffffffu, r, o);
     if (c < n && me == 0) use(c, r);
-    if (team > 1) break;  // (every c has had its team)
   }
 }
 
@@ -192,9 +194,9 @@ struct BeamShared {
   u64 cand[kCap];
   u64 red_k[kWarps];
   u64 win_key[kThreads], lim;
-  int winner[kThreads], chosen[kMaxBeamCandidates];
+  int single[kThreads], multi[kThreads];
   float red_m[kWarps], red_s[kWarps];
-  int n_cand, n_win;
+  int n_cand, n_win, n_single, n_multi;
   // the merge
   double score[kMaxBeams], log_sum[kMaxBeams];  // score -inf: no finite candidate
   float top[kMaxBeams];
@@ -212,6 +214,19 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
   const int M = a.M;
   const int64_t e0 = (int64_t)seg * a.seg_len;
   const int64_t e1 = e0 + a.seg_len < a.V ? e0 + a.seg_len : (int64_t)a.V;
+  const Row<T> x(static_cast<const T*>(a.logits) + row * a.ld, a.V);
+  const int n_vec = e1 > e0 ? (int)((e1 - e0 + E - 1) / E) : 0;
+  uint4 next[U];  // the batch after the one at hand
+  auto fetch = [&](int v0) {
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      const int v = v0 + q * kThreads;
+      next[q] = v < n_vec ? x.load(e0 + (int64_t)v * E)
+                          : make_uint4(Vec<T>::kNegInf, Vec<T>::kNegInf, Vec<T>::kNegInf,
+                                       Vec<T>::kNegInf);
+    }
+  };
+  fetch(tid);  // (before the beam's state is known: its loads take as long)
   const int kind = beam_kind(a, row);
   if (kind != kLive) {
     // every token -inf, in index order, but a finished beam's end token 0
@@ -232,54 +247,60 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
     return;
   }
 
-  const Row<T> x(static_cast<const T*>(a.logits) + row * a.ld, a.V);
-  const int n_vec = e1 > e0 ? (int)((e1 - e0 + E - 1) / E) : 0;
-  if (tid == 0) sh.n_cand = sh.n_win = 0;
-  // One pass: the sum s of exp(x - m), and the thread's best vector (its largest
-  // value, the first vector that has it).  m need not be the maximum: it is
-  // the first vector's and moves only when exp(x - m) would grow past e^40,
-  // so that most vectors cost no rescaling.  With c = fl(m log2 e), the
-  // exponent is x log2 e - c, one instruction; what c is off by is a factor
-  // common to the thread's terms, put right at the end.  Values beyond 1e30 and
-  // vectors with NaN take the long way.
-  float m = -FLT_MAX, c = 0.f, s = 0.f, best = -INFINITY;
+  if (tid == 0) sh.n_cand = sh.n_win = sh.n_single = sh.n_multi = 0;
+  // One pass: the sum s of exp(x - m), the thread's best vector (its largest
+  // value, the first vector that has it) and the largest value of its other
+  // vectors.  m need not be the maximum: it is the first batch's and moves
+  // only when exp(x - m) would grow past e^40, so that most batches cost no
+  // rescaling.  With c = fl(m log2 e), the exponent is x log2 e - c, one
+  // instruction; what c is off by is a factor common to the thread's terms, put
+  // right at the end.  Values beyond 1e30 and batches with NaN take the long
+  // way.
+  float m = -FLT_MAX, c = 0.f, s = 0.f, best = -INFINITY, other = -INFINITY;
   uint32_t best_v = (uint32_t)tid;
   for (int v0 = tid; v0 < n_vec; v0 += U * kThreads) {
     uint4 r[U];
+    float peak = -INFINITY;
 #pragma unroll
-    for (int q = 0; q < U; ++q) {
-      const int v = v0 + q * kThreads;
-      r[q] = v < n_vec ? x.load(e0 + (int64_t)v * E)
-                       : make_uint4(Vec<T>::kNegInf, Vec<T>::kNegInf, Vec<T>::kNegInf,
-                                    Vec<T>::kNegInf);
-    }
+    for (int q = 0; q < U; ++q) r[q] = next[q];
+    if (v0 + U * kThreads < n_vec) fetch(v0 + U * kThreads);
 #pragma unroll
     for (int q = 0; q < U; ++q) {
       const float top = tame(Vec<T>::top(r[q]));
+      other = fmaxf(other, fminf(top, best));
       if (top > best) {
         best = top;
         best_v = (uint32_t)(v0 + q * kThreads);
       }
-      if (top > m + 40.f) {  // (-FLT_MAX + 40 is -FLT_MAX; nothing is summed yet or it vanishes)
-        s *= sm100::ex2_approx(__fmul_rn(__fadd_rn(m, -top), kLog2e));
-        m = top;
-        c = fabsf(m) < 1e30f ? __fmul_rn(m, kLog2e) : 0.f;
-      }
-      float f[E];
-      Vec<T>::get(r[q], f);
-      float sum = 0.f;
+      peak = fmaxf(peak, top);
+    }
+    if (peak > m + 40.f) {  // (-FLT_MAX + 40 is -FLT_MAX; what was summed vanishes, if any was)
+      s *= sm100::ex2_approx(__fmul_rn(__fadd_rn(m, -peak), kLog2e));
+      m = peak;
+      c = fabsf(m) < 1e30f ? __fmul_rn(m, kLog2e) : 0.f;
+    }
+    float sum = 0.f;
 #pragma unroll
-      for (int j = 0; j < E; ++j) sum += sm100::ex2_approx(__fmaf_rn(f[j], kLog2e, -c));
-      // (m <= 1e30 unless a value is beyond)
-      if (!(sum <= FLT_MAX) || !(fabsf(m) < 1e30f)) {
-        const float c_off = fabsf(m) < 1e30f ? __fmaf_rn(m, kLog2e, -c) : 0.f;
-        sum = 0.f;
+    for (int q = 0; q < U; ++q) {
+      float f[E], part = 0.f;
+      Vec<T>::get(r[q], f);
+#pragma unroll
+      for (int j = 0; j < E; ++j) part += sm100::ex2_approx(__fmaf_rn(f[j], kLog2e, -c));
+      sum += part;
+    }
+    if (!(sum <= FLT_MAX) || !(fabsf(m) < 1e30f)) {
+      const float c_off = fabsf(m) < 1e30f ? __fmaf_rn(m, kLog2e, -c) : 0.f;
+      sum = 0.f;
+#pragma unroll 1
+      for (int v = v0; v < n_vec && v < v0 + U * kThreads; v += kThreads) {
+        float f[E];
+        Vec<T>::get(x.load(e0 + (int64_t)v * E), f);
 #pragma unroll
         for (int j = 0; j < E; ++j)
           sum += sm100::ex2_approx(__fmaf_rn(__fadd_rn(tame(f[j]), -m), kLog2e, c_off));
       }
-      s += sum;
     }
+    s += sum;
   }
   if (fabsf(m) < 1e30f)  // 2^(c - m log2 e)
     s = __fmaf_rn(s, -0.6931471805599453f * __fmaf_rn(m, kLog2e, -c), s);
@@ -304,35 +325,41 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
       bs += sh.red_s[w] * sm100::ex2_approx(__fmul_rn(__fadd_rn(sh.red_m[w], -bm), kLog2e));
     sums(bm, bs);
   }
-  if (mine >= lim && mine != 0) {
-    const int w = atomicAdd(&sh.n_win, 1);
-    sh.winner[w] = tid;
-    sh.win_key[w] = mine;
-  }
-  __syncthreads();
-  // What is at or above the limit lies with the threads whose best is: their
-  // vectors again (from the caches), shared out over all threads.  Where that
-  // is more than a vector each, the limit is first raised to the M-th best of
-  // the threads' best.
-  const int per = (n_vec + kThreads - 1) / kThreads;
-  int n_win = sh.n_win;
-  const int* winner = sh.winner;
-  if (n_win > M && n_win * per > kThreads) {
-    rank_by_count(n_win, [&](int c, int d) { return sh.win_key[d] > sh.win_key[c]; },
-                  [&](int c, int r) {
-                    if (r < M) sh.chosen[r] = sh.winner[c];
-                    if (r == M - 1) sh.lim = sh.win_key[c];
-                  });
+  // Above 64 threads at the limit it is raised to the M-th best of their best:
+  // the counting pays for what need not be read again and ranked.
+  if (__syncthreads_count(mine >= lim && mine != 0) > 64) {
+    if (mine >= lim && mine != 0) sh.win_key[atomicAdd(&sh.n_win, 1)] = mine;
     __syncthreads();
-    n_win = M;
-    winner = sh.chosen;
+    rank_by_count(
+        sh.n_win, [&](int i, int j) { return sh.win_key[j] > sh.win_key[i]; },
+        [&](int i, int r) {
+          if (r == M - 1) sh.lim = sh.win_key[i];
+        });
+    __syncthreads();
     lim = sh.lim;
   }
+  // What is at or above the limit lies with the threads whose best is: in their
+  // best vector, or anywhere in theirs if another vector reaches the limit too.
+  // These are read again (from the caches), shared out over all threads.
   const float lim_x = lim == 0 ? -INFINITY : unordered((uint32_t)(lim >> 32));
   const uint32_t lim_v = ~(uint32_t)lim;
-  for (int i = tid; i < n_win * per; i += kThreads) {
-    const int v = winner[i % n_win] + (i / n_win) * kThreads;
-    if (v >= n_vec) continue;
+  if (mine >= lim && mine != 0) {
+    if (other >= lim_x) sh.multi[atomicAdd(&sh.n_multi, 1)] = tid;
+    else sh.single[atomicAdd(&sh.n_single, 1)] = (int)best_v;
+  }
+  __syncthreads();
+  const int per = (n_vec + kThreads - 1) / kThreads;
+  const int n_single = sh.n_single, n_multi = sh.n_multi;
+#pragma unroll 2
+  for (int i = tid; i < n_single + n_multi * per; i += kThreads) {
+    int v;
+    if (i < n_single) {
+      v = sh.single[i];
+    } else {
+      const int e = i - n_single;
+      v = sh.multi[e % n_multi] + (e / n_multi) * kThreads;
+      if (v >= n_vec) continue;
+    }
     const int64_t at = e0 + (int64_t)v * E;
     float f[E];
     Vec<T>::get(x.load(at), f);
@@ -340,8 +367,8 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
     for (int j = 0; j < E; ++j) {
       const float z = tame(f[j]);
       if ((z > lim_x || (z == lim_x && (uint32_t)v <= lim_v)) && at + j < e1) {
-        const int c = atomicAdd(&sh.n_cand, 1);
-        if (c < kCap) sh.cand[c] = key_of(z, (uint32_t)(at + j));
+        const int k = atomicAdd(&sh.n_cand, 1);
+        if (k < kCap) sh.cand[k] = key_of(z, (uint32_t)(at + j));
       }
     }
   }
@@ -411,6 +438,13 @@ __global__ void __launch_bounds__(kThreads) beam_select_kernel(const BeamArgs a)
   float2* sums = reinterpret_cast<float2*>(cand_f + ((N + 1) & ~1));
   const uint32_t keys0 = sm100::mapa_shared(sm100::smem_u32(keys), 0);
   const uint32_t sums0 = sm100::mapa_shared(sm100::smem_u32(sums), 0);
+  float my_score = 0.f;  // (the first CTA's thread k: beam k's, loaded ahead)
+  int my_kind = kDead;
+  if (rank == 0 && tid < K) {
+    my_score = a.scores[g * K + tid];
+    my_kind = beam_kind(a, g * K + tid);
+    sh.done[tid] = a.finished != nullptr && a.finished[g * K + tid] != 0;
+  }
   if (n_cta > 1) sm100::cluster_sync();  // the first CTA runs before any writes into it
 
   for (int u = rank; u < lists; u += n_cta) {
@@ -434,8 +468,6 @@ __global__ void __launch_bounds__(kThreads) beam_select_kernel(const BeamArgs a)
   // The rows: c = score + ((x - top) - log_sum), the difference of the logits
   // first, since x and top may be as large as the type allows.
   if (tid < K) {
-    const int64_t row = g * K + tid;
-    const int kind = beam_kind(a, row);
     float m = -FLT_MAX;
     for (int i = 0; i < S; ++i) m = fmaxf(m, sums[tid * S + i].x);
     double s = 0.0;
@@ -444,11 +476,10 @@ __global__ void __launch_bounds__(kThreads) beam_select_kernel(const BeamArgs a)
       s += (double)(p.y * sm100::ex2_approx(__fmul_rn(__fadd_rn(p.x, -m), kLog2e)));
     }
     // (a row of -inf has s = 0: it takes part like a dead beam)
-    const bool some = kind != kDead && s > 0.0, live = some && kind == kLive;
-    sh.score[tid] = some ? (double)a.scores[row] : -INFINITY;
+    const bool some = my_kind != kDead && s > 0.0, live = some && my_kind == kLive;
+    sh.score[tid] = some ? (double)my_score : -INFINITY;
     sh.log_sum[tid] = live ? log(s) : 0.0;
     sh.top[tid] = live ? m : 0.f;
-    sh.done[tid] = a.finished != nullptr && a.finished[row] != 0;
   }
   if (tid == 0) sh.n_cand = 0;
   __syncthreads();
@@ -488,7 +519,8 @@ __global__ void __launch_bounds__(kThreads) beam_select_kernel(const BeamArgs a)
   rank_by_count(
       n,
       [&](int c, int d) {
-        return cand_o[d] > cand_o[c] || (cand_o[d] == cand_o[c] && cand_f[d] < cand_f[c]);
+        const u64 o = cand_o[d], mine_o = cand_o[c];
+        return o > mine_o || (o == mine_o && cand_f[d] < cand_f[c]);
       },
       [&](int c, int r) {
         if (r >= M) return;

@@ -574,8 +574,8 @@ gdn_status gdn_glr_step(const void* x, const void* log_alpha, const void* beta,
  * and ordered by c, then by the lowest k V + v (within a beam, by the logit).
  * A finished beam has one continuation, end_token at c = scores[k]; its other
  * tokens score -inf.  A beam whose score is not finite scores -inf throughout,
- * and so does a row of logits that are all -inf; neither these beams' nor
- * finished beams' logits are read.  If fewer than M candidates are finite, the
+ * and so does a row of logits that are all -inf; these beams' logits, and
+ * finished beams', do not count.  If fewer than M candidates are finite, the
  * rest of the M are candidates of score -inf, the lowest k V + v first.
  * A NaN logit counts as -inf; +inf logits share their row equally.
  *
