@@ -169,34 +169,63 @@ __device__ __forceinline__ u64 least_of_groups(u64 mine, int g, u64 (*best)[32])
   return v;
 }
 
-// For every c in [0, n): use(c, r), once, r the number of d with before(c, d).
-// All threads, several to a c where there are enough.
-template <typename Before, typename Use>
-__device__ __forceinline__ void rank_by_count(int n, Before before, Use use) {
-  int team = 1;  // threads to a c, in one warp
-  while (team < 32 && 2 * team * n <= kThreads) team *= 2;
-  const int me = threadIdx.x & (team - 1);
-  for (int c = threadIdx.x / team; c < ((n + kThreads - 1) & ~(kThreads - 1));
-       c += team > 1 ? 2 * kThreads : kThreads) {  // (teams of several: once is enough)
+// For every c in [0, n): use(c, r), once, r the number of keys above key c; TIE:
+// of equal keys the one with the lower tie value is above.  All threads,
+// several to a c where there are enough; keys and ties 16-byte aligned, n
+// rounded up to even of them there (a key behind the last, 0).
+template <bool TIE, typename Use>
+__device__ __forceinline__ void rank_by_count(const u64* keys, const uint32_t* ties, int n,
+                                              Use use) {
+  const int fit = n > 0 ? kThreads / n : 32;
+  const int shift = fit >= 32 ? 5 : fit >= 2 ? 31 - __clz(fit) : 0, team = 1 << shift;
+  const int me = threadIdx.x & (team - 1), pairs = (n + 1) >> 1;
+  const ulonglong2* two = reinterpret_cast<const ulonglong2*>(keys);
+  [[maybe_unused]] const uint2* tie = reinterpret_cast<const uint2*>(ties);
+  for (int c = threadIdx.x >> shift; c < ((n + kThreads - 1) & ~(kThreads - 1));
+       c += shift > 0 ? 2 * kThreads : kThreads) {  // (teams of several: once is enough)
     int r = 0;
-    if (c < n) {
-#pragma unroll 8
-      for (int d = me; d < n; d += team) r += before(c, d) ? 1 : 0;
+    const u64 k = c < n ? keys[c] : ~0ull;
+    [[maybe_unused]] const uint32_t f = TIE && c < n ? ties[c] : 0;
+#pragma unroll 4
+    for (int d = me; d < pairs; d += team) {
+      const ulonglong2 q = two[d];
+      bool x = q.x > k, y = q.y > k;
+      if constexpr (TIE) {
+        const uint2 e = tie[d];
+        x |= (q.x == k) & (e.x < f);
+        y |= (q.y == k) & (e.y < f);
+      }
+      r += (x ? 1 : 0) + (y ? 1 : 0);
     }
-    for (int o = team / 2; o > 0; o /= 2) r += __shfl_xor_sync(0xffffffffu, r, o);
+    for (int o = team >> 1; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
     if (c < n && me == 0) use(c, r);
   }
 }
 
+// A whole warp: room for `count` items of each lane behind *counter; the first
+// of this lane's places.
+__device__ __forceinline__ int places(int count, int* counter) {
+  const int lane = threadIdx.x & 31;
+  int upto = count;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  int base = 0;
+  if (lane == 31 && upto > 0) base = atomicAdd(counter, upto);
+  return __shfl_sync(0xffffffffu, base, 31) + upto - count;
+}
+
 // Shared memory of a CTA besides the merge's lists.
-struct BeamShared {
+struct __align__(16) BeamShared {
   u64 best[kWarps][32];
-  u64 cand[kCap];
-  u64 red_k[kWarps];
-  u64 win_key[kThreads], lim;
-  int single[kThreads], multi[kThreads];
+  u64 cand[kCap + 2];
+  u64 win_key[kThreads + 2];
+  u64 red_k[kWarps], lim;
+  int multi[kThreads];
   float red_m[kWarps], red_s[kWarps];
-  int n_cand, n_win, n_single, n_multi;
+  int n_cand, n_win, n_multi;
   // the merge
   double score[kMaxBeams], log_sum[kMaxBeams];  // score -inf: no finite candidate
   float top[kMaxBeams];
@@ -247,7 +276,7 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
     return;
   }
 
-  if (tid == 0) sh.n_cand = sh.n_win = sh.n_single = sh.n_multi = 0;
+  if (tid == 0) sh.n_cand = sh.n_win = sh.n_multi = 0;
   // One pass: the sum s of exp(x - m), the thread's best vector (its largest
   // value, the first vector that has it) and the largest value of its other
   // vectors.  m need not be the maximum: it is the first batch's and moves
@@ -317,7 +346,79 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
   int g = 1;
   while (g < M) g *= 2;
   u64 lim = least_of_groups(mine, g, sh.best);  // (0: fewer vectors than groups)
-  if (tid == 0) {
+  // Above 64 threads at the limit it is raised to the M-th best of their best:
+  // the counting pays for what need not be read again and ranked.
+  if (__syncthreads_count(mine >= lim && mine != 0) > 64) {
+    const int at = places(mine >= lim && mine != 0, &sh.n_win);
+    if (mine >= lim && mine != 0) sh.win_key[at] = mine;
+    __syncthreads();
+    if (tid == 0) sh.win_key[sh.n_win] = 0;
+    __syncthreads();
+    rank_by_count<false>(sh.win_key, nullptr, sh.n_win, [&](int i, int r) {
+      if (r == M - 1) sh.lim = sh.win_key[i];
+    });
+    __syncthreads();
+    lim = sh.lim;
+  }
+  // What is at or above the limit lies with the threads whose best is: in their
+  // best vector, which each reads again (from the caches), or anywhere in theirs
+  // if another vector reaches the limit too; those are shared out over all
+  // threads.
+  const float lim_x = lim == 0 ? -INFINITY : unordered((uint32_t)(lim >> 32));
+  const uint32_t lim_v = ~(uint32_t)lim;
+  const bool wins = mine >= lim && mine != 0, many = wins && other >= lim_x;
+  {
+    const int at = places(many, &sh.n_multi);
+    if (many) sh.multi[at] = tid;
+  }
+  __syncthreads();
+  const int per = (n_vec + kThreads - 1) / kThreads, n_multi = sh.n_multi;
+  constexpr int R = 3;  // vectors of a thread at a time; at first its own and two shared ones
+  for (int i0 = (tid & ~31) - kThreads; i0 < n_multi * per; i0 += R * kThreads) {
+    int v[R];
+    uint4 w[R];
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      const int i = i0 + lane + q * kThreads;
+      v[q] = -1;
+      if (i < 0) {
+        if (wins && !many) v[q] = (int)best_v;
+      } else if (i < n_multi * per) {
+        v[q] = sh.multi[i / per] + (i % per) * kThreads;
+        if (v[q] >= n_vec) v[q] = -1;
+      }
+      if (v[q] >= 0) w[q] = x.load(e0 + (int64_t)v[q] * E);
+    }
+    uint32_t hits = 0;
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      if (v[q] < 0) continue;
+      float f[E];
+      Vec<T>::get(w[q], f);
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const float z = tame(f[j]);
+        if ((z > lim_x || (z == lim_x && (uint32_t)v[q] <= lim_v)) &&
+            (int64_t)v[q] * E + j < e1 - e0)
+          hits |= 1u << (q * E + j);
+      }
+    }
+    if (!__any_sync(0xffffffffu, hits != 0)) continue;
+    int k = places(__popc(hits), &sh.n_cand);
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      if ((hits >> (q * E) & ((1u << E) - 1u)) == 0) continue;
+      float f[E];
+      Vec<T>::get(w[q], f);
+#pragma unroll
+      for (int j = 0; j < E; ++j)
+        if (hits >> (q * E + j) & 1) {
+          if (k < kCap) sh.cand[k] = key_of(tame(f[j]), (uint32_t)(e0 + (int64_t)v[q] * E + j));
+          ++k;
+        }
+    }
+  }
+  if (tid == kThreads - 1) {  // (the last to have a rank to count)
     float bm = sh.red_m[0];
     for (int w = 1; w < kWarps; ++w) bm = fmaxf(bm, sh.red_m[w]);
     float bs = 0.f;
@@ -325,60 +426,14 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
       bs += sh.red_s[w] * sm100::ex2_approx(__fmul_rn(__fadd_rn(sh.red_m[w], -bm), kLog2e));
     sums(bm, bs);
   }
-  // Above 64 threads at the limit it is raised to the M-th best of their best:
-  // the counting pays for what need not be read again and ranked.
-  if (__syncthreads_count(mine >= lim && mine != 0) > 64) {
-    if (mine >= lim && mine != 0) sh.win_key[atomicAdd(&sh.n_win, 1)] = mine;
-    __syncthreads();
-    rank_by_count(
-        sh.n_win, [&](int i, int j) { return sh.win_key[j] > sh.win_key[i]; },
-        [&](int i, int r) {
-          if (r == M - 1) sh.lim = sh.win_key[i];
-        });
-    __syncthreads();
-    lim = sh.lim;
-  }
-  // What is at or above the limit lies with the threads whose best is: in their
-  // best vector, or anywhere in theirs if another vector reaches the limit too.
-  // These are read again (from the caches), shared out over all threads.
-  const float lim_x = lim == 0 ? -INFINITY : unordered((uint32_t)(lim >> 32));
-  const uint32_t lim_v = ~(uint32_t)lim;
-  if (mine >= lim && mine != 0) {
-    if (other >= lim_x) sh.multi[atomicAdd(&sh.n_multi, 1)] = tid;
-    else sh.single[atomicAdd(&sh.n_single, 1)] = (int)best_v;
-  }
-  __syncthreads();
-  const int per = (n_vec + kThreads - 1) / kThreads;
-  const int n_single = sh.n_single, n_multi = sh.n_multi;
-#pragma unroll 2
-  for (int i = tid; i < n_single + n_multi * per; i += kThreads) {
-    int v;
-    if (i < n_single) {
-      v = sh.single[i];
-    } else {
-      const int e = i - n_single;
-      v = sh.multi[e % n_multi] + (e / n_multi) * kThreads;
-      if (v >= n_vec) continue;
-    }
-    const int64_t at = e0 + (int64_t)v * E;
-    float f[E];
-    Vec<T>::get(x.load(at), f);
-#pragma unroll
-    for (int j = 0; j < E; ++j) {
-      const float z = tame(f[j]);
-      if ((z > lim_x || (z == lim_x && (uint32_t)v <= lim_v)) && at + j < e1) {
-        const int k = atomicAdd(&sh.n_cand, 1);
-        if (k < kCap) sh.cand[k] = key_of(z, (uint32_t)(at + j));
-      }
-    }
-  }
   __syncthreads();
   const int n = sh.n_cand;
   if (n <= kCap) {
-    rank_by_count(n, [&](int c, int d) { return sh.cand[d] > sh.cand[c]; },
-                  [&](int c, int r) {
-                    if (r < M) put(r, sh.cand[c]);
-                  });
+    if (tid == 0) sh.cand[n] = 0;
+    __syncthreads();
+    rank_by_count<false>(sh.cand, nullptr, n, [&](int i, int r) {
+      if (r < M) put(r, sh.cand[i]);
+    });
     for (int r = n + tid; r < M; r += kThreads) put(r, (u64)0);
     return;
   }
@@ -423,8 +478,8 @@ __device__ __forceinline__ double unordered64(u64 o) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) beam_select_kernel(const BeamArgs a) {
-  extern __shared__ __align__(16) unsigned char smem[];
+__global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs a) {
+  extern __shared__ __align__(16) unsigned char beam_smem[];
   __shared__ BeamShared sh;
   const int tid = threadIdx.x;
   const int n_cta = (int)gridDim.x, rank = (int)blockIdx.x;  // one cluster along x
@@ -432,10 +487,11 @@ __global__ void __launch_bounds__(kThreads) beam_select_kernel(const BeamArgs a)
   const int K = a.K, M = a.M, S = a.n_seg, lists = K * S, N = lists * M;
   // (used in the first CTA) keys [M][lists]: list u = k S + segment; then the
   // merge's candidates; then the segments' sums
-  u64* keys = reinterpret_cast<u64*>(smem);
-  u64* cand_o = keys + N;
-  uint32_t* cand_f = reinterpret_cast<uint32_t*>(cand_o + N);
-  float2* sums = reinterpret_cast<float2*>(cand_f + ((N + 1) & ~1));
+  u64* keys = reinterpret_cast<u64*>(beam_smem);
+  const int Np = (N + 3) & ~1;  // (room for a key behind the last, 16-byte steps)
+  u64* cand_o = keys + Np;
+  uint32_t* cand_f = reinterpret_cast<uint32_t*>(cand_o + Np);
+  float2* sums = reinterpret_cast<float2*>(cand_f + Np);
   const uint32_t keys0 = sm100::mapa_shared(sm100::smem_u32(keys), 0);
   const uint32_t sums0 = sm100::mapa_shared(sm100::smem_u32(sums), 0);
   float my_score = 0.f;  // (the first CTA's thread k: beam k's, loaded ahead)
@@ -503,35 +559,34 @@ __global__ void __launch_bounds__(kThreads) beam_select_kernel(const BeamArgs a)
   int groups = 1;
   while (groups < M) groups *= 2;
   const u64 lim = least_of_groups(mine, groups, sh.best);
-  if (mine >= lim)
-    for (int i = tid; i < N; i += kThreads) {
-      u64 o;
-      uint32_t flat;
-      candidate(i, o, flat);
-      if (o != 0 && o >= lim) {
-        const int c = atomicAdd(&sh.n_cand, 1);
-        cand_o[c] = o;
-        cand_f[c] = flat;
-      }
+  for (int i0 = tid & ~31; i0 < N; i0 += kThreads) {
+    const int i = i0 + (tid & 31);
+    u64 o = 0;
+    uint32_t flat = 0;
+    if (mine >= lim && i < N) candidate(i, o, flat);
+    const bool in = o != 0 && o >= lim;
+    if (!__any_sync(0xffffffffu, in)) continue;
+    const int c = places(in, &sh.n_cand);
+    if (in) {
+      cand_o[c] = o;
+      cand_f[c] = flat;
     }
+  }
   __syncthreads();
   const int n = sh.n_cand;
-  rank_by_count(
-      n,
-      [&](int c, int d) {
-        const u64 o = cand_o[d], mine_o = cand_o[c];
-        return o > mine_o || (o == mine_o && cand_f[d] < cand_f[c]);
-      },
-      [&](int c, int r) {
-        if (r >= M) return;
-        const uint32_t flat = cand_f[c];
-        const int k = (int)(flat / (uint32_t)a.V), token = (int)(flat % (uint32_t)a.V);
-        const int64_t at = g * M + r;
-        a.out_scores[at] = (float)unordered64(cand_o[c]);
-        a.out_parents[at] = k;
-        a.out_tokens[at] = token;
-        if (a.out_finished != nullptr) a.out_finished[at] = sh.done[k] || token == a.end_token;
-      });
+  if (tid == 0) cand_o[n] = 0;
+  __syncthreads();
+  rank_by_count<true>(cand_o, cand_f, n, [&](int c, int r) {
+    if (r >= M) return;
+    const u64 o = cand_o[c];
+    const uint32_t flat = cand_f[c];
+    const int k = (int)(flat / (uint32_t)a.V), token = (int)(flat % (uint32_t)a.V);
+    const int64_t at = g * M + r;
+    a.out_scores[at] = (float)unordered64(o);
+    a.out_parents[at] = k;
+    a.out_tokens[at] = token;
+    if (a.out_finished != nullptr) a.out_finished[at] = sh.done[k] || token == a.end_token;
+  });
 }
 
 // In-place reordering.  A thread owns one W-wide column of a group's K rows of
@@ -607,14 +662,14 @@ gdn_status launch_beam_select(BeamArgs a, cudaStream_t stream) {
   void (*kernel)(BeamArgs) = a.dtype == GDN_BF16 ? beam_select_kernel<__nv_bfloat16>
                                                  : beam_select_kernel<float>;
   const int lists = a.K * a.n_seg;
-  const size_t smem = (size_t)lists * a.M * 20 + 8 + (size_t)lists * sizeof(float2);
+  const size_t smem = ((size_t)lists * a.M + 3) * 20 + (size_t)lists * sizeof(float2);
   static std::atomic<bool> attr_set[64][2];  // per device; setting it twice does no harm
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return GDN_ERR_CUDA;
   std::atomic<bool>& set = attr_set[dev][a.dtype == GDN_BF16 ? 0 : 1];
   if (!set.load(std::memory_order_relaxed)) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kBeamMergeKeys * 28 + 8) != cudaSuccess ||
+                             kBeamMergeKeys * 28 + 60) != cudaSuccess ||
         cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
             cudaSuccess)
       return GDN_ERR_CUDA;
