@@ -89,52 +89,68 @@ struct Vec<__nv_bfloat16> {
   }
 };
 
-// One row, read as vectors of 16 bytes by element index whatever its address:
-// a row that does not begin on 16 bytes is read as aligned pairs and shifted
-// together.  Nothing outside the row is touched: vectors whose aligned pair
-// would reach over either end are gathered element by element.
+// One row, read as vectors of 16 bytes by element index whatever its address.  A
+// row that begins on 16 bytes gives a vector in one load.  Any other gives
+// aligned words, five where elements of 2 bytes begin in the middle of one, which
+// are shifted together only when they are used, so that loads stay in
+// flight.  Nothing outside the row is touched: vectors whose words would
+// reach over either end are gathered element by element.
 template <typename T>
 struct Row {
+  struct Raw {
+    uint32_t w[5];
+  };
   const T* p;
   int64_t V;
-  uint32_t shift;  // bytes from the aligned address below
+  bool whole;     // begins on 16 bytes
+  uint32_t bits;  // of the first word before the vector
 
-  __device__ __forceinline__ Row(const T* row, int64_t v)
-      : p(row), V(v), shift((uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u)) {}
-
-  __device__ __forceinline__ uint4 load(int64_t i) const {  // elements i .. i + Vec::n - 1
+  __device__ __forceinline__ Row(const T* row, int64_t v) : p(row), V(v) {
+    const uint32_t at = (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u);
+    whole = at == 0;
+    bits = (at & 3u) * 8u;
+  }
+  static __device__ __forceinline__ Raw none() {  // -inf throughout
+    Raw r;
+#pragma unroll
+    for (int k = 0; k < 5; ++k) r.w[k] = Vec<T>::kNegInf;
+    return r;
+  }
+  __device__ __forceinline__ Raw load(int64_t i) const {  // elements i .. i + Vec::n - 1
     constexpr int E = Vec<T>::n;
-    if (shift == 0) {
-      if (i + E <= V) return __ldg(reinterpret_cast<const uint4*>(p + i));
-    } else if (i > 0 && i + 2 * E <= V) {
-      const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(p + i) - shift);
-      const uint4 a = __ldg(q), b = __ldg(q + 1);
-      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-      const uint32_t bits = (shift & 3u) * 8u, word = shift >> 2;
-      uint32_t o[4];
+    Raw r;
+    if (whole && i + E <= V) {
+      const uint4 a = __ldg(reinterpret_cast<const uint4*>(p + i));
+      r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
+      r.w[4] = 0;
+    } else if (!whole && (bits == 0 || i > 0) && i + E < V) {
+      const uint32_t* q =
+          reinterpret_cast<const uint32_t*>(reinterpret_cast<const char*>(p + i) - bits / 8);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) r.w[k] = __ldg(q + k);
+      r.w[4] = E == 8 && bits != 0 ? __ldg(q + 4) : 0;
+    } else {
+      uint32_t o[6];  // the vector's words, none before and behind
+      o[0] = o[5] = 0;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        // (word is uniform over the CTA: selects, no indexed registers)
-        const uint32_t lo = word == 0 ? w[k] : word == 1 ? w[k + 1] : word == 2 ? w[k + 2] : w[k + 3];
-        const uint32_t hi =
-            word == 0 ? w[k + 1] : word == 1 ? w[k + 2] : word == 2 ? w[k + 3] : w[(k + 4) & 7];
-        o[k] = __funnelshift_r(lo, hi, bits);
+        if (E == 4) {
+          o[k + 1] = i + k < V ? reinterpret_cast<const uint32_t*>(p)[i + k] : Vec<T>::kNegInf;
+        } else {
+          const unsigned short* h = reinterpret_cast<const unsigned short*>(p);
+          const uint32_t lo = i + 2 * k < V ? h[i + 2 * k] : 0xff80u;
+          const uint32_t hi = i + 2 * k + 1 < V ? h[i + 2 * k + 1] : 0xff80u;
+          o[k + 1] = lo | hi << 16;
+        }
       }
-      return make_uint4(o[0], o[1], o[2], o[3]);
-    }
-    uint32_t o[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (E == 4) {
-        o[k] = i + k < V ? reinterpret_cast<const uint32_t*>(p)[i + k] : Vec<T>::kNegInf;
-      } else {
-        const unsigned short* h = reinterpret_cast<const unsigned short*>(p);
-        const uint32_t lo = i + 2 * k < V ? h[i + 2 * k] : 0xff80u;
-        const uint32_t hi = i + 2 * k + 1 < V ? h[i + 2 * k + 1] : 0xff80u;
-        o[k] = lo | hi << 16;
-      }
+      for (int k = 0; k < 5; ++k) r.w[k] = __funnelshift_l(o[k], o[k + 1], bits);
     }
-    return make_uint4(o[0], o[1], o[2], o[3]);
+    return r;
+  }
+  __device__ __forceinline__ uint4 get(const Raw& r) const {
+    return make_uint4(__funnelshift_r(r.w[0], r.w[1], bits), __funnelshift_r(r.w[1], r.w[2], bits),
+                      __funnelshift_r(r.w[2], r.w[3], bits), __funnelshift_r(r.w[3], r.w[4], bits));
   }
 };
 
@@ -245,14 +261,12 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
   const int64_t e1 = e0 + a.seg_len < a.V ? e0 + a.seg_len : (int64_t)a.V;
   const Row<T> x(static_cast<const T*>(a.logits) + row * a.ld, a.V);
   const int n_vec = e1 > e0 ? (int)((e1 - e0 + E - 1) / E) : 0;
-  uint4 next[U];  // the batch after the one at hand
+  typename Row<T>::Raw next[U];  // the batch after the one at hand
   auto fetch = [&](int v0) {
 #pragma unroll
     for (int q = 0; q < U; ++q) {
       const int v = v0 + q * kThreads;
-      next[q] = v < n_vec ? x.load(e0 + (int64_t)v * E)
-                          : make_uint4(Vec<T>::kNegInf, Vec<T>::kNegInf, Vec<T>::kNegInf,
-                                       Vec<T>::kNegInf);
+      next[q] = v < n_vec ? x.load(e0 + (int64_t)v * E) : x.none();
     }
   };
   fetch(tid);  // (before the beam's state is known: its loads take as long)
@@ -291,7 +305,7 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
     uint4 r[U];
     float peak = -INFINITY;
 #pragma unroll
-    for (int q = 0; q < U; ++q) r[q] = next[q];
+    for (int q = 0; q < U; ++q) r[q] = x.get(next[q]);
     if (v0 + U * kThreads < n_vec) fetch(v0 + U * kThreads);
 #pragma unroll
     for (int q = 0; q < U; ++q) {
@@ -323,7 +337,7 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
 #pragma unroll 1
       for (int v = v0; v < n_vec && v < v0 + U * kThreads; v += kThreads) {
         float f[E];
-        Vec<T>::get(x.load(e0 + (int64_t)v * E), f);
+        Vec<T>::get(x.get(x.load(e0 + (int64_t)v * E)), f);
 #pragma unroll
         for (int j = 0; j < E; ++j)
           sum += sm100::ex2_approx(__fmaf_rn(__fadd_rn(tame(f[j]), -m), kLog2e, c_off));
@@ -376,7 +390,7 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
   constexpr int R = 3;  // vectors of a thread at a time; at first its own and two shared ones
   for (int i0 = (tid & ~31) - kThreads; i0 < n_multi * per; i0 += R * kThreads) {
     int v[R];
-    uint4 w[R];
+    typename Row<T>::Raw w[R];
 #pragma unroll
     for (int q = 0; q < R; ++q) {
       const int i = i0 + lane + q * kThreads;
@@ -394,7 +408,7 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
     for (int q = 0; q < R; ++q) {
       if (v[q] < 0) continue;
       float f[E];
-      Vec<T>::get(w[q], f);
+      Vec<T>::get(x.get(w[q]), f);
 #pragma unroll
       for (int j = 0; j < E; ++j) {
         const float z = tame(f[j]);
@@ -409,7 +423,7 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
     for (int q = 0; q < R; ++q) {
       if ((hits >> (q * E) & ((1u << E) - 1u)) == 0) continue;
       float f[E];
-      Vec<T>::get(w[q], f);
+      Vec<T>::get(x.get(w[q]), f);
 #pragma unroll
       for (int j = 0; j < E; ++j)
         if (hits >> (q * E + j) & 1) {
@@ -446,7 +460,7 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
     for (int v = tid; v < n_vec; v += kThreads) {
       const int64_t at = e0 + (int64_t)v * E;
       float f[E];
-      Vec<T>::get(x.load(at), f);
+      Vec<T>::get(x.get(x.load(at)), f);
 #pragma unroll
       for (int j = 0; j < E; ++j) {
         const u64 q = key_of(tame(f[j]), (uint32_t)(at + j));
@@ -478,7 +492,7 @@ __device__ __forceinline__ double unordered64(u64 o) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) beam_select_kernel(const BeamArgs a) {
   extern __shared__ __align__(16) unsigned char beam_smem[];
   __shared__ BeamShared sh;
   const int tid = threadIdx.x;
@@ -633,17 +647,59 @@ __global__ void __launch_bounds__(kThreads) state_reorder_kernel(const ReorderAr
 
 }  // namespace
 
-// How a call is cut.  CTAs of a group's cluster: enough that the device's 148
-// SMs have two each, none with less than a vector a thread; a power of two, at
-// most 16 (more than the portable 8 by leave of cudaFuncSetAttribute).
-constexpr int kMaxCluster = 16;
+// Clusters of 2^i CTAs that the device holds at once, per type (asked once per
+// device; the answers are the same whoever asks, so threads may race).
+constexpr int kMaxDevices = 64, kLogMaxCluster = 4;
+std::atomic<int> g_fit[kMaxDevices][2][kLogMaxCluster + 1];
 
 gdn_status launch_beam_select(BeamArgs a, cudaStream_t stream) {
-  const int64_t step = (int64_t)kThreads * (a.dtype == GDN_BF16 ? 8 : 4);
+  const bool bf16 = a.dtype == GDN_BF16;
+  void (*kernel)(BeamArgs) =
+      bf16 ? beam_select_kernel<__nv_bfloat16> : beam_select_kernel<float>;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return GDN_ERR_CUDA;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+
+  // The group's cluster: the largest power of two at which all groups are on the
+  // device at once, none of its CTAs with less than a vector a thread; at
+  // most 16 (more than the portable 8 by leave of cudaFuncSetAttribute).
+  // Measured on a B200 (K = 8, V = 130000, M = 16, bf16): 32 groups in clusters
+  // of 16 (two waves) 37.9 us, of 8 29.4, of 4 45.2; 16 groups in clusters of
+  // 16 24.1, of 8 24.7.
+  const int64_t step = (int64_t)kThreads * (bf16 ? 8 : 4);
   const int64_t vectors = a.K * ((a.V + step - 1) / step);
   int cluster = 1;
-  while (cluster < kMaxCluster && (int64_t)cluster * a.n_groups < 2 * 148 && cluster < vectors)
-    cluster *= 2;
+  for (int i = kLogMaxCluster; i > 0; --i) {
+    std::atomic<int>& slot = g_fit[dev][bf16 ? 0 : 1][i];
+    int fit = slot.load(std::memory_order_relaxed);
+    if (fit == 0) {
+      attr.val.clusterDim.x = 1u << i;
+      cfg.gridDim = dim3(1u << i);
+      cfg.dynamicSmemBytes = 16384;
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kBeamMergeKeys * 28 + 60) != cudaSuccess ||
+          cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+              cudaSuccess)
+        return GDN_ERR_CUDA;
+      if (cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg) != cudaSuccess || fit < 1) {
+        cudaGetLastError();  // (a size that the device cannot hold)
+        fit = -1;
+      }
+      slot.store(fit, std::memory_order_relaxed);
+    }
+    if (fit >= a.n_groups && (1 << i) < 2 * vectors) {
+      cluster = 1 << i;
+      break;
+    }
+  }
   // Segments of a row: the least time of the busiest CTA, whose every list
   // costs its elements and about as much as 8192 more for the choice among them.
   const int hold = kBeamMergeKeys / (a.K * a.M);
@@ -658,35 +714,10 @@ gdn_status launch_beam_select(BeamArgs a, cudaStream_t stream) {
   }
   a.seg_len = ((a.V + segs - 1) / segs + step - 1) / step * step;
   a.n_seg = (int)((a.V + a.seg_len - 1) / a.seg_len);
-
-  void (*kernel)(BeamArgs) = a.dtype == GDN_BF16 ? beam_select_kernel<__nv_bfloat16>
-                                                 : beam_select_kernel<float>;
   const int lists = a.K * a.n_seg;
-  const size_t smem = ((size_t)lists * a.M + 3) * 20 + (size_t)lists * sizeof(float2);
-  static std::atomic<bool> attr_set[64][2];  // per device; setting it twice does no harm
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return GDN_ERR_CUDA;
-  std::atomic<bool>& set = attr_set[dev][a.dtype == GDN_BF16 ? 0 : 1];
-  if (!set.load(std::memory_order_relaxed)) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kBeamMergeKeys * 28 + 60) != cudaSuccess ||
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
-            cudaSuccess)
-      return GDN_ERR_CUDA;
-    set.store(true, std::memory_order_relaxed);
-  }
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = (unsigned)cluster;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)cluster, (unsigned)a.n_groups);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.dynamicSmemBytes = ((size_t)lists * a.M + 3) * 20 + (size_t)lists * sizeof(float2);
   return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
