@@ -425,15 +425,13 @@ struct Exchange {
     }
     return h;
   }
-  // The tile's runs, as one to the cluster and, through the others' in return,
-  // h before this warp's run.
+  // The tile's runs: what lies before this warp's, the whole to the cluster.
   template <int W, bool BACK, bool CUT>
-  __device__ __forceinline__ f2 before(int64_t step, int lane, int warp, const Run (*runs)[32],
-                                       f2& carry) {
-    Run b, all;
-    fold_tile<W, BACK, CUT>(runs, lane, warp, b, all);
+  __device__ __forceinline__ Run give(int64_t step, int lane, int warp, const Run (*runs)[32]) {
+    Run before, all;
+    fold_tile<W, BACK, CUT>(runs, lane, warp, before, all);
     send<W>(step, lane, warp, all);
-    return through<CUT>(b, receive<CUT>(step, lane, carry));
+    return before;
   }
 };
 
@@ -559,9 +557,14 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
     runs[warp][lane] = run;
     __syncthreads();  // the runs are complete; the step before is done with its stage
     if (step > 0) load(step + 1);
-    f2 h = p.cu_seqlens == nullptr
-               ? ex.template before<W, false, false>(step, lane, warp, runs, carry)
-               : ex.template before<W, false, true>(step, lane, warp, runs, carry);
+    f2 h;
+    if (p.cu_seqlens == nullptr) {
+      const Run before = ex.template give<W, false, false>(step, lane, warp, runs);
+      h = through<false>(before, ex.template receive<false>(step, lane, carry));
+    } else {
+      const Run before = ex.template give<W, false, true>(step, lane, warp, runs);
+      h = through<true>(before, ex.template receive<true>(step, lane, carry));
+    }
     if (p.checkpoints != nullptr && t0 % kGlrTile == 0 && t0 < T_)
       ch.put(p.checkpoints, t0 / kGlrTile, C, h);
     if (p.y == nullptr) continue;
@@ -722,14 +725,42 @@ __global__ void __launch_bounds__(32 * BwdShape::W, 16 / BwdShape::W)
     rev_runs[warp][lane] = rr;
     __syncthreads();  // the runs are complete; the step before is done with its stage
     if (step > 0) load(step + 1);
-    f2 e;
+    // While the cluster's runs are under way: the state before this run, and
+    // h_{t-1} of every token (into u).
+    Run behind;
     if (p.cu_seqlens == nullptr) {
-      e = ex.template before<W, true, false>(step, lane, warp, rev_runs, carry);
-      for (int w = 0; w < warp; ++w) h = through<false>(fwd_runs[w][lane], h);
+      behind = ex.template give<W, true, false>(step, lane, warp, rev_runs);
+#pragma unroll
+      for (int w = 0; w < W - 1; ++w)
+        if (w < warp) h = through<false>(fwd_runs[w][lane], h);
     } else {
-      e = ex.template before<W, true, true>(step, lane, warp, rev_runs, carry);
-      for (int w = 0; w < warp; ++w) h = through<true>(fwd_runs[w][lane], h);
+      behind = ex.template give<W, true, true>(step, lane, warp, rev_runs);
+#pragma unroll
+      for (int w = 0; w < W - 1; ++w)
+        if (w < warp) h = through<true>(fwd_runs[w][lane], h);
     }
+    if (m.first == 0) {
+#pragma unroll
+      for (int i = 0; i < RUN; ++i) {
+        const f2 next = fma2(a[i], h, u[i]);
+        u[i] = h;
+        h = next;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < RUN; ++i) {
+        const f2 next = (m.first >> i & 1) ? u[i] : fma2(a[i], h, u[i]);
+        u[i] = h;
+        h = next;
+      }
+      for (uint32_t f = m.first; f != 0; f &= f - 1) {  // before a first token: h_0
+        const int k = __ffs((int)f) - 1;
+        replace(u, k, ch.get(p.initial_state, m.seq_of(k), C));
+      }
+    }
+    f2 e = p.cu_seqlens == nullptr
+               ? through<false>(behind, ex.template receive<false>(step, lane, carry))
+               : through<true>(behind, ex.template receive<true>(step, lane, carry));
     // Token i's gradients, from its x, h_{t-1} (hb), dh, e and b's parts.
     const int64_t o0 = tile * ROWS * row_bytes;
     auto out = [&](int i, f2 dh, f2 hb, f2 om_i) {
@@ -751,28 +782,12 @@ __global__ void __launch_bounds__(32 * BwdShape::W, 16 / BwdShape::W)
     };
     if (inside) {
 #pragma unroll
-      for (int i = 0; i < RUN; ++i) {  // h_{t-1} of every token, into u
-        const f2 next = fma2(a[i], h, u[i]);
-        u[i] = h;
-        h = next;
-      }
-#pragma unroll
       for (int i = RUN - 1; i >= 0; --i) {
         const f2 dh = add2(in(kDy, i), e);
         e = mul2(a[i], dh);
         out(i, dh, u[i], om[i]);
       }
     } else {
-#pragma unroll
-      for (int i = 0; i < RUN; ++i) {
-        const f2 next = (m.first >> i & 1) ? u[i] : fma2(a[i], h, u[i]);
-        u[i] = h;
-        h = next;
-      }
-      for (uint32_t f = m.first; f != 0; f &= f - 1) {  // before a first token: h_0
-        const int k = __ffs((int)f) - 1;
-        replace(u, k, ch.get(p.initial_state, m.seq_of(k), C));
-      }
       f2 d[RUN];
       all_dy(d);
 #pragma unroll
