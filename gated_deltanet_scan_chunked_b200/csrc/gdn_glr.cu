@@ -112,12 +112,15 @@ __device__ __forceinline__ int seq_at(const int32_t* cu, int n_seq, int64_t t) {
 
 // Which of a run's tokens from t0 on begin or end a sequence (bit i: token
 // t0 + i; tokens outside [0, total_T) neither); lane i has token i's sequence.
-// The bounds [lo, hi) of the sequence that the run leaves into are kept: most
-// runs lie inside it and need no look at the offsets.
+// The sequence that the walk has come to and its bounds [lo, hi) are kept: most
+// runs lie inside it and need no look at the offsets.  Another run's
+// sequences are counted from there over the next 31 offsets, read in one load;
+// only where those are not enough are they searched for.
 template <int RUN, bool BACK>
 struct Marks {
   uint32_t first = 0, last = 0;
-  int seq = 0;
+  int seq = 0;           // (lane i) of token i
+  int at = -1;           // of the walk's last token, -1: none yet
   int64_t lo = 0, hi = 0;
 
   __device__ __forceinline__ void look(const GlrArgs& p, int64_t t0, int lane) {
@@ -130,19 +133,45 @@ struct Marks {
     }
     if (lo < t0 && t0 + RUN < hi) return;
     const int64_t t = t0 + lane;
+    const bool in = lane < RUN && t >= 0 && t < p.total_T;
     int64_t l = 0, h = 0;
-    bool f = false, e = false;
-    if (lane < RUN && t >= 0 && t < p.total_T) {
+    bool found = false;  // (the same in every lane)
+    if (at >= 0) {
+      // offset `at + 1 + lane` ahead, or `at - lane` behind; of offsets 0 ..
+      // n_seq those below n_seq count
+      const int i = BACK ? at - lane : at + 1 + lane;
+      const int64_t off = i < 0 ? -1 : i > p.n_seq ? (int64_t)1 << 62 : __ldg(p.cu_seqlens + i);
+      int passed = 0;
+#pragma unroll
+      for (int k = 0; k < RUN; ++k) {
+        const uint32_t b = __ballot_sync(0xffffffffu, BACK ? off > t0 + k : i < p.n_seq && off <= t0 + k);
+        if (lane == k) passed = __popc(b);
+      }
+      found = !__any_sync(0xffffffffu, in && passed >= 31);
+      if (found) {
+        seq = BACK ? max(at - passed, 0) : at + passed;  // (0: whatever the offsets hold)
+        // offsets seq and seq + 1, which others have loaded, but for the one
+        // before the first: the walk's own bounds
+        const int64_t x = __shfl_sync(0xffffffffu, off, BACK ? passed : passed - 1 & 31);
+        const int64_t y = __shfl_sync(0xffffffffu, off, BACK ? passed - 1 & 31 : passed);
+        l = !BACK && passed == 0 ? lo : x;
+        h = BACK && passed == 0 ? hi : y;
+      }
+    }
+    if (!found && in) {
       seq = seq_at(p.cu_seqlens, p.n_seq, t);
       l = __ldg(p.cu_seqlens + seq);
       h = __ldg(p.cu_seqlens + seq + 1);
-      f = l == t;
-      e = h == t + 1;
     }
-    first = __ballot_sync(0xffffffffu, f);
-    last = __ballot_sync(0xffffffffu, e);
-    lo = __shfl_sync(0xffffffffu, l, BACK ? 0 : RUN - 1);
-    hi = __shfl_sync(0xffffffffu, h, BACK ? 0 : RUN - 1);
+    first = __ballot_sync(0xffffffffu, in && l == t);
+    last = __ballot_sync(0xffffffffu, in && h == t + 1);
+    const uint32_t some = __ballot_sync(0xffffffffu, in);
+    if (some != 0) {
+      const int end = BACK ? __ffs((int)some) - 1 : 31 - __clz(some);
+      at = __shfl_sync(0xffffffffu, seq, end);
+      lo = __shfl_sync(0xffffffffu, l, end);
+      hi = __shfl_sync(0xffffffffu, h, end);
+    }
   }
   __device__ __forceinline__ int seq_of(int i) const {
     return __shfl_sync(0xffffffffu, seq, i);
