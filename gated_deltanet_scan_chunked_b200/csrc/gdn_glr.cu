@@ -264,11 +264,9 @@ struct Piece {
   }
 };
 
-// Stores a lane's two channels of a token row (unaligned rows); `base` is the
-// same for the whole CTA, `off` the bytes from it to the row's channel 0.
+// Stores a lane's two channels of a token row (unaligned rows); q: its first.
 template <typename T>
-__device__ __forceinline__ void put_out(char* base, uint32_t off, const Chan<false>& ch, f2 v) {
-  T* q = reinterpret_cast<T*>(base + (off + (uint32_t)ch.c0 * (uint32_t)sizeof(T)));
+__device__ __forceinline__ void put_out(T* q, const Chan<false>& ch, f2 v) {
   if (ch.ok0) Elem<T>::store(q, v.x);
   if (ch.ok1) Elem<T>::store(q + 32, v.y);
 }
@@ -597,12 +595,14 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
     if (p.checkpoints != nullptr && t0 % kGlrTile == 0 && t0 < T_)
       ch.put(p.checkpoints, t0 / kGlrTile, C, h);
     if (p.y == nullptr) continue;
-    char* y = static_cast<char*>(p.y) + tile0 * row_bytes;
-    auto out = [&](int i) {
+    [[maybe_unused]] T* y = static_cast<T*>(p.y) + t0 * C + ch.c0;
+    [[maybe_unused]] const int n_tok = T_ - t0 < RUN ? (int)(T_ - t0) : RUN;
+    auto out = [&](int i) {  // (called with i ascending)
       if constexpr (AL) {
         P::put(st + i * P::kPitch, lane, h);
       } else {
-        if (t0 + i < T_) put_out<T>(y, (uint32_t)(warp * RUN + i) * row_bytes, ch, h);
+        if (i < n_tok) put_out<T>(y, ch, h);
+        y += C;
       }
     };
     if (inside) {
@@ -791,7 +791,8 @@ __global__ void __launch_bounds__(32 * BwdShape::W, 16 / BwdShape::W)
                ? through<false>(behind, ex.template receive<false>(step, lane, carry))
                : through<true>(behind, ex.template receive<true>(step, lane, carry));
     // Token i's gradients, from its x, h_{t-1} (hb), dh, e and b's parts.
-    const int64_t o0 = tile * ROWS * row_bytes;
+    const int64_t o0 = t0 * C + ch.c0;
+    [[maybe_unused]] const int n_tok = t0 < 0 ? 0 : T_ - t0 < RUN ? (int)(T_ - t0) : RUN;
     auto out = [&](int i, f2 dh, f2 hb, f2 om_i) {
       const f2 x = in(0, i);
       const f2 dx = gated<GATE>(dh, GATE == kGateBeta ? in(kBeta, i) : both(0.f), om_i);
@@ -802,11 +803,11 @@ __global__ void __launch_bounds__(32 * BwdShape::W, 16 / BwdShape::W)
         P::put(row, lane, dx);
         P::put(row + stages.kTensor, lane, dl);
         if (GATE == kGateBeta) P::put(row + kBeta * stages.kTensor, lane, db);
-      } else if (t0 + i >= 0 && t0 + i < T_) {
-        const uint32_t off = (uint32_t)(warp * RUN + i) * row_bytes;
-        put_out<T>(static_cast<char*>(p.dx) + o0, off, ch, dx);
-        put_out<T>(static_cast<char*>(p.dlog_alpha) + o0, off, ch, dl);
-        if (GATE == kGateBeta) put_out<T>(static_cast<char*>(p.dbeta) + o0, off, ch, db);
+      } else if (i < n_tok) {
+        const int64_t o = o0 + (int64_t)i * C;
+        put_out<T>(static_cast<T*>(p.dx) + o, ch, dx);
+        put_out<T>(static_cast<T*>(p.dlog_alpha) + o, ch, dl);
+        if (GATE == kGateBeta) put_out<T>(static_cast<T*>(p.dbeta) + o, ch, db);
       }
     };
     if (inside) {

@@ -832,9 +832,9 @@ def gdn_beam_select(logits, scores, n_candidates, finished=None, end_token=-1, o
             finished = finished.view(torch.uint8)
         _need(finished, "finished", torch.uint8, (G, K), i)
     if out is None:
-        out = (scores.new_empty((G, M)), scores.new_empty((G, M), dtype=torch.int32),
-               scores.new_empty((G, M), dtype=torch.int32),
-               scores.new_empty((G, M), dtype=torch.uint8))
+        best = torch.empty_like(scores) if M == K else scores.new_empty((G, M))
+        parents = torch.empty_like(best, dtype=torch.int32)
+        out = (best, parents, torch.empty_like(parents), torch.empty_like(best, dtype=torch.uint8))
         _keep(stream, *out)
     else:
         out = tuple(out)

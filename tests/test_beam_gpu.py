@@ -91,6 +91,38 @@ def test_select_against_oracle(G, K, V, M, pad, offset, dtype):
     check(x, s, M, end_token=0, groups=range(0, G, max(1, G // 20)))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("G,K,V,M", [(3000, 4, 700, 8), (65535, 1, 40, 3), (1, 32, 9000, 64),
+                                     (5, 12, 70001, 24), (2, 31, 20011, 1), (40, 3, 33333, 6)])
+def test_select_over_groups_and_beams(G, K, V, M, dtype):
+    x, s = rows(V, G, K, V, dtype)
+    check(x, s, M, groups=sorted({0, 1 % G, G // 3, G // 2, G - 1}))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_select_with_few_tokens_allowed(dtype):
+    """Masks that leave a few tokens of a large vocabulary, at its start, its end
+    and scattered: fewer finite values than threads, M, or one."""
+    V = 70001
+    x, s = rows(61, 6, 4, V, dtype, 3, 1)
+    keep = [[0], [V - 1], [5, V - 2], list(range(100, 106)), list(range(0, V, 9973)),
+            list(range(V - 300, V))]
+    for g, k in enumerate(keep):
+        m = torch.ones(V, dtype=torch.bool, device="cuda")
+        m[k] = False
+        x[g][:, m] = -INF
+    check(x, s, 12)
+
+
+def test_select_past_32_bit_offsets():
+    """Rows that begin more than 2^32 elements into the logits."""
+    ld = (1 << 31) + 1003
+    buf = torch.empty(3 * ld + 4096, dtype=BF16, device="cuda")
+    x = buf.as_strided((1, 4, 4001), (4 * ld, ld, 1))
+    x.copy_(torch.randn(1, 4, 4001, generator=torch.Generator().manual_seed(1)))
+    check(x, torch.tensor([[-1.0, -2.0, -0.5, -0.25]], device="cuda"), 8)
+
+
 def test_select_long_vocabulary():
     x, s = rows(3, 1, 2, 1 << 20, BF16, 0, 0)
     check(x, s, 64)

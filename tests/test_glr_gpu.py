@@ -1,6 +1,10 @@
 """Gated linear recurrence on the GPU against the fp64 oracle, elementwise
 inside the oracle's derived fp32 bounds (plus half a step of the output's
 type), and its contracts: packing, carrying, aliasing, streams, graphs."""
+import pathlib
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -11,6 +15,7 @@ from oracle import glr
 
 pytestmark = pytest.mark.gpu
 BF16, F32 = torch.bfloat16, torch.float32
+ROOT = str(pathlib.Path(__file__).resolve().parent.parent)
 HALF_STEP = {BF16: 2.0 ** -8, F32: 2.0 ** -24}
 GATES = ["none", "beta", "complement"]
 
@@ -89,15 +94,64 @@ def test_against_oracle(lens, C, gate, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("lens,C", [([300], 8), ([40, 90, 7], 16), ([129], 24), ([2000, 61], 4),
+                                    ([3000], 64), ([700, 900], 192)])
+def test_narrow_against_oracle(lens, C, dtype):
+    """Rows shorter than a CTA's channels; few channels, so the largest clusters."""
+    check(make(40 + C, lens, C, "complement", dtype), dtype)
+
+
+@pytest.mark.parametrize("lens", [[0] * 100 + [1] * 200 + [0] * 50 + [700] + [2] * 90,
+                                  [3] * 500, [40, 0] * 30 + [1] * 300,
+                                  [600] + [0] * 80 + [1] + [0] * 33 + [500]])
+def test_many_sequences_against_oracle(lens):
+    """More sequences between two runs than the walk counts at once."""
+    check(make(len(lens), lens, 24, "beta", BF16), BF16)
+    check(make(len(lens), lens, 9, "none", F32), F32)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("lens,C", [([3000, 1, 1500], 70), ([4500], 33)])
 def test_long_memory_against_oracle(lens, C, dtype):
     """Channels that remember thousands of tokens, over several cluster steps."""
     check(make(11, lens, C, "beta", dtype, slow=True), dtype)
 
 
-@pytest.mark.parametrize("C", [2560, 6145])
-def test_wide_against_oracle(C):
-    check(make(12, [140, 0, 90], C, "beta", BF16), BF16)
+@pytest.mark.parametrize("lens,C", [([140, 0, 90], 2560), ([140, 0, 90], 6145),
+                                    ([1000, 300], 6144), ([700], 9216)])
+def test_wide_against_oracle(lens, C):
+    check(make(12, lens, C, "beta", BF16), BF16)
+
+
+@pytest.mark.parametrize("C", [2048, 2049])
+def test_offsets_past_32_bits(C):
+    """More than 2^32 elements: the last sequence equals the same one alone."""
+    T, n = (1 << 21) + 300, 200
+    g = torch.Generator("cuda").manual_seed(C)
+    tail = {k: torch.rand(n, C, generator=g, device="cuda").to(BF16) for k in ("x", "be", "dy")}
+    tail["la"] = -torch.rand(n, C, generator=g, device="cuda").to(BF16)
+    h0 = torch.randn(2, C, generator=g, device="cuda")
+    big = {}
+    for k, v in tail.items():
+        big[k] = torch.full((T, C), -0.5 if k == "la" else 0.25, dtype=BF16, device="cuda")
+        big[k][T - n:] = v
+    cu = torch.tensor([0, T - n, T], dtype=torch.int32, device="cuda")
+    y, hT, ck = lib.gdn_glr_fwd(big["x"], big["la"], big["be"], initial_state=h0, cu_seqlens=cu,
+                                checkpoints=True)
+    d = lib.gdn_glr_bwd(big["x"], big["la"], big["dy"], big["be"], initial_state=h0,
+                        cu_seqlens=cu, checkpoints=ck)
+    ref = glr.forward(f64(tail["x"]), f64(tail["la"]), f64(tail["be"]), f64(h0[1:]))
+    inside(y[T - n:], ref["y"], ref["y_bound"], BF16, "y")
+    inside(hT[1:], ref["final_state"], ref["final_bound"], F32, "final_state")
+    ref_d, bound = glr.backward(f64(tail["x"]), f64(tail["la"]), f64(tail["dy"]), f64(tail["be"]),
+                                f64(h0[1:]))
+    for k in ("dx", "dlog_alpha", "dbeta"):
+        inside(d[k][T - n:], ref_d[k], bound[k], BF16, k)
+    inside(d["d_initial_state"][1:], ref_d["d_initial_state"], bound["d_initial_state"], F32, "dh0")
+    # the long sequence has settled: h = a h + b x with a = e^-1/2, b x = 1/16
+    fixed = 0.0625 / (1 - np.exp(-0.5))
+    assert (hT[0] - fixed).abs().max().item() < 1e-5 * fixed
+    assert (y[T // 2].float() - fixed).abs().max().item() <= 2.0 ** -8 * fixed * 1.01
 
 
 def test_no_initial_state_is_zeros():
@@ -264,6 +318,53 @@ def test_results_do_not_depend_on_timing_or_stream():
         s.synchronize()
         assert torch.equal(y, y2) and torch.equal(hT, hT2) and torch.equal(ck, ck2)
         assert all(torch.equal(d[k], d2[k]) for k in d)
+
+
+def test_calls_at_the_same_time():
+    """Different batches on streams that overlap: nothing is shared between calls."""
+    ps = [{k: cuda(v) for k, v in make(50 + i, [900 + 37 * i, 5], 640 + 8 * i, "beta", BF16).items()}
+          for i in range(4)]
+    want = [(forward(p, checkpoints=True), backward(p)) for p in ps]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ps]
+    got = [[] for _ in ps]
+    for _ in range(5):
+        for i, (p, s) in enumerate(zip(ps, streams)):
+            got[i].append((forward(p, checkpoints=True, stream=s), backward(p, stream=s)))
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        for f, d in g:
+            assert all(torch.equal(a, b) for a, b in zip(f, w[0]))
+            assert all(torch.equal(d[k], w[1][k]) for k in d)
+
+
+FIRST = """
+import torch, gated_deltanet_scan_chunked_b200 as lib
+x = torch.ones(200, 64, device="cuda", dtype=torch.bfloat16)
+la = torch.full_like(x, float("-inf"))
+z = torch.zeros(1, 2, 50, device="cuda"); z[0, 1, 7] = 9
+s = torch.zeros(1, 2, device="cuda"); S = torch.arange(8.0, device="cuda").reshape(2, 4)
+h = torch.zeros(200, 64, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    y, hT, ck = lib.gdn_glr_fwd(x, la, checkpoints=True)
+    d = lib.gdn_glr_bwd(x, la, x, checkpoints=ck)
+    ys = lib.gdn_glr_step(x, la, h)
+    sc, pa, to, fi = lib.gdn_beam_select(z, s, 2)
+    lib.gdn_state_reorder(S, pa)
+g.replay(); torch.cuda.synchronize()
+assert (y == 1).all() and (hT == 1).all() and (d["dx"] == 1).all() and (ys == 1).all()
+assert (h == 1).all() and pa.tolist()[0][0] == 1 and to.tolist()[0][0] == 7
+assert S[0].tolist() == [4.0, 5.0, 6.0, 7.0], S
+print("ok")
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    out = subprocess.run([sys.executable, "-c", FIRST], cwd=ROOT, capture_output=True, text=True,
+                         timeout=300)
+    assert out.returncode == 0 and out.stdout.strip().endswith("ok"), out.stderr[-2000:]
 
 
 def test_captured_and_replayed():
