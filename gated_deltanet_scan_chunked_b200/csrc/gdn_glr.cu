@@ -485,15 +485,13 @@ __device__ __forceinline__ void empty_sequences(const GlrArgs& p, const float* i
   }
 }
 
-// Tokens of a thread's run and warps of a CTA.  The forward holds a and b x of
-// its run in registers (4 a token) and comes with 4 and with 8 warps; the
-// backward starts each tile from a checkpoint.
+// Tokens of a thread's run.  The forward holds a and b x of its run in registers
+// (4 a token), the backward more.  Both come with 4 and with 8 warps to a CTA;
+// the backward's tiles begin at checkpoints.
 template <typename T>
 constexpr int fwd_run() { return sizeof(T) == 2 ? 16 : 8; }
-struct BwdShape {
-  static constexpr int W = 8, RUN = 8;
-};
-static_assert(BwdShape::W * BwdShape::RUN == kGlrTile, "a tile per checkpoint");
+constexpr int kBwdRun = 8;
+static_assert(4 * kBwdRun % kGlrTile == 0 && kGlrTile % 16 == 0, "tiles begin at checkpoints");
 
 // Shared memory of a CTA: the runs of a tile (`sets` arrays, two buffers each),
 // the cluster's tiles (two buffers), the barriers, two stages.
@@ -642,10 +640,10 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
 // tiles from the last to the first.  The h_{t-1} of a tile are folded again
 // from the tile's checkpoint (the state before it, from the forward), so the
 // forward carry needs the first two levels only.
-template <typename T, int GATE, bool AL>
-__global__ void __launch_bounds__(32 * BwdShape::W, 16 / BwdShape::W)
+template <typename T, int GATE, bool AL, int W>
+__global__ void __launch_bounds__(32 * W, 16 / W)
     glr_bwd_kernel(const GlrArgs p, const __grid_constant__ ScanMaps maps) {
-  constexpr int RUN = BwdShape::RUN, W = BwdShape::W, ROWS = W * RUN;
+  constexpr int RUN = kBwdRun, ROWS = W * RUN;
   constexpr int N = GATE == kGateBeta ? 4 : 3;  // x, log_alpha, [beta,] dy
   constexpr int kBeta = 2, kDy = N - 1;
   using P = Piece<T, AL>;
@@ -695,7 +693,7 @@ __global__ void __launch_bounds__(32 * BwdShape::W, 16 / BwdShape::W)
     m.look(p, t0, lane);
     const bool inside = (m.first | m.last) == 0;
     f2 h = both(0.f);
-    if (tile >= 0) h = ch.get(p.checkpoints, tile, C);
+    if (tile >= 0) h = ch.get(p.checkpoints, tile * (ROWS / kGlrTile), C);
     ex.ok = stages.wait(step, ex.ok);
     char* st = stages.at + (int)(step & 1) * stages.kStage + warp * RUN * P::kPitch;
     const uint32_t rem = (uint32_t)t0 * row_bytes + (uint32_t)cb * (uint32_t)sizeof(T);
@@ -893,7 +891,7 @@ struct Scan {
   int threads, rows, smem;
 };
 
-enum : int { kFwd8 = 0, kFwd4 = 1, kBwd = 2 };
+enum : int { kFwd8 = 0, kFwd4 = 1, kBwd8 = 2, kBwd4 = 3, kScans = 4 };
 
 template <typename T, bool AL, int GATE, int W>
 Scan fwd_scan() {
@@ -901,13 +899,17 @@ Scan fwd_scan() {
   return {glr_fwd_kernel<T, GATE, AL, W>, 32 * W, rows,
           runs_bytes(W, 1) + kBarBytes + 2 * n * Piece<T, AL>::bytes(rows)};
 }
+template <typename T, bool AL, int GATE, int W>
+Scan bwd_scan() {
+  constexpr int rows = W * kBwdRun, n = GATE == kGateBeta ? 4 : 3;
+  return {glr_bwd_kernel<T, GATE, AL, W>, 32 * W, rows,
+          runs_bytes(W, 2) + kBarBytes + 2 * n * Piece<T, AL>::bytes(rows)};
+}
 template <typename T, bool AL, int GATE>
 Scan scan_of(int what) {
   if (what == kFwd8) return fwd_scan<T, AL, GATE, 8>();
   if (what == kFwd4) return fwd_scan<T, AL, GATE, 4>();
-  constexpr int W = BwdShape::W, rows = W * BwdShape::RUN, n = GATE == kGateBeta ? 4 : 3;
-  return {glr_bwd_kernel<T, GATE, AL>, 32 * W, rows,
-          runs_bytes(W, 2) + kBarBytes + 2 * n * Piece<T, AL>::bytes(rows)};
+  return what == kBwd8 ? bwd_scan<T, AL, GATE, 8>() : bwd_scan<T, AL, GATE, 4>();
 }
 template <typename T, bool AL>
 Scan scan_gate(int what, int gate) {
@@ -974,7 +976,7 @@ bool encode_map(CUtensorMap* m, const GlrArgs& a, const void* base, int rows) {
 // (asked once per device; the answers are the same whoever asks, so threads may
 // race).  -1: none of that size.
 constexpr int kMaxDevices = 64;
-constexpr int kVariants = 2 * 2 * 3 * 3;
+constexpr int kVariants = 2 * 2 * kScans * 3;
 std::atomic<int> g_fit[kMaxDevices][kVariants][kMaxCluster + 1];
 std::atomic<int> g_sms[kMaxDevices];
 
@@ -999,14 +1001,18 @@ int clusters_that_fit(int dev, int variant, const Scan& k, int cluster) {
 
 // How a scan is cut: its kernel and cluster size, by the least estimated time.
 //   steps of a cluster  x  waves of clusters  x  a step's time,
-// the latter by how many CTAs share an SM.  Measured on a B200 (bf16, gate
-// beta, us a step): 8 warps 2.1 alone and 2.85 by twos, 4 warps (half the
-// tokens) 1.46, 1.87, 2.26 and 2.6; a further wave costs about a tenth.  What
-// this settles, C = 6144, T = 32768, forward: 8 warps in clusters of 2 (one
-// wave, a third of the SMs with two CTAs) 336 us, of 8 (three waves) 311, 4
-// warps in clusters of 4 289; C = 2560, T = 65536: 8 warps in clusters of 6
-// 250, 4 warps in clusters of 8 282; backward, C = 6144, T = 32768: clusters
-// of 2 641, of 5 (two waves) 569.
+// the latter by how many CTAs share an SM.  Measured on a B200 (forward, bf16,
+// gate beta, us a step): 8 warps 2.1 alone and 2.85 by twos, 4 warps (half the
+// tokens) 1.46, 1.87, 2.26 and 2.6; a further wave costs about a tenth; the
+// backward's steps keep the proportions.  What this settles (us, bf16):
+//   forward, C = 6144, T = 32768: 8 warps in clusters of 2 (one wave, a third
+//     of the SMs with two CTAs) 338, of 8 (three waves) 303, 4 warps in
+//     clusters of 4 289;
+//   forward, C = 2560, T = 65536: 8 warps in clusters of 6 249, of 7 (a second
+//     wave for 3 of 40 groups) 338, 4 warps in clusters of 8 283;
+//   backward, C = 6144, T = 32768: 8 warps in clusters of 2 633, of 5 (two
+//     waves) 567, 4 warps in clusters of 5 517; C = 9216, T = 16384: 8 warps
+//     in clusters of 2 358, 4 warps in clusters of 7 391.
 struct Choice {
   Scan scan;
   int cluster;  // 0: none
@@ -1015,8 +1021,10 @@ struct Choice {
 
 Choice choose(int dev, int sms, const GlrArgs& a, bool al, int what, int groups) {
   static const double kStep8[] = {2.1, 2.85}, kStep4[] = {1.46, 1.87, 2.26, 2.6};
+  const bool small = what == kFwd4 || what == kBwd4;
   const Scan k = scan_for(a, al, what);
-  const int variant = (((a.dtype == GDN_BF16 ? 0 : 1) * 2 + (al ? 0 : 1)) * 3 + what) * 3 + a.gate;
+  const int variant =
+      (((a.dtype == GDN_BF16 ? 0 : 1) * 2 + (al ? 0 : 1)) * kScans + what) * 3 + a.gate;
   const int64_t n_tiles = (a.total_T + k.rows - 1) / k.rows;
   const int most = (int)(n_tiles < kMaxCluster ? (n_tiles < 1 ? 1 : n_tiles) : kMaxCluster);
   Choice best = {k, 0, 0.0};
@@ -1028,9 +1036,9 @@ Choice choose(int dev, int sms, const GlrArgs& a, bool al, int what, int groups)
     // fit (clusters lie within a GPC, so not all of its SMs' places are taken)
     const int per = (fit * r + sms - 1) / sms;
     int share = (at_once * per + fit - 1) / fit;
-    if (share > (what == kFwd4 ? 4 : 2)) share = what == kFwd4 ? 4 : 2;
+    if (share > (small ? 4 : 2)) share = small ? 4 : 2;
     const double cost = (double)((n_tiles + r - 1) / r) * waves * (1.0 + 0.1 * (waves - 1)) *
-                        (what == kFwd4 ? kStep4 : kStep8)[share - 1];
+                        (small ? kStep4 : kStep8)[share - 1];
     if (best.cluster == 0 || cost <= best.cost) best = {k, r, cost};
   }
   return best;
@@ -1048,11 +1056,9 @@ gdn_status launch_scan(const GlrArgs& a, bool bwd, cudaStream_t stream) {
     g_sms[dev].store(sms, std::memory_order_relaxed);
   }
   const int groups = (a.C + kChan - 1) / kChan;
-  Choice c = choose(dev, sms, a, al, bwd ? kBwd : kFwd8, groups);
-  if (!bwd) {
-    const Choice small = choose(dev, sms, a, al, kFwd4, groups);
-    if (small.cluster != 0 && (c.cluster == 0 || small.cost < c.cost)) c = small;
-  }
+  Choice c = choose(dev, sms, a, al, bwd ? kBwd8 : kFwd8, groups);
+  const Choice small = choose(dev, sms, a, al, bwd ? kBwd4 : kFwd4, groups);
+  if (small.cluster != 0 && (c.cluster == 0 || small.cost < c.cost)) c = small;
   if (c.cluster == 0) return GDN_ERR_CUDA;
   const Scan& k = c.scan;
   ScanMaps maps = {};

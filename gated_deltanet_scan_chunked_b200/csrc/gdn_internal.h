@@ -160,9 +160,8 @@ struct GrWriteArgs {
 
 size_t gr_read_workspace_bytes(int64_t T, int32_t n_r, int32_t d, int32_t rank);
 
-// Gated linear recurrence (gdn_glr.cu): tokens per tile, which is also how far
-// apart the forward's checkpoints lie.
-constexpr int kGlrTile = 64;
+// Gated linear recurrence (gdn_glr.cu): tokens from checkpoint to checkpoint.
+constexpr int kGlrTile = 32;
 constexpr int kGlrMaxChannels = 65535 * 32;  // groups of 32 channels along the grid
 
 struct GlrArgs {
@@ -178,7 +177,7 @@ struct GlrArgs {
   int32_t gate;                // gdn_glr_gate
   void* y;                     // nullptr: only checkpoints are written
   float* final_state;          // [n_seq, C] or nullptr; the step: the state, rewritten
-  float* checkpoints;          // [ceil(total_T / kGlrTile), C]: the state before each tile
+  float* checkpoints;          // [ceil(total_T / kGlrTile), C]: the state before every kGlrTile-th token
   const void* dy;
   const float* d_final_state;  // [n_seq, C] or nullptr (zeros)
   void* dx;

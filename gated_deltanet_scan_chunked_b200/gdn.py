@@ -590,7 +590,7 @@ def gdn_gr_write(codes, scales, y, s, stream=None):
 
 # --- gated linear recurrence, beam search -------------------------------------
 
-GLR_TILE = 64  # tokens between two checkpoints
+GLR_TILE = 32  # tokens between two checkpoints
 _GATE_NONE, _GATE_BETA, _GATE_COMPLEMENT = 0, 1, 2
 
 
@@ -662,7 +662,7 @@ def _glr_sequences(cu_seqlens, i):
 
 
 def glr_checkpoint_shape(total_T: int, C: int):
-    """Shape of the recurrence's checkpoints: [ceil(total_T / 64), C]."""
+    """Shape of the recurrence's checkpoints: [ceil(total_T / 32), C]."""
     return ((total_T + GLR_TILE - 1) // GLR_TILE, C)
 
 

@@ -499,8 +499,8 @@ typedef enum {
  *   C              channels (>= 1, any; at most 2,097,120)
  *   y              [total_T, C] in_dtype, written
  *   final_state    [n_seq, C] fp32 or NULL; may be initial_state exactly
- *   checkpoints    [ceil(total_T / 64), C] fp32 or NULL: the state before
- *                  every 64th packed token, which gdn_glr_bwd takes (their
+ *   checkpoints    [ceil(total_T / 32), C] fp32 or NULL: the state before
+ *                  every 32nd packed token, which gdn_glr_bwd takes (their
  *                  contents are otherwise unspecified)
  * Apart from final_state = initial_state, outputs must not overlap inputs or
  * each other.  One kernel; every element is read once and written once.

@@ -92,11 +92,11 @@ def test_step_rejects(lib, kw, code):
 def test_workspace_and_checkpoint_sizes(lib):
     assert gdn.glr_bwd_workspace_size(0, 10) == 0
     assert gdn.glr_bwd_workspace_size(1, 10) == 256
-    assert gdn.glr_bwd_workspace_size(4096, 2560) == 64 * 2560 * 4
+    assert gdn.glr_bwd_workspace_size(4096, 2560) == 128 * 2560 * 4
     assert gdn.glr_bwd_workspace_size(-1, 10) == 0
     assert gdn.glr_bwd_workspace_size(10, 0) == 0
-    assert gdn.glr_checkpoint_shape(64, 5) == (1, 5)
-    assert gdn.glr_checkpoint_shape(65, 5) == (2, 5)
+    assert gdn.glr_checkpoint_shape(32, 5) == (1, 5)
+    assert gdn.glr_checkpoint_shape(33, 5) == (2, 5)
 
 
 def test_binding_refuses_cpu_tensors(lib):
