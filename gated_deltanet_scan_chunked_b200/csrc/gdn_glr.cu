@@ -487,11 +487,11 @@ __device__ __forceinline__ void empty_sequences(const GlrArgs& p, const float* i
 
 // Tokens of a thread's run.  The forward holds a and b x of its run in registers
 // (4 a token), the backward more.  Both come with 4 and with 8 warps to a CTA;
-// the backward's tiles begin at checkpoints.
-template <typename T>
-constexpr int fwd_run() { return sizeof(T) == 2 ? 16 : 8; }
-constexpr int kBwdRun = 8;
-static_assert(4 * kBwdRun % kGlrTile == 0 && kGlrTile % 16 == 0, "tiles begin at checkpoints");
+// the backward's tiles begin at checkpoints.  (Forward runs of 8 tokens in
+// fp32 against 16: 20011 tokens of 24 sequences, C = 1336 98 us for 74, with beta
+// 90 for 76, C = 1333 115 for 104, C = 2560 110 for 109; C = 6144 both 263.)
+constexpr int kFwdRun = 16, kBwdRun = 8;
+static_assert(4 * kBwdRun % kGlrTile == 0 && kGlrTile % kFwdRun == 0, "checkpoints at runs");
 
 // Shared memory of a CTA: the runs of a tile (`sets` arrays, two buffers each),
 // the cluster's tiles (two buffers), the barriers, two stages.
@@ -503,7 +503,7 @@ static_assert(runs_bytes(1, 1) % 128 == 0 && tiles_bytes(1) % 128 == 0, "stages 
 template <typename T, int GATE, bool AL, int W>
 __global__ void __launch_bounds__(32 * W, 16 / W)
     glr_fwd_kernel(const GlrArgs p, const __grid_constant__ ScanMaps maps) {
-  constexpr int RUN = fwd_run<T>(), ROWS = W * RUN;
+  constexpr int RUN = kFwdRun, ROWS = W * RUN;
   constexpr int N = GATE == kGateBeta ? 3 : 2;
   using P = Piece<T, AL>;
   extern __shared__ __align__(128) char smem[];
@@ -895,7 +895,7 @@ enum : int { kFwd8 = 0, kFwd4 = 1, kBwd8 = 2, kBwd4 = 3, kScans = 4 };
 
 template <typename T, bool AL, int GATE, int W>
 Scan fwd_scan() {
-  constexpr int rows = W * fwd_run<T>(), n = GATE == kGateBeta ? 3 : 2;
+  constexpr int rows = W * kFwdRun, n = GATE == kGateBeta ? 3 : 2;
   return {glr_fwd_kernel<T, GATE, AL, W>, 32 * W, rows,
           runs_bytes(W, 1) + kBarBytes + 2 * n * Piece<T, AL>::bytes(rows)};
 }
@@ -986,12 +986,15 @@ int clusters_that_fit(int dev, int variant, const Scan& k, int cluster) {
   if (n != 0) return n;
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg = scan_config(k, cluster, 1, nullptr, &attr);
-  if (cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           k.smem + tiles_bytes(kMaxCluster)) != cudaSuccess ||
-      cudaFuncSetAttribute(k.kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
-          cudaSuccess)
+  int most = 0;  // (of shared memory; a shape that needs more is not used)
+  if (cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess)
     return -1;
-  if (cudaOccupancyMaxActiveClusters(&n, k.kernel, &cfg) != cudaSuccess || n < 1) {
+  if (k.smem + tiles_bytes(cluster) > most ||
+      cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) !=
+          cudaSuccess ||
+      cudaFuncSetAttribute(k.kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+          cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, k.kernel, &cfg) != cudaSuccess || n < 1) {
     cudaGetLastError();  // (a size that the device cannot hold)
     n = -1;
   }
