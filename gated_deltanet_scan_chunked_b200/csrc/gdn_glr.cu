@@ -199,14 +199,27 @@ struct __align__(16) Run {
   f2 A, h;
 };
 
-// h behind a run that is entered with h.  CUT (a packed batch): a run whose A is
-// 0 forgets what was before it, even an infinity or NaN: those belong to
-// another sequence.
+// A run that a sequence's border cuts has A = -0 in its first channel (products
+// of a, which is never negative, have no sign): it forgets what was before it,
+// even an infinity or NaN, since those belong to another sequence.  A product
+// that falls to +0 inside a sequence does not: 0 x NaN stays NaN there, as in
+// the recurrence.  CUT: a packed batch, which alone has anything to forget.
+__device__ __forceinline__ f2 cut_A() { return both(-0.f); }
+
+// h behind a run that is entered with h.
 template <bool CUT>
 __device__ __forceinline__ f2 through(const Run& r, f2 h) {
   const f2 n = fma2(r.A, h, r.h);
-  if (!CUT) return n;
-  return make_float2(r.A.x == 0.f ? r.h.x : n.x, r.A.y == 0.f ? r.h.y : n.y);
+  return CUT && __float_as_int(r.A.x) < 0 ? r.h : n;
+}
+// A of two runs, one behind the other.
+template <bool CUT>
+__device__ __forceinline__ f2 behind_A(f2 a, f2 b) {
+  f2 r = mul2(a, b);
+  if (CUT)
+    r.x = __int_as_float(__float_as_int(r.x) |
+                         ((__float_as_int(a.x) | __float_as_int(b.x)) & (int)0x80000000));
+  return r;
 }
 
 // A lane's two channels: neighbours where rows are aligned, else 32 apart.
@@ -403,7 +416,7 @@ __device__ __forceinline__ void fold_tile(const Run (*runs)[32], int lane, int w
     if (w == warp) before = all;
     const Run r = runs[w][lane];
     all.h = through<CUT>(r, all.h);
-    all.A = mul2(all.A, r.A);
+    all.A = behind_A<CUT>(all.A, r.A);
   }
 }
 
@@ -571,7 +584,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
         const f2 h0 = ch.get(p.initial_state, m.seq_of(k), C);
         replace(u, k, fma2(pick(a, k), h0, pick(u, k)));
       }
-      run.A = both(0.f);
+      run.A = cut_A();
 #pragma unroll
       for (int i = 0; i < RUN; ++i)
         run.h = (m.first >> i & 1) ? u[i] : fma2(a[i], run.h, u[i]);
@@ -733,14 +746,14 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
 #pragma unroll
       for (int i = RUN - 1; i >= 0; --i)
         rr.h = mul2(a[i], (m.last >> i & 1) ? d[i] : add2(d[i], rr.h));
-      if (m.last != 0) rr.A = both(0.f);
+      if (m.last != 0) rr.A = cut_A();
       if (m.first != 0) {  // as in the forward
         for (uint32_t f = m.first; f != 0; f &= f - 1) {
           const int k = __ffs((int)f) - 1;
           const f2 h0 = ch.get(p.initial_state, m.seq_of(k), C);
           replace(u, k, fma2(pick(a, k), h0, pick(u, k)));
         }
-        fr.A = both(0.f);
+        fr.A = cut_A();
 #pragma unroll
         for (int i = 0; i < RUN; ++i)
           fr.h = (m.first >> i & 1) ? u[i] : fma2(a[i], fr.h, u[i]);

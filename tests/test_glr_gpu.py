@@ -211,6 +211,28 @@ def test_infinities_and_nan_stay_in_their_sequence():
         assert torch.equal(d[k][70:200, [4, 5, 6, 7]], d0[k][70:200, [4, 5, 6, 7]]), k
 
 
+@pytest.mark.parametrize("C", [32, 33])
+@pytest.mark.parametrize("packed", [True, False])
+def test_nan_is_not_forgotten_where_the_decays_underflow(C, packed):
+    """exp(-20) is not 0, so a NaN stays to the end of its sequence (backward: to
+    its beginning), although products of a few such decays are 0 in fp32."""
+    lens = [100, 900, 200] if packed else [1200]
+    p = make(19, lens, C, "none", F32)
+    p["log_alpha"][:] = -20.0
+    p["x"][150, 3] = p["dy"][950, 4] = float("nan")
+    p["x"][170, 5] = float("inf")
+    lo, hi = (100, 1000) if packed else (0, 1200)
+    y, hT, _ = forward(p)
+    d = backward(p)["dx"]
+    for c, at in ((3, 150), (5, 170)):
+        assert not torch.isfinite(y[at:hi, c]).any()
+        assert torch.isfinite(y[:at, c]).all() and torch.isfinite(y[hi:, c]).all()
+        assert not torch.isfinite(hT[1 if packed else 0, c])
+    assert torch.isnan(y[150:hi, 3]).all()
+    assert torch.isnan(d[lo:951, 4]).all()
+    assert torch.isfinite(d[951:, 4]).all() and torch.isfinite(d[:lo, 4]).all()
+
+
 def test_in_place_state_equals_separate():
     p = make(17, [100, 0, 1, 200], 50, "beta", BF16)
     y, hT, _ = forward(p)
