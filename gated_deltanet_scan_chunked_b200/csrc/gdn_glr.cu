@@ -298,11 +298,15 @@ struct ScanMaps {
 
 // Two stages of N input tensors' tiles of ROWS tokens.  Tokens outside [0, T)
 // become zeros: a = exp(0) = 1 and x = 0 leave a state as it is.  Loads are
-// numbered by step; step s goes to stage s & 1.
-template <typename T, bool AL, int ROWS, int N, int THREADS>
+// numbered by step; step s goes to stage s & 1.  APART: the outputs are not left in
+// the inputs' places but (AL) in room of their own behind the stages, or (else)
+// are stored from registers, and the inputs are read once: a stage may be filled
+// again in the middle of its own step, for the step after the next.
+template <typename T, bool AL, int ROWS, int N, int THREADS, bool APART>
 struct Stages {
   using P = Piece<T, AL>;
   static constexpr int kTensor = P::bytes(ROWS), kStage = N * kTensor;
+  static constexpr int kBytes = 2 * kStage + (AL && APART ? kTensor : 0);
   char* at;
   uint64_t* full;  // [2] (AL)
 
@@ -323,13 +327,20 @@ struct Stages {
     if constexpr (AL) {
       if (any && threadIdx.x == 0) {
         uint64_t* bar = &full[step & 1];
-        sm100::bulk_wait_read_all();
+        if (!APART) sm100::bulk_wait_read_all();
         sm100::mbar_arrive_expect_tx(bar, kStage);
 #pragma unroll
         for (int k = 0; k < N; ++k)
           sm100::tma_load_2d(stage + k * kTensor, &maps.in[k], cb, (int)t0, bar);
       }
-    } else if (any) {
+    } else {
+      if (any) copy(stage, src, t0, total_T, C, cb);
+      sm100::cp_async_commit();
+    }
+  }
+  __device__ __forceinline__ void copy(uint32_t stage, const char* const (&src)[N], int64_t t0,
+                                       int64_t total_T, int C, int cb) {
+    if constexpr (!AL) {
       // a thread has one 16-byte column of every kRows-th row
       constexpr int kRows = THREADS / P::kCopies;
       const int q = (int)threadIdx.x % P::kCopies, r0 = (int)threadIdx.x / P::kCopies;
@@ -369,13 +380,18 @@ struct Stages {
     if constexpr (AL) {
       return ok && sm100::mbar_wait(&full[step & 1], (uint32_t)(step >> 1) & 1u, kWait);
     } else {
-      sm100::cp_async_wait_all();
+      if (APART) sm100::cp_async_wait_group1();  // (the next step's may be under way)
+      else sm100::cp_async_wait_all();
       __syncthreads();
       return ok;
     }
   }
-  // (by every thread, its outputs in the places of the first `n` inputs; AL)
-  // Sends the tile of step `step` off.
+  // (by thread 0, before a barrier in front of the next outputs; AL, APART) The
+  // last ones have left.
+  __device__ __forceinline__ void free_outputs() {
+    if (AL && APART && threadIdx.x == 0) sm100::bulk_wait_read_all();
+  }
+  // (by every thread, its outputs in place; AL) Sends the tile of step `step` off.
   __device__ __forceinline__ void store(int64_t step, int n, const ScanMaps& maps, int64_t t0,
                                         int cb) {
     sm100::fence_proxy_async();  // the outputs, before the copies read them
@@ -385,7 +401,7 @@ struct Stages {
     }
     sm100::named_sync(1, THREADS);
     if (threadIdx.x == 0) {
-      const uint32_t stage = sm100::smem_u32(at) + (uint32_t)(step & 1) * kStage;
+      const uint32_t stage = sm100::smem_u32(at) + (APART ? 2u : (uint32_t)(step & 1)) * kStage;
       for (int k = 0; k < n; ++k)
         sm100::tma_store_2d(&maps.out[k], cb, (int)t0, stage + k * kTensor);
       sm100::bulk_commit();
@@ -513,6 +529,29 @@ constexpr int tiles_bytes(int cluster) { return 2 * cluster * 32 * (int)sizeof(R
 constexpr int kBarBytes = 128;
 static_assert(runs_bytes(1, 1) % 128 == 0 && tiles_bytes(1) % 128 == 0, "stages on 128 bytes");
 
+// CTAs of an SM (of 128 registers a thread, in clusters of 8) with that much
+// shared memory for the stages.
+constexpr int ctas_of_sm(int w, int stages) {
+  const int fit = 227 * 1024 / (runs_bytes(w, 1) + tiles_bytes(8) + kBarBytes + stages + 1024);
+  return fit < 16 / w ? fit : 16 / w;
+}
+// The forward's outputs get room apart where that costs no CTA of an SM: loads
+// then have a step and a half to arrive, not a half (bf16, gate beta, us, apart
+// against in place: 4 warps, C = 6144, T = 32768 263 for 290, C = 2560, T = 131072
+// 444 for 483; 8 warps, two CTAs of an SM in place and one apart, C = 9216, T =
+// 16384 216 for 199; fp32, gate beta, 4 warps likewise, C = 2560, T = 32768 233
+// for 210).
+template <typename T, int GATE, bool AL, int W, bool APART>
+using FwdStagesOf = Stages<T, AL, W * kFwdRun, GATE == kGateBeta ? 3 : 2, 32 * W, APART>;
+template <typename T, int GATE, bool AL, int W>
+constexpr bool kFwdApart = ctas_of_sm(W, FwdStagesOf<T, GATE, AL, W, true>::kBytes) ==
+                           ctas_of_sm(W, FwdStagesOf<T, GATE, AL, W, false>::kBytes);
+template <typename T, int GATE, bool AL, int W>
+using FwdStages = FwdStagesOf<T, GATE, AL, W, kFwdApart<T, GATE, AL, W>>;
+static_assert(kFwdApart<float, kGateBeta, false, 8>, "outputs from registers cost no room");
+template <typename T, int GATE, bool AL, int W>
+using BwdStages = Stages<T, AL, W * kBwdRun, GATE == kGateBeta ? 4 : 3, 32 * W, false>;
+
 template <typename T, int GATE, bool AL, int W>
 __global__ void __launch_bounds__(32 * W, 16 / W)
     glr_fwd_kernel(const GlrArgs p, const __grid_constant__ ScanMaps maps) {
@@ -528,7 +567,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
   ex.rank = rank;
   ex.tiles = run_buf + 2 * W;
   ex.bar = reinterpret_cast<uint64_t*>(ex.tiles + 2 * n_cta);
-  Stages<T, AL, ROWS, N, 32 * W> stages;
+  FwdStages<T, GATE, AL, W> stages;
   stages.full = ex.bar + 2;
   stages.at = reinterpret_cast<char*>(ex.bar) + kBarBytes;
 
@@ -561,6 +600,9 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
     const bool inside = (m.first | m.last) == 0;
     ex.ok = stages.wait(step, ex.ok);
     char* st = stages.at + (int)(step & 1) * stages.kStage + warp * RUN * P::kPitch;
+    [[maybe_unused]] char* to = kFwdApart<T, GATE, AL, W>
+                                    ? stages.at + 2 * stages.kStage + warp * RUN * P::kPitch
+                                    : st;
     const uint32_t rem = (uint32_t)t0 * row_bytes + (uint32_t)cb * (uint32_t)sizeof(T);
     auto in = [&](int k, int i) {  // tensor k at token i of the run
       return P::get(st + k * stages.kTensor + i * P::kPitch,
@@ -593,8 +635,12 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
     // the next one's)
     Run(*runs)[32] = run_buf + (int)(step & 1) * W;
     runs[warp][lane] = run;
-    __syncthreads();  // the runs are complete; the step before is done with its stage
-    if (step > 0) load(step + 1);
+    stages.free_outputs();
+    // the runs are complete; this step's inputs are read, the step before is done
+    // with its stage
+    __syncthreads();
+    if (kFwdApart<T, GATE, AL, W>) load(step + 2);
+    else if (step > 0) load(step + 1);
     f2 h;
     if (p.cu_seqlens == nullptr) {
       const Run before = ex.template give<W, false, false>(step, lane, warp, runs);
@@ -610,7 +656,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
     [[maybe_unused]] const int n_tok = T_ - t0 < RUN ? (int)(T_ - t0) : RUN;
     auto out = [&](int i) {  // (called with i ascending)
       if constexpr (AL) {
-        P::put(st + i * P::kPitch, lane, h);
+        P::put(to + i * P::kPitch, lane, h);
       } else {
         if (i < n_tok) put_out<T>(y, ch, h);
         y += C;
@@ -669,7 +715,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
   ex.rank = rank;
   ex.tiles = run_buf + 4 * W;
   ex.bar = reinterpret_cast<uint64_t*>(ex.tiles + 2 * n_cta);
-  Stages<T, AL, ROWS, N, 32 * W> stages;
+  BwdStages<T, GATE, AL, W> stages;
   stages.full = ex.bar + 2;
   stages.at = reinterpret_cast<char*>(ex.bar) + kBarBytes;
 
@@ -908,15 +954,15 @@ enum : int { kFwd8 = 0, kFwd4 = 1, kBwd8 = 2, kBwd4 = 3, kScans = 4 };
 
 template <typename T, bool AL, int GATE, int W>
 Scan fwd_scan() {
-  constexpr int rows = W * kFwdRun, n = GATE == kGateBeta ? 3 : 2;
+  constexpr int rows = W * kFwdRun;
   return {glr_fwd_kernel<T, GATE, AL, W>, 32 * W, rows,
-          runs_bytes(W, 1) + kBarBytes + 2 * n * Piece<T, AL>::bytes(rows)};
+          runs_bytes(W, 1) + kBarBytes + FwdStages<T, GATE, AL, W>::kBytes};
 }
 template <typename T, bool AL, int GATE, int W>
 Scan bwd_scan() {
-  constexpr int rows = W * kBwdRun, n = GATE == kGateBeta ? 4 : 3;
+  constexpr int rows = W * kBwdRun;
   return {glr_bwd_kernel<T, GATE, AL, W>, 32 * W, rows,
-          runs_bytes(W, 2) + kBarBytes + 2 * n * Piece<T, AL>::bytes(rows)};
+          runs_bytes(W, 2) + kBarBytes + BwdStages<T, GATE, AL, W>::kBytes};
 }
 template <typename T, bool AL, int GATE>
 Scan scan_of(int what) {
@@ -1018,14 +1064,15 @@ int clusters_that_fit(int dev, int variant, const Scan& k, int cluster) {
 // How a scan is cut: its kernel and cluster size, by the least estimated time.
 //   steps of a cluster  x  waves of clusters  x  a step's time,
 // the latter by how many CTAs share an SM.  Measured on a B200 (forward, bf16,
-// gate beta, us a step): 8 warps 2.1 alone and 2.85 by twos, 4 warps (half the
-// tokens) 1.46, 1.87, 2.26 and 2.6; a further wave costs about a tenth; the
-// backward's steps keep the proportions.  What this settles (us, bf16):
+// gate beta, us a step): 8 warps 2.05 alone and 2.85 by twos, 4 warps (half the
+// tokens) 1.28, 1.65, 2.1 and 2.5; a further wave costs about a tenth; the
+// backward's 4 warps are slower by comparison.  What this settles (us, bf16):
 //   forward, C = 6144, T = 32768: 8 warps in clusters of 2 (one wave, a third
-//     of the SMs with two CTAs) 338, of 8 (three waves) 303, 4 warps in
-//     clusters of 4 289;
-//   forward, C = 2560, T = 65536: 8 warps in clusters of 6 249, of 7 (a second
-//     wave for 3 of 40 groups) 338, 4 warps in clusters of 8 283;
+//     of the SMs with two CTAs) 336, of 8 (three waves) 307, 4 warps in
+//     clusters of 4 263;
+//   forward, C = 2560, T = 131072: 8 warps in clusters of 6 487, of 7 (a second
+//     wave for 3 of 40 groups) 668, 4 warps in clusters of 10 444;
+//   forward, C = 9216, T = 16384: 8 warps in clusters of 2 199, 4 warps 211;
 //   backward, C = 6144, T = 32768: 8 warps in clusters of 2 633, of 5 (two
 //     waves) 567, 4 warps in clusters of 5 517; C = 9216, T = 16384: 8 warps
 //     in clusters of 2 358, 4 warps in clusters of 7 391.
@@ -1036,8 +1083,10 @@ struct Choice {
 };
 
 Choice choose(int dev, int sms, const GlrArgs& a, bool al, int what, int groups) {
-  static const double kStep8[] = {2.1, 2.85}, kStep4[] = {1.46, 1.87, 2.26, 2.6};
+  static const double kStep8[] = {2.05, 2.85}, kFwdStep4[] = {1.28, 1.65, 2.1, 2.5},
+                      kBwdStep4[] = {1.46, 1.87, 2.26, 2.6};
   const bool small = what == kFwd4 || what == kBwd4;
+  const double* step_us = what == kFwd4 ? kFwdStep4 : what == kBwd4 ? kBwdStep4 : kStep8;
   const Scan k = scan_for(a, al, what);
   const int variant =
       (((a.dtype == GDN_BF16 ? 0 : 1) * 2 + (al ? 0 : 1)) * kScans + what) * 3 + a.gate;
@@ -1054,7 +1103,7 @@ Choice choose(int dev, int sms, const GlrArgs& a, bool al, int what, int groups)
     int share = (at_once * per + fit - 1) / fit;
     if (share > (small ? 4 : 2)) share = small ? 4 : 2;
     const double cost = (double)((n_tiles + r - 1) / r) * waves * (1.0 + 0.1 * (waves - 1)) *
-                        (small ? kStep4 : kStep8)[share - 1];
+                        step_us[share - 1];
     if (best.cluster == 0 || cost <= best.cost) best = {k, r, cost};
   }
   return best;
