@@ -983,12 +983,12 @@ Scan scan_for(const GlrArgs& a, bool al, int what) {
   return al ? scan_gate<float, true>(what, a.gate) : scan_gate<float, false>(what, a.gate);
 }
 
-cudaLaunchConfig_t scan_config(const Scan& k, int cluster, int groups, cudaStream_t stream,
-                               cudaLaunchAttribute* attr) {
+cudaLaunchConfig_t scan_config(const Scan& k, int cluster, int smem, int groups,
+                               cudaStream_t stream, cudaLaunchAttribute* attr) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)cluster, (unsigned)groups);
   cfg.blockDim = dim3((unsigned)k.threads);
-  cfg.dynamicSmemBytes = (size_t)(k.smem + tiles_bytes(cluster));
+  cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = stream;
   attr->id = cudaLaunchAttributeClusterDimension;
   attr->val.clusterDim.x = (unsigned)cluster;
@@ -1031,24 +1031,50 @@ bool encode_map(CUtensorMap* m, const GlrArgs& a, const void* base, int rows) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Clusters of each size that the device holds at once, per kernel, and its SMs
-// (asked once per device; the answers are the same whoever asks, so threads may
-// race).  -1: none of that size.
-constexpr int kMaxDevices = 64;
+// What is known of a device (asked once; the answers are the same whoever asks,
+// so threads may race): its shared memory, and how many clusters of each kernel,
+// size and share of an SM it holds at once (-1: none).
+constexpr int kMaxDevices = 64, kMaxShare = 4;
 constexpr int kVariants = 2 * 2 * kScans * 3;
-std::atomic<int> g_fit[kMaxDevices][kVariants][kMaxCluster + 1];
-std::atomic<int> g_sms[kMaxDevices];
+struct Device {
+  std::atomic<int> of_block, of_sm, reserved;  // bytes: most of a block, of an SM, a block's own
+  std::atomic<int> fit[kVariants][kMaxShare][kMaxCluster + 1];
+};
+Device g_device[kMaxDevices];
 
-int clusters_that_fit(int dev, int variant, const Scan& k, int cluster) {
-  std::atomic<int>& slot = g_fit[dev][variant][cluster];
+bool know_device(int dev) {
+  Device& d = g_device[dev];
+  if (d.of_block.load(std::memory_order_acquire) != 0) return true;
+  int block = 0, sm = 0, own = 0;
+  if (cudaDeviceGetAttribute(&block, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) !=
+          cudaSuccess ||
+      cudaDeviceGetAttribute(&sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev) !=
+          cudaSuccess ||
+      cudaDeviceGetAttribute(&own, cudaDevAttrReservedSharedMemoryPerBlock, dev) != cudaSuccess)
+    return false;
+  d.of_sm.store(sm, std::memory_order_relaxed);
+  d.reserved.store(own, std::memory_order_relaxed);
+  d.of_block.store(block, std::memory_order_release);
+  return true;
+}
+
+// Shared memory of a CTA of which an SM shall hold at most `share`.
+int shared_bytes(const Device& d, const Scan& k, int cluster, int share) {
+  const int need = k.smem + tiles_bytes(cluster);
+  const int least = d.of_sm.load(std::memory_order_relaxed) / (share + 1) -
+                    d.reserved.load(std::memory_order_relaxed) + 128;
+  return need > least ? need : least;
+}
+
+int clusters_that_fit(int dev, int variant, const Scan& k, int cluster, int share) {
+  std::atomic<int>& slot = g_device[dev].fit[variant][share - 1][cluster];
   int n = slot.load(std::memory_order_relaxed);
   if (n != 0) return n;
+  const int smem = shared_bytes(g_device[dev], k, cluster, share);
+  const int most = g_device[dev].of_block.load(std::memory_order_relaxed);
   cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = scan_config(k, cluster, 1, nullptr, &attr);
-  int most = 0;  // (of shared memory; a shape that needs more is not used)
-  if (cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess)
-    return -1;
-  if (k.smem + tiles_bytes(cluster) > most ||
+  const cudaLaunchConfig_t cfg = scan_config(k, cluster, smem, 1, nullptr, &attr);
+  if (smem > most ||
       cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) !=
           cudaSuccess ||
       cudaFuncSetAttribute(k.kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
@@ -1061,12 +1087,17 @@ int clusters_that_fit(int dev, int variant, const Scan& k, int cluster) {
   return n;
 }
 
-// How a scan is cut: its kernel and cluster size, by the least estimated time.
+// How a scan is cut: its kernel, cluster size and CTAs of an SM, by the least
+// estimated time,
 //   steps of a cluster  x  waves of clusters  x  a step's time,
-// the latter by how many CTAs share an SM.  Measured on a B200 (forward, bf16,
-// gate beta, us a step): 8 warps 2.05 alone and 2.85 by twos, 4 warps (half the
-// tokens) 1.28, 1.65, 2.1 and 2.5; a further wave costs about a tenth; the
-// backward's 4 warps are slower by comparison.  What this settles (us, bf16):
+// the latter by how many CTAs share an SM.  Clusters are not spread evenly: of
+// eight clusters of 16 CTAs two to an SM, some lie together on a few SMs and the
+// others' steps are half as long; so no more CTAs are let onto an SM than the
+// choice counts on, by the shared memory asked for.  Measured on a B200
+// (forward, bf16, gate beta, us a step): 8 warps 2.05 alone and 2.85 by twos, 4
+// warps (half the tokens) 1.28, 1.65, 2.1 and 2.5; a further wave costs about a
+// tenth; the backward's 4 warps are slower by comparison.  What this settles
+// (us, bf16):
 //   forward, C = 6144, T = 32768: 8 warps in clusters of 2 (one wave, a third
 //     of the SMs with two CTAs) 336, of 8 (three waves) 307, 4 warps in
 //     clusters of 4 263;
@@ -1078,11 +1109,11 @@ int clusters_that_fit(int dev, int variant, const Scan& k, int cluster) {
 //     in clusters of 2 358, 4 warps in clusters of 7 391.
 struct Choice {
   Scan scan;
-  int cluster;  // 0: none
+  int cluster, smem;  // cluster 0: none
   double cost;
 };
 
-Choice choose(int dev, int sms, const GlrArgs& a, bool al, int what, int groups) {
+Choice choose(int dev, const GlrArgs& a, bool al, int what, int groups) {
   static const double kStep8[] = {2.05, 2.85}, kFwdStep4[] = {1.28, 1.65, 2.1, 2.5},
                       kBwdStep4[] = {1.46, 1.87, 2.26, 2.6};
   const bool small = what == kFwd4 || what == kBwd4;
@@ -1092,20 +1123,17 @@ Choice choose(int dev, int sms, const GlrArgs& a, bool al, int what, int groups)
       (((a.dtype == GDN_BF16 ? 0 : 1) * 2 + (al ? 0 : 1)) * kScans + what) * 3 + a.gate;
   const int64_t n_tiles = (a.total_T + k.rows - 1) / k.rows;
   const int most = (int)(n_tiles < kMaxCluster ? (n_tiles < 1 ? 1 : n_tiles) : kMaxCluster);
-  Choice best = {k, 0, 0.0};
-  for (int r = 1; r <= most; ++r) {
-    const int fit = clusters_that_fit(dev, variant, k, r);
-    if (fit < 1) continue;
-    const int at_once = fit < groups ? fit : groups, waves = (groups + fit - 1) / fit;
-    // CTAs of an SM: of the `per` that it holds, the part of the clusters that
-    // fit (clusters lie within a GPC, so not all of its SMs' places are taken)
-    const int per = (fit * r + sms - 1) / sms;
-    int share = (at_once * per + fit - 1) / fit;
-    if (share > (small ? 4 : 2)) share = small ? 4 : 2;
-    const double cost = (double)((n_tiles + r - 1) / r) * waves * (1.0 + 0.1 * (waves - 1)) *
-                        step_us[share - 1];
-    if (best.cluster == 0 || cost <= best.cost) best = {k, r, cost};
-  }
+  Choice best = {k, 0, 0, 0.0};
+  for (int share = 1; share <= (small ? kMaxShare : 2); ++share)
+    for (int r = 1; r <= most; ++r) {
+      const int fit = clusters_that_fit(dev, variant, k, r, share);
+      if (fit < 1) continue;
+      const int waves = (groups + fit - 1) / fit;
+      const double cost = (double)((n_tiles + r - 1) / r) * waves * (1.0 + 0.1 * (waves - 1)) *
+                          step_us[share - 1];
+      if (best.cluster == 0 || cost < best.cost)
+        best = {k, r, shared_bytes(g_device[dev], k, r, share), cost};
+    }
   return best;
 }
 
@@ -1114,15 +1142,10 @@ gdn_status launch_scan(const GlrArgs& a, bool bwd, cudaStream_t stream) {
   const bool al = (int64_t)a.C * (bf16 ? 2 : 4) % 16 == 0;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return GDN_ERR_CUDA;
-  int sms = g_sms[dev].load(std::memory_order_relaxed);
-  if (sms == 0) {
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-      return GDN_ERR_CUDA;
-    g_sms[dev].store(sms, std::memory_order_relaxed);
-  }
+  if (!know_device(dev)) return GDN_ERR_CUDA;
   const int groups = (a.C + kChan - 1) / kChan;
-  Choice c = choose(dev, sms, a, al, bwd ? kBwd8 : kFwd8, groups);
-  const Choice small = choose(dev, sms, a, al, bwd ? kBwd4 : kFwd4, groups);
+  Choice c = choose(dev, a, al, bwd ? kBwd8 : kFwd8, groups);
+  const Choice small = choose(dev, a, al, bwd ? kBwd4 : kFwd4, groups);
   if (small.cluster != 0 && (c.cluster == 0 || small.cost < c.cost)) c = small;
   if (c.cluster == 0) return GDN_ERR_CUDA;
   const Scan& k = c.scan;
@@ -1140,7 +1163,7 @@ gdn_status launch_scan(const GlrArgs& a, bool bwd, cudaStream_t stream) {
       if (!encode_map(&maps.out[i], a, out[i], k.rows)) return GDN_ERR_CUDA;
   }
   cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = scan_config(k, c.cluster, groups, stream, &attr);
+  const cudaLaunchConfig_t cfg = scan_config(k, c.cluster, c.smem, groups, stream, &attr);
   return cudaLaunchKernelEx(&cfg, k.kernel, a, maps) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
