@@ -111,70 +111,86 @@ __device__ __forceinline__ int seq_at(const int32_t* cu, int n_seq, int64_t t) {
 }
 
 // Which of a run's tokens from t0 on begin or end a sequence (bit i: token
-// t0 + i; tokens outside [0, total_T) neither); lane i has token i's sequence.
-// The sequence that the walk has come to and its bounds [lo, hi) are kept: most
-// runs lie inside it and need no look at the offsets.  Another run's
-// sequences are counted from there over the next 31 offsets, read in one load;
-// only where those are not enough are they searched for.
+// t0 + i; tokens outside [0, total_T) neither).  The sequence that the walk has
+// come to and its bounds [lo, hi) are kept: most runs of long sequences lie
+// inside it and need no look at the offsets.  For another run a lane has one of
+// the 32 offsets beyond them: those that fall into the run are its marks, and a
+// token's sequence is counted from the walk's over those up to it.  Only where
+// 32 are not enough are sequences searched for.
 template <int RUN, bool BACK>
 struct Marks {
   uint32_t first = 0, last = 0;
-  int seq = 0;           // (lane i) of token i
-  int at = -1;           // of the walk's last token, -1: none yet
-  int64_t lo = 0, hi = 0;
+  int at;       // sequence of the walk's last token; before the first, none
+  int lo, hi;   // its bounds
+  int from;     // (this run's) the walk's sequence before the run; none: searched for
+  int off;      // (this lane's) an offset beyond it; searched for: token `lane`'s sequence
+  static constexpr int kSearched = -2;
+
+  __device__ __forceinline__ explicit Marks(const GlrArgs& p)
+      : at(BACK ? p.n_seq : -1), lo(BACK ? 0x7fffffff : 0), hi(BACK ? 0x7fffffff : 0), from(at) {}
 
   __device__ __forceinline__ void look(const GlrArgs& p, int64_t t0, int lane) {
     first = last = 0;
+    if (t0 < 0 || t0 >= p.total_T) return;
+    const int t = (int)t0, n = p.total_T - t0 < RUN ? (int)(p.total_T - t0) : RUN;
     if (p.cu_seqlens == nullptr) {
-      if (t0 <= 0 && t0 + RUN > 0) first = 1u << (int)(-t0);
-      const int64_t d = p.total_T - 1 - t0;
-      if (d >= 0 && d < RUN) last = 1u << (int)d;
+      if (t == 0) first = 1;
+      if (t0 + RUN >= p.total_T) last = 1u << (n - 1);
       return;
     }
-    if (lo < t0 && t0 + RUN < hi) return;
-    const int64_t t = t0 + lane;
-    const bool in = lane < RUN && t >= 0 && t < p.total_T;
-    int64_t l = 0, h = 0;
-    bool found = false;  // (the same in every lane)
-    if (at >= 0) {
-      // offset `at + 1 + lane` ahead, or `at - lane` behind; of offsets 0 ..
-      // n_seq those below n_seq count
-      const int i = BACK ? at - lane : at + 1 + lane;
-      const int64_t off = i < 0 ? -1 : i > p.n_seq ? (int64_t)1 << 62 : __ldg(p.cu_seqlens + i);
-      int passed = 0;
-#pragma unroll
-      for (int k = 0; k < RUN; ++k) {
-        const uint32_t b = __ballot_sync(0xffffffffu, BACK ? off > t0 + k : i < p.n_seq && off <= t0 + k);
-        if (lane == k) passed = __popc(b);
+    if (lo < t && t0 + RUN < hi) return;
+    const uint32_t valid = 0xffffffffu >> (32 - n);
+    const int i = BACK ? at - lane : at + 1 + lane;
+    from = at;
+    off = i < 0 ? -1 : i > p.n_seq ? 0x7fffffff : __ldg(p.cu_seqlens + i);
+    const int passed = __popc(upto(p, BACK ? t : t + n - 1, lane));
+    if (passed < 32) {
+      const uint32_t d = (uint32_t)off - (uint32_t)t;  // (others are at or above RUN)
+      uint32_t b = d < RUN ? 1u << d : 0, e = d - 1u < RUN ? 1u << (d - 1u) : 0;
+      if (BACK) {  // (the walk's own end is not among the 32)
+        const uint32_t z = (uint32_t)hi - (uint32_t)t - 1u;
+        if (z < RUN) e |= 1u << z;
       }
-      found = !__any_sync(0xffffffffu, in && passed >= 31);
-      if (found) {
-        seq = BACK ? max(at - passed, 0) : at + passed;  // (0: whatever the offsets hold)
-        // offsets seq and seq + 1, which others have loaded, but for the one
-        // before the first: the walk's own bounds
-        const int64_t x = __shfl_sync(0xffffffffu, off, BACK ? passed : passed - 1 & 31);
-        const int64_t y = __shfl_sync(0xffffffffu, off, BACK ? passed - 1 & 31 : passed);
-        l = !BACK && passed == 0 ? lo : x;
-        h = BACK && passed == 0 ? hi : y;
+      first = __reduce_or_sync(0xffffffffu, b) & valid;
+      last = __reduce_or_sync(0xffffffffu, e) & valid;
+      const int x = __shfl_sync(0xffffffffu, off, passed);
+      const int y = __shfl_sync(0xffffffffu, off, passed - 1 & 31);
+      if (BACK) {
+        hi = passed != 0 ? y : hi;
+        lo = x;
+        at -= passed;
+      } else {
+        lo = passed != 0 ? y : lo;
+        hi = x;
+        at += passed;
       }
-    }
-    if (!found && in) {
-      seq = seq_at(p.cu_seqlens, p.n_seq, t);
-      l = __ldg(p.cu_seqlens + seq);
-      h = __ldg(p.cu_seqlens + seq + 1);
-    }
-    first = __ballot_sync(0xffffffffu, in && l == t);
-    last = __ballot_sync(0xffffffffu, in && h == t + 1);
-    const uint32_t some = __ballot_sync(0xffffffffu, in);
-    if (some != 0) {
-      const int end = BACK ? __ffs((int)some) - 1 : 31 - __clz(some);
-      at = __shfl_sync(0xffffffffu, seq, end);
+    } else {
+      from = kSearched;
+      int l = 0, h = 0;
+      if (lane < n) {
+        off = seq_at(p.cu_seqlens, p.n_seq, t + lane);
+        l = __ldg(p.cu_seqlens + off);
+        h = __ldg(p.cu_seqlens + off + 1);
+      }
+      first = __ballot_sync(0xffffffffu, lane < n && l == t + lane);
+      last = __ballot_sync(0xffffffffu, lane < n && h == t + lane + 1);
+      const int end = BACK ? 0 : n - 1;
+      at = __shfl_sync(0xffffffffu, off, end);
       lo = __shfl_sync(0xffffffffu, l, end);
       hi = __shfl_sync(0xffffffffu, h, end);
     }
   }
-  __device__ __forceinline__ int seq_of(int i) const {
-    return __shfl_sync(0xffffffffu, seq, i);
+  // The lanes whose offset lies between the walk's sequence and token t's.
+  __device__ __forceinline__ uint32_t upto(const GlrArgs& p, int t, int lane) const {
+    return __ballot_sync(0xffffffffu, BACK ? off > t : from + 1 + lane < p.n_seq && off <= t);
+  }
+  // Sequence of the run's token i, one of the marked (some index, whatever the
+  // offsets hold).
+  __device__ __forceinline__ int seq_of(const GlrArgs& p, int64_t t0, int i, int lane) const {
+    if (p.cu_seqlens == nullptr) return 0;
+    if (from == kSearched) return __shfl_sync(0xffffffffu, off, i);
+    const int passed = __popc(upto(p, (int)t0 + i, lane));
+    return min(max(BACK ? from - passed : from + passed, 0), p.n_seq - 1);
   }
 };
 
@@ -586,7 +602,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
   };
 
   f2 carry = both(0.f);  // state before this step's first tile
-  Marks<RUN, false> m;
+  Marks<RUN, false> m(p);
   if (n_steps > 0) {
     stages.init();
     ex.init();
@@ -623,7 +639,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
     if (m.first != 0) {  // h_0 joins at first tokens, which forget what was before them
       for (uint32_t f = m.first; f != 0; f &= f - 1) {
         const int k = __ffs((int)f) - 1;
-        const f2 h0 = ch.get(p.initial_state, m.seq_of(k), C);
+        const f2 h0 = ch.get(p.initial_state, m.seq_of(p, t0, k, lane), C);
         replace(u, k, fma2(pick(a, k), h0, pick(u, k)));
       }
       run.A = cut_A();
@@ -678,7 +694,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
       if (p.final_state != nullptr)
         for (uint32_t f = m.last; f != 0; f &= f - 1) {
           const int k = __ffs((int)f) - 1;
-          ch.put(p.final_state, m.seq_of(k), C, pick(u, k));
+          ch.put(p.final_state, m.seq_of(p, t0, k, lane), C, pick(u, k));
         }
     }
     if (AL && tile0 < T_) stages.store(step, 1, maps, tile0, cb);
@@ -738,7 +754,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
   };
 
   f2 carry = both(0.f);  // e of the token behind this step's last tile
-  Marks<RUN, true> m;
+  Marks<RUN, true> m(p);
   if (n_steps > 0) {
     stages.init();
     ex.init();
@@ -767,7 +783,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
       if (p.d_final_state != nullptr)
         for (uint32_t f = m.last; f != 0; f &= f - 1) {
           const int k = __ffs((int)f) - 1;
-          replace(d, k, add2(pick(d, k), ch.get(p.d_final_state, m.seq_of(k), C)));
+          replace(d, k, add2(pick(d, k), ch.get(p.d_final_state, m.seq_of(p, t0, k, lane), C)));
         }
     };
     f2 a[RUN], u[RUN], om[RUN];  // om: 1 - a
@@ -796,7 +812,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
       if (m.first != 0) {  // as in the forward
         for (uint32_t f = m.first; f != 0; f &= f - 1) {
           const int k = __ffs((int)f) - 1;
-          const f2 h0 = ch.get(p.initial_state, m.seq_of(k), C);
+          const f2 h0 = ch.get(p.initial_state, m.seq_of(p, t0, k, lane), C);
           replace(u, k, fma2(pick(a, k), h0, pick(u, k)));
         }
         fr.A = cut_A();
@@ -841,7 +857,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
       }
       for (uint32_t f = m.first; f != 0; f &= f - 1) {  // before a first token: h_0
         const int k = __ffs((int)f) - 1;
-        replace(u, k, ch.get(p.initial_state, m.seq_of(k), C));
+        replace(u, k, ch.get(p.initial_state, m.seq_of(p, t0, k, lane), C));
       }
     }
     f2 e = p.cu_seqlens == nullptr
@@ -886,7 +902,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
       if (p.d_initial_state != nullptr)
         for (uint32_t f = m.first; f != 0; f &= f - 1) {
           const int k = __ffs((int)f) - 1;
-          ch.put(p.d_initial_state, m.seq_of(k), C, pick(d, k));
+          ch.put(p.d_initial_state, m.seq_of(p, t0, k, lane), C, pick(d, k));
         }
     }
     if (AL && tile >= 0) stages.store(step, N - 1, maps, tile * ROWS, cb);
