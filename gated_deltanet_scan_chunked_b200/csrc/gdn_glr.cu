@@ -20,12 +20,29 @@
 // once.
 //
 // Inputs come into two shared-memory stages, so that the next step's loads are
-// in flight while this one is folded, and outputs leave from the places of the
-// inputs that they replace: by TMA where rows of C elements are a multiple of
-// 16 bytes (AL), one box of 64 channels a tensor.  Other rows begin anywhere: a
-// row's piece is then copied from the 16-byte boundary below it by 16-byte
-// asynchronous copies, one more than it needs, and read from its remainder on;
-// outputs are stored from registers.
+// in flight while this one is folded, and outputs leave through shared memory
+// (the forward's from room of their own where there is some, else from the
+// places of the inputs that they replace): by TMA where rows of C elements are a
+// multiple of 16 bytes (AL), one box of 64 channels a tensor.  Other rows begin
+// anywhere: a row's piece is then copied from the 16-byte boundary below it by
+// 16-byte asynchronous copies, one more than it needs, and read from its
+// remainder on; outputs are stored from registers.
+//
+// What bounds it.  A dozen operations an element leave it memory bound in
+// principle.  In practice a step is a chain (inputs, fold, the cluster's
+// exchange, outputs) that the two to four CTAs of an SM overlap: at wide C the
+// memory is the limit, at others the part of the SMs that whole clusters of one
+// wave can fill, and with three tensors the latency of that chain.  Measured on a
+// B200 (a copy runs at 6.54 TB/s), time and bytes read and written by time:
+//   forward, bf16, beta, C = 6144, T = 4096          36.9 us   5.45 TB/s
+//   forward, bf16, beta, C = 9216, T = 16384          199 us   6.07 TB/s
+//   forward, bf16, b = 1 - a, C = 2560, T = 131072    449 us   4.48 TB/s
+//   forward, fp32, b = 1, C = 1333 (unaligned),
+//     20011 tokens of 24 sequences                   91.2 us   3.51 TB/s
+//   backward, bf16, beta, C = 6144, T = 32768         514 us   5.53 TB/s
+//   backward, bf16, beta, C = 2560, T = 4096         38.9 us   3.81 TB/s
+//   forward, bf16, beta, C = 2560, T = 128            4.3 us   (one step: its
+//     load, the exchange, its store)
 //
 // Runs in which a sequence begins or ends take a path of their own behind the
 // common one: for each such token, in a loop over the marks, the states of
@@ -926,7 +943,8 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
 
 // One token: [N, C] arrays, all dense and of one shape, so n = N C values in
 // a row.  A thread takes 8 of them with 16-byte accesses; the last n % 8
-// are taken singly.
+// are taken singly.  Bound by memory, and by its launch when small: bf16 with
+// beta, N = 256, C = 6144 5.3 us (25 MB, 4.7 TB/s), N = 3, C = 2561 2.2 us.
 template <typename Tin, int GATE>
 __global__ void __launch_bounds__(256) glr_step_kernel(const Tin* __restrict__ x,
                                                        const Tin* __restrict__ la,
