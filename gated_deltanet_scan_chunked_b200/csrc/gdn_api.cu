@@ -508,6 +508,7 @@ gdn_status glr_check_packed(const int32_t* cu_seqlens, int32_t n_seq, int64_t to
     return GDN_ERR_INVALID_ARG;
   if (total_T > 0x7fffffffLL) return GDN_ERR_INVALID_ARG;  // cu_seqlens is int32
   if (cu_seqlens && (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u)) return GDN_ERR_INVALID_ARG;
+  if (n_seq > kGlrMaxSequences) return GDN_ERR_UNSUPPORTED;
   return GDN_OK;
 }
 
@@ -555,7 +556,8 @@ extern "C" gdn_status gdn_glr_fwd(const void* x, const void* log_alpha, const vo
   const Span in[] = {{x, nb}, {log_alpha, nb}, {beta, nb},
                      {initial_state == final_state ? nullptr : initial_state, sb}};
   const Span out[] = {{y, nb}, {final_state, sb}, {checkpoints, cb}};
-  if (!spans_ok(in, 4, out, 3)) return GDN_ERR_INVALID_ARG;
+  const Span cu = {cu_seqlens, ((size_t)n_seq + 1) * 4};
+  if (!spans_ok(in, 4, out, 3) || !disjoint(&cu, 1, out, 3)) return GDN_ERR_INVALID_ARG;
   GlrArgs a = {};
   a.x = x; a.log_alpha = log_alpha; a.beta = beta; a.initial_state = initial_state;
   a.cu_seqlens = cu_seqlens; a.n_seq = n_seq; a.total_T = total_T; a.C = C; a.dtype = in_dtype;
@@ -597,7 +599,8 @@ extern "C" gdn_status gdn_glr_bwd(const void* x, const void* log_alpha, const vo
                      {d_final_state, sb}, {checkpoints, cb}};
   const Span out[] = {{dx, nb}, {dlog_alpha, nb}, {dbeta, nb}, {d_initial_state, sb},
                       {recompute ? workspace : nullptr, cb}};
-  if (!spans_ok(in, 7, out, 5)) return GDN_ERR_INVALID_ARG;
+  const Span cu = {cu_seqlens, ((size_t)n_seq + 1) * 4};
+  if (!spans_ok(in, 7, out, 5) || !disjoint(&cu, 1, out, 5)) return GDN_ERR_INVALID_ARG;
   GlrArgs a = {};
   a.x = x; a.log_alpha = log_alpha; a.beta = beta; a.initial_state = initial_state;
   a.cu_seqlens = cu_seqlens; a.n_seq = n_seq; a.total_T = total_T; a.C = C; a.dtype = in_dtype;

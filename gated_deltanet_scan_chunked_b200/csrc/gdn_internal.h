@@ -162,7 +162,8 @@ size_t gr_read_workspace_bytes(int64_t T, int32_t n_r, int32_t d, int32_t rank);
 
 // Gated linear recurrence (gdn_glr.cu): tokens from checkpoint to checkpoint.
 constexpr int kGlrTile = 32;
-constexpr int kGlrMaxChannels = 65535 * 32;  // groups of 32 channels along the grid
+constexpr int kGlrMaxChannels = 65535 * 32;  // groups of 64 along the grid's y
+constexpr int32_t kGlrMaxSequences = 1 << 30;  // indexes run a little past the last
 
 struct GlrArgs {
   const void* x;               // [total_T, C] input dtype, as are log_alpha, beta, y, dy

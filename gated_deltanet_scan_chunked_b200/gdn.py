@@ -698,7 +698,10 @@ def gdn_glr_fwd(x, log_alpha, beta=None, initial_state=None, cu_seqlens=None, y=
     if final_state is not None:
         _need(final_state, "final_state", torch.float32, (n_seq, C), i)
     elif output_final_state:
-        final_state = x.new_empty((n_seq, C), dtype=torch.float32)
+        if initial_state is not None:
+            final_state = torch.empty_like(initial_state)
+        else:
+            final_state = x.new_empty((n_seq, C), dtype=torch.float32)
         _keep(stream, final_state)
     if checkpoints is True:
         checkpoints = x.new_empty(glr_checkpoint_shape(T, C), dtype=torch.float32)

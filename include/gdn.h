@@ -492,10 +492,10 @@ typedef enum {
  *   beta           [total_T, C] in_dtype with GDN_GLR_GATE_BETA, else NULL
  *   gate           the input gate (gdn_glr_gate)
  *   initial_state  [n_seq, C] fp32 or NULL (zeros)
- *   cu_seqlens, n_seq, total_T   as for gdn_chunk_fwd.  A malformed
- *                  cu_seqlens is reported by gdn_check_device_error; nothing
- *                  outside the outputs is written, but their contents are
- *                  not meaningful then.
+ *   cu_seqlens, n_seq, total_T   as for gdn_chunk_fwd; n_seq at most 2^30,
+ *                  total_T below 2^31.  A malformed cu_seqlens is reported by
+ *                  gdn_check_device_error; nothing outside the outputs is
+ *                  written, but their contents are not meaningful then.
  *   C              channels (>= 1, any; at most 2,097,120)
  *   y              [total_T, C] in_dtype, written
  *   final_state    [n_seq, C] fp32 or NULL; may be initial_state exactly
@@ -634,7 +634,8 @@ gdn_status gdn_state_reorder(void* const* states, const size_t* row_bytes, int32
  * library's device-side error word on the current device.  Returns GDN_OK,
  * GDN_ERR_TIMEOUT (a kernel's bounded wait ran out and the kernel returned
  * early; its outputs are incomplete), GDN_ERR_INVALID_ARG (a kernel found a
- * malformed cu_seqlens or a parent out of range) or GDN_ERR_CUDA (the synchronisation itself failed).
+ * malformed cu_seqlens or a parent out of range) or GDN_ERR_CUDA (the
+ * synchronisation itself failed).
  * This call blocks the host; the compute entry points never do.
  */
 gdn_status gdn_check_device_error(gdn_stream_t stream);

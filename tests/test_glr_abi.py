@@ -36,6 +36,7 @@ PACKED = [
     (dict(C=0), BAD), (dict(C=-5), BAD), (dict(C=65535 * 32 + 1), UNSUP),
     (dict(dt=2), UNSUP), (dict(dt=-1), UNSUP),
     (dict(x=at(1) + 8), BAD), (dict(h0=at(4) + 4), BAD),
+    (dict(n=(1 << 30) + 1), UNSUP),
 ]
 
 
@@ -44,6 +45,7 @@ PACKED = [
     (dict(y=at(2) + 16), BAD), (dict(hT=at(4) + 16), BAD),  # a partial overlap of the state
     (dict(ck=at(6) + 64), BAD),                           # checkpoints inside y
     (dict(hT=at(7) + 2), BAD),
+    (dict(y=at(5)), BAD), (dict(hT=at(5) - 16), BAD), (dict(ck=at(5)), BAD),  # on the offsets
 ])
 def test_forward_rejects(lib, kw, code):
     assert _fwd(lib, **kw) == code
@@ -67,6 +69,7 @@ def _bwd(lib, **kw):
     (dict(ck=None, ws=at(13) + 16, wsb=MB), BAD),         # not 256-byte aligned
     (dict(ck=None, ws=at(9), wsb=MB), BAD),               # the workspace on an output
     (dict(dx=at(6)), BAD), (dict(dx=at(10)), BAD), (dict(dh0=at(7)), BAD),
+    (dict(dx=at(5)), BAD), (dict(dbe=at(5)), BAD), (dict(dh0=at(5)), BAD),  # on the offsets
 ])
 def test_backward_rejects(lib, kw, code):
     assert _bwd(lib, **kw) == code
