@@ -440,6 +440,28 @@ def test_malformed_sequence_offsets_are_reported(cu):
     assert gdn.gdn_check_device_error() == gdn.GDN_OK
 
 
+@pytest.mark.parametrize("seed", range(6))
+def test_malformed_offsets_of_many_sequences_write_nothing_outside(seed):
+    """Offsets out of order and far out of range among 300, at widths with and without
+    aligned rows: reported, and nothing but the outputs is written."""
+    rng = np.random.default_rng(seed)
+    T, C, n = 1500, (40, 33)[seed % 2], 300
+    p = make(27, [T], C, "beta", F32)
+    cu = np.concatenate([[0], np.sort(rng.integers(0, T, n - 1)), [T]])
+    cu[rng.integers(1, n, 5)] = [-2 ** 31, 2 ** 31 - 1, T + 1, -1, 0]
+    p["cu"] = torch.tensor(cu, dtype=torch.int32)
+    p["h0"] = torch.randn(n, C)
+    p["dhT"] = torch.randn(n, C)
+    y = torch.full((T + 64, C), 7.0, device="cuda")
+    h = torch.full((n + 64, C), 7.0, device="cuda")
+    lib.gdn_glr_fwd(cuda(p["x"]), cuda(p["log_alpha"]), cuda(p["beta"]), cu_seqlens=p["cu"].cuda(),
+                    initial_state=p["h0"].cuda(), y=y[:T], final_state=h[:n])
+    assert gdn.gdn_check_device_error() == gdn.GDN_ERR_INVALID_ARG
+    assert (y[T:] == 7.0).all() and (h[n:] == 7.0).all()
+    backward(p)
+    assert gdn.gdn_check_device_error() == gdn.GDN_ERR_INVALID_ARG
+
+
 def test_binding_refuses_mismatches():
     p = {k: cuda(v) for k, v in make(26, [9], 6, "beta", F32).items()}
     x, la, be = p["x"], p["log_alpha"], p["beta"]
