@@ -24,9 +24,12 @@
 // (the forward's from room of their own where there is some, else from the
 // places of the inputs that they replace): by TMA where rows of C elements are a
 // multiple of 16 bytes (AL), one box of 64 channels a tensor.  Other rows begin
-// anywhere: a row's piece is then copied from the 16-byte boundary below it by
-// 16-byte asynchronous copies, one more than it needs, and read from its
-// remainder on; outputs are stored from registers.
+// anywhere, but 4 (fp32) or 8 (bf16) of them together are such a multiple: the
+// inputs are then loaded as boxes of every 4th or 8th row, from the 16-byte
+// boundary below a piece on and 16 bytes wider, and outputs are stored from
+// registers.  (Against 16-byte asynchronous copies of all threads: fp32, C = 1333,
+// 20011 tokens of 24 sequences 80 us for 91, with beta, one sequence 74 for 100;
+// the backward 135 for 169 and 156 for 211.)
 //
 // What bounds it.  A dozen operations an element leave it memory bound in
 // principle.  In practice a step is a chain (inputs, fold, the cluster's
@@ -38,9 +41,9 @@
 //   forward, bf16, beta, C = 9216, T = 16384          199 us   6.07 TB/s
 //   forward, bf16, b = 1 - a, C = 2560, T = 131072    449 us   4.48 TB/s
 //   forward, fp32, b = 1, C = 1333 (unaligned),
-//     20011 tokens of 24 sequences                   91.2 us   3.51 TB/s
+//     20011 tokens of 24 sequences                   81.9 us   3.91 TB/s
 //   backward, bf16, beta, C = 6144, T = 32768         514 us   5.53 TB/s
-//   backward, bf16, beta, C = 2560, T = 4096         38.9 us   3.81 TB/s
+//   backward, bf16, beta, C = 2560, T = 4096         36.0 us   4.11 TB/s
 //   forward, bf16, beta, C = 2560, T = 128            4.3 us   (one step: its
 //     load, the exchange, its store)
 //
@@ -280,9 +283,12 @@ struct Chan {
 // Shared-memory image of one input tensor's piece of a tile.
 template <typename T, bool AL>
 struct Piece {
-  static constexpr int kCopies = kChan * (int)sizeof(T) / 16 + (AL ? 0 : 1);  // 16 bytes each
-  static constexpr int kPitch = 16 * kCopies;                                 // bytes of a row
-  static constexpr int bytes(int rows) { return rows * kPitch; }
+  static constexpr int kGroup = AL ? 1 : 16 / (int)sizeof(T);  // rows of a map's row
+  static constexpr int kPitch = kChan * (int)sizeof(T) + (AL ? 0 : 16);  // bytes of a row
+  // rows r = kGroup q + j of one j lie together
+  static constexpr int part(int rows) { return (rows / kGroup * kPitch + 127) & ~127; }
+  static constexpr int bytes(int rows) { return kGroup * part(rows); }
+  static constexpr int at(int rows, int r) { return r % kGroup * part(rows) + r / kGroup * kPitch; }
   // A lane's two channels of one row; rem: where the row's piece begins.
   static __device__ __forceinline__ f2 get(const char* row, int rem, int lane) {
     if (sizeof(T) == 2) {
@@ -317,14 +323,11 @@ __device__ __forceinline__ void put_out(T* q, const Chan<false>& ch, f2 v) {
   if (ch.ok1) Elem<T>::store(q + 32, v.y);
 }
 
-// 16 bytes of which the first n (0 .. 16) are read, the rest zero filled.
-__device__ __forceinline__ void copy16(uint32_t dst, const char* src, int n) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
-               : "memory");
-}
-
-// TMA maps of the inputs and outputs (AL only): [total_T, C] with boxes of kChan
-// channels x a tile's tokens.
+// TMA maps of the inputs and (AL) outputs: [total_T, C] with boxes of kChan
+// channels x a tile's tokens.  Rows that are no multiple of 16 bytes: `kGroup`
+// rows together are one, so the inputs' maps are [total_T / kGroup, kGroup C], and
+// a box of every kGroup-th row begins at the 16-byte boundary below its piece,
+// 16 bytes wider than it.  The last total_T % kGroup tokens are not in the maps.
 struct ScanMaps {
   CUtensorMap in[4], out[3];
 };
@@ -345,7 +348,7 @@ struct Stages {
 
   // (by every thread, before the block's first barrier)
   __device__ __forceinline__ void init() {
-    if (AL && threadIdx.x == 0) {
+    if (threadIdx.x == 0) {
       sm100::mbar_init(&full[0], 1);
       sm100::mbar_init(&full[1], 1);
       sm100::fence_mbar_init();
@@ -353,71 +356,51 @@ struct Stages {
   }
   // (by every thread, after a barrier behind the last use of the stage; the
   // outputs that leave from it are read before it is filled again)
-  __device__ __forceinline__ void load(int64_t step, bool any, const char* const (&src)[N],
-                                       const ScanMaps& maps, int64_t t0, int64_t total_T, int C,
-                                       int cb) {
+  __device__ __forceinline__ void load(int64_t step, bool any, const ScanMaps& maps, int64_t t0,
+                                       int64_t total_T, int C, int cb) {
+    if (!any || threadIdx.x != 0) return;
+    constexpr int G = P::kGroup;
     const uint32_t stage = sm100::smem_u32(at) + (uint32_t)(step & 1) * kStage;
-    if constexpr (AL) {
-      if (any && threadIdx.x == 0) {
-        uint64_t* bar = &full[step & 1];
-        if (!APART) sm100::bulk_wait_read_all();
-        sm100::mbar_arrive_expect_tx(bar, kStage);
+    uint64_t* bar = &full[step & 1];
+    if (AL && !APART) sm100::bulk_wait_read_all();
+    sm100::mbar_arrive_expect_tx(bar, N * ROWS * P::kPitch);
+    // (fewer than G tokens are in no map: the box lies outside it)
+    const int y = (int)(t0 / G) + (!AL && total_T < G ? 1 << 20 : 0);
+    for (int j = 0; j < G; ++j) {
+      const int x = AL ? cb : (j * C + cb) & ~(G - 1);
 #pragma unroll
-        for (int k = 0; k < N; ++k)
-          sm100::tma_load_2d(stage + k * kTensor, &maps.in[k], cb, (int)t0, bar);
-      }
-    } else {
-      if (any) copy(stage, src, t0, total_T, C, cb);
-      sm100::cp_async_commit();
+      for (int k = 0; k < N; ++k)
+        sm100::tma_load_2d(stage + k * kTensor + j * P::part(ROWS), &maps.in[k], x, y, bar);
     }
   }
-  __device__ __forceinline__ void copy(uint32_t stage, const char* const (&src)[N], int64_t t0,
-                                       int64_t total_T, int C, int cb) {
-    if constexpr (!AL) {
-      // a thread has one 16-byte column of every kRows-th row
-      constexpr int kRows = THREADS / P::kCopies;
-      const int q = (int)threadIdx.x % P::kCopies, r0 = (int)threadIdx.x / P::kCopies;
-      if (r0 >= kRows) return;
-      const uint32_t row_bytes = (uint32_t)C * (uint32_t)sizeof(T);
-      // bytes of the tensors up to the tile, of which the last few not a
-      // multiple of 16 count with the rows
-      const int64_t before = (t0 < 0 ? 0 : t0) * (int64_t)row_bytes + (int64_t)cb * (int)sizeof(T);
-      const int64_t left = total_T * (int64_t)row_bytes - (before & ~(int64_t)15);
-      // (all of the tile's copies lie inside the tensors)
-      const bool whole =
-          t0 >= 0 && left >= (int64_t)(ROWS - 1) * row_bytes + 16 + P::kPitch;
-      const char* base[N];
+  // (by every warp, behind wait; !AL) The tokens of its run, from row `r0` of the
+  // tile, that are in no map, each lane's own channels.
+  template <int RUN>
+  __device__ __forceinline__ void last_tokens(int64_t step, const char* const (&src)[N], int r0,
+                                              int64_t t0, int64_t total_T, int C,
+                                              const Chan<AL>& ch, int lane) {
+    constexpr int G = P::kGroup, E = (int)sizeof(T);
+    const int64_t mapped = total_T / G * G;
+    if (t0 >= total_T || t0 + RUN <= mapped) return;
+    char* stage = at + (int)(step & 1) * kStage;
+#pragma unroll 1
+    for (int64_t t = t0 > mapped ? t0 : mapped; t < t0 + RUN && t < total_T; ++t) {
+      const int r = r0 + (int)(t - t0), rem = (int)((uint32_t)t * (uint32_t)(C * E) & 15u);
+      char* row = stage + P::at(ROWS, r) + rem + E * lane;
+      const int64_t from = t * C + ch.c0;
 #pragma unroll
-      for (int k = 0; k < N; ++k) base[k] = src[k] + (before & ~(int64_t)15);
-      uint32_t row = (uint32_t)(before & 15) + (uint32_t)r0 * row_bytes;
-      uint32_t dst = stage + r0 * P::kPitch + 16 * q;
-#pragma unroll 4
-      for (int r = r0; r < ROWS; r += kRows) {
-        uint32_t off = (row & ~15u) + 16u * q;
-        int n = 16;
-        if (!whole) {
-          const bool in = t0 + r >= 0 && t0 + r < total_T && (int64_t)off < left;
-          n = !in ? 0 : left - off >= 16 ? 16 : (int)(left - off);
-          if (n == 0) off = 0;
-        }
-#pragma unroll
-        for (int k = 0; k < N; ++k) copy16(dst + k * kTensor, base[k] + off, n);
-        row += kRows * row_bytes;
-        dst += kRows * P::kPitch;
+      for (int k = 0; k < N; ++k) {
+        const T* q = reinterpret_cast<const T*>(src[k]) + from;
+        if (ch.ok0) *reinterpret_cast<T*>(row + k * kTensor) = q[0];
+        if (ch.ok1) *reinterpret_cast<T*>(row + k * kTensor + 32 * E) = q[32];
       }
     }
+    sm100::fence_proxy_async();  // before the stage is filled again
   }
   // (by every thread) Waits for the step's inputs.  ok: no bounded wait ran out
   // yet (then none is made).
   __device__ __forceinline__ bool wait(int64_t step, bool ok) {
-    if constexpr (AL) {
-      return ok && sm100::mbar_wait(&full[step & 1], (uint32_t)(step >> 1) & 1u, kWait);
-    } else {
-      if (APART) sm100::cp_async_wait_group1();  // (the next step's may be under way)
-      else sm100::cp_async_wait_all();
-      __syncthreads();
-      return ok;
-    }
+    return ok && sm100::mbar_wait(&full[step & 1], (uint32_t)(step >> 1) & 1u, kWait);
   }
   // (by thread 0, before a barrier in front of the next outputs; AL, APART) The
   // last ones have left.
@@ -551,7 +534,7 @@ __device__ __forceinline__ void empty_sequences(const GlrArgs& p, const float* i
 // (4 a token), the backward more.  Both come with 4 and with 8 warps to a CTA;
 // the backward's tiles begin at checkpoints.  (Forward runs of 8 tokens in
 // fp32 against 16: 20011 tokens of 24 sequences, C = 1336 98 us for 74, with beta
-// 90 for 76, C = 1333 115 for 104, C = 2560 110 for 109; C = 6144 both 263.)
+// 90 for 76, C = 2560 110 for 109; C = 6144 both 263.)
 constexpr int kFwdRun = 16, kBwdRun = 8;
 static_assert(4 * kBwdRun % kGlrTile == 0 && kGlrTile % kFwdRun == 0, "checkpoints at runs");
 
@@ -615,7 +598,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
   src[1] = static_cast<const char*>(p.log_alpha);
   if (N == 3) src[N - 1] = static_cast<const char*>(p.beta);
   auto load = [&](int64_t step) {
-    stages.load(step, step < n_steps, src, maps, (step * n_cta + rank) * ROWS, T_, C, cb);
+    stages.load(step, step < n_steps, maps, (step * n_cta + rank) * ROWS, T_, C, cb);
   };
 
   f2 carry = both(0.f);  // state before this step's first tile
@@ -632,14 +615,15 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
     m.look(p, t0, lane);
     const bool inside = (m.first | m.last) == 0;
     ex.ok = stages.wait(step, ex.ok);
-    char* st = stages.at + (int)(step & 1) * stages.kStage + warp * RUN * P::kPitch;
+    if constexpr (!AL)
+      stages.template last_tokens<RUN>(step, src, warp * RUN, t0, T_, C, ch, lane);
+    char* st = stages.at + (int)(step & 1) * stages.kStage + warp * (RUN / P::kGroup) * P::kPitch;
     [[maybe_unused]] char* to = kFwdApart<T, GATE, AL, W>
                                     ? stages.at + 2 * stages.kStage + warp * RUN * P::kPitch
                                     : st;
-    const uint32_t rem = (uint32_t)t0 * row_bytes + (uint32_t)cb * (uint32_t)sizeof(T);
     auto in = [&](int k, int i) {  // tensor k at token i of the run
-      return P::get(st + k * stages.kTensor + i * P::kPitch,
-                    AL ? 0 : (int)((rem + (uint32_t)i * row_bytes) & 15u), lane);
+      return P::get(st + k * stages.kTensor + P::at(ROWS, i),
+                    AL ? 0 : (int)((uint32_t)(i % P::kGroup) * row_bytes & 15u), lane);
     };
     f2 a[RUN], u[RUN];
     Run run;
@@ -672,22 +656,14 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
     // the runs are complete; this step's inputs are read, the step before is done
     // with its stage
     __syncthreads();
-    // The next loads: by TMA at once, by every thread's copies behind the sends,
-    // which the cluster waits for (C = 1333 as above 91 us for 100; TMA behind
-    // the sends 1% slower).
-    auto load_next = [&] {
-      if (kFwdApart<T, GATE, AL, W>) load(step + 2);
-      else if (step > 0) load(step + 1);
-    };
-    if (AL) load_next();
+    if (kFwdApart<T, GATE, AL, W>) load(step + 2);
+    else if (step > 0) load(step + 1);
     f2 h;
     if (p.cu_seqlens == nullptr) {
       const Run before = ex.template give<W, false, false>(step, lane, warp, runs);
-      if (!AL) load_next();
       h = through<false>(before, ex.template receive<false>(step, lane, carry));
     } else {
       const Run before = ex.template give<W, false, true>(step, lane, warp, runs);
-      if (!AL) load_next();
       h = through<true>(before, ex.template receive<true>(step, lane, carry));
     }
     if (p.checkpoints != nullptr && t0 % kGlrTile == 0 && t0 < T_)
@@ -774,8 +750,8 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
   // tiles in reverse: rank r of step s has tile n_tiles - 1 - (s n_cta + r),
   // negative (nothing to do, all neutral) behind the first tile
   auto load = [&](int64_t step) {
-    stages.load(step, step < n_steps, src, maps, (n_tiles - 1 - (step * n_cta + rank)) * ROWS, T_,
-                C, cb);
+    stages.load(step, step < n_steps, maps, (n_tiles - 1 - (step * n_cta + rank)) * ROWS, T_, C,
+                cb);
   };
 
   f2 carry = both(0.f);  // e of the token behind this step's last tile
@@ -795,11 +771,12 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
     f2 h = both(0.f);
     if (tile >= 0) h = ch.get(p.checkpoints, tile * (ROWS / kGlrTile), C);
     ex.ok = stages.wait(step, ex.ok);
-    char* st = stages.at + (int)(step & 1) * stages.kStage + warp * RUN * P::kPitch;
-    const uint32_t rem = (uint32_t)t0 * row_bytes + (uint32_t)cb * (uint32_t)sizeof(T);
+    if constexpr (!AL)
+      stages.template last_tokens<RUN>(step, src, warp * RUN, t0, T_, C, ch, lane);
+    char* st = stages.at + (int)(step & 1) * stages.kStage + warp * (RUN / P::kGroup) * P::kPitch;
     auto in = [&](int k, int i) {  // tensor k at token i of the run
-      return P::get(st + k * stages.kTensor + i * P::kPitch,
-                    AL ? 0 : (int)((rem + (uint32_t)i * row_bytes) & 15u), lane);
+      return P::get(st + k * stages.kTensor + P::at(ROWS, i),
+                    AL ? 0 : (int)((uint32_t)(i % P::kGroup) * row_bytes & 15u), lane);
     };
     // dy of the run; dh_T joins at its sequence's last token
     auto all_dy = [&](f2(&d)[RUN]) {
@@ -851,19 +828,17 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
     fwd_runs[warp][lane] = fr;
     rev_runs[warp][lane] = rr;
     __syncthreads();  // the runs are complete; the step before is done with its stage
-    if (AL && step > 0) load(step + 1);  // (see the forward)
+    if (step > 0) load(step + 1);
     // While the cluster's runs are under way: the state before this run, and
     // h_{t-1} of every token (into u).
     Run behind;
     if (p.cu_seqlens == nullptr) {
       behind = ex.template give<W, true, false>(step, lane, warp, rev_runs);
-      if (!AL && step > 0) load(step + 1);
 #pragma unroll
       for (int w = 0; w < W - 1; ++w)
         if (w < warp) h = through<false>(fwd_runs[w][lane], h);
     } else {
       behind = ex.template give<W, true, true>(step, lane, warp, rev_runs);
-      if (!AL && step > 0) load(step + 1);
 #pragma unroll
       for (int w = 0; w < W - 1; ++w)
         if (w < warp) h = through<true>(fwd_runs[w][lane], h);
@@ -1061,12 +1036,15 @@ EncodeTiledFn encode_tiled() {
   return fn;
 }
 
-bool encode_map(CUtensorMap* m, const GlrArgs& a, const void* base, int rows) {
+bool encode_map(CUtensorMap* m, const GlrArgs& a, const void* base, int rows, bool al) {
   const EncodeTiledFn fn = encode_tiled();
   const bool bf16 = a.dtype == GDN_BF16;
-  const cuuint64_t dims[2] = {(cuuint64_t)a.C, (cuuint64_t)a.total_T};
-  const cuuint64_t strides[1] = {(cuuint64_t)a.C * (bf16 ? 2 : 4)};
-  const cuuint32_t box[2] = {(cuuint32_t)kChan, (cuuint32_t)rows};
+  // (Piece has the other side of this)
+  const int g = al ? 1 : bf16 ? 8 : 4;
+  const cuuint64_t whole = (cuuint64_t)(a.total_T / g);
+  const cuuint64_t dims[2] = {(cuuint64_t)a.C * g, whole > 0 ? whole : 1};
+  const cuuint64_t strides[1] = {(cuuint64_t)a.C * g * (bf16 ? 2 : 4)};
+  const cuuint32_t box[2] = {(cuuint32_t)(al ? kChan : kChan + g), (cuuint32_t)(rows / g)};
   const cuuint32_t one[2] = {1, 1};
   return fn != nullptr &&
          fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
@@ -1140,8 +1118,8 @@ int clusters_that_fit(int dev, int variant, const Scan& k, int cluster, int shar
 // choice counts on, by the shared memory asked for.  Measured on a B200
 // (forward, bf16, gate beta, us a step): 8 warps 2.05 alone and 2.85 by twos, 4
 // warps (half the tokens) 1.28, 1.65, 2.1 and 2.5; a further wave costs about a
-// tenth; the backward's 4 warps are slower by comparison.  What this settles
-// (us, bf16):
+// tenth; the backward's 4 warps are slower by comparison (on the scale of its 8:
+// 1.46, 1.87, 2.26, 2.72).  What this settles (us, bf16):
 //   forward, C = 6144, T = 32768: 8 warps in clusters of 2 (one wave, a third
 //     of the SMs with two CTAs) 336, of 8 (three waves) 307, 4 warps in
 //     clusters of 4 263;
@@ -1149,8 +1127,10 @@ int clusters_that_fit(int dev, int variant, const Scan& k, int cluster, int shar
 //     wave for 3 of 40 groups) 668, 4 warps in clusters of 10 444;
 //   forward, C = 9216, T = 16384: 8 warps in clusters of 2 199, 4 warps 211;
 //   backward, C = 6144, T = 32768: 8 warps in clusters of 2 633, of 5 (two
-//     waves) 567, 4 warps in clusters of 5 517; C = 9216, T = 16384: 8 warps
-//     in clusters of 2 358, 4 warps in clusters of 7 391.
+//     waves) 567, 4 warps in clusters of 5, four to an SM, 515; C = 9216, T =
+//     16384: 8 warps in clusters of 2 358, 4 warps in clusters of 7 391; C =
+//     2560, T = 4096: 4 warps in clusters of 12, four to an SM, 38.9, of 10,
+//     three to an SM, 36.0.
 struct Choice {
   Scan scan;
   int cluster, smem;  // cluster 0: none
@@ -1159,7 +1139,7 @@ struct Choice {
 
 Choice choose(int dev, const GlrArgs& a, bool al, int what, int groups) {
   static const double kStep8[] = {2.05, 2.85}, kFwdStep4[] = {1.28, 1.65, 2.1, 2.5},
-                      kBwdStep4[] = {1.46, 1.87, 2.26, 2.6};
+                      kBwdStep4[] = {1.46, 1.87, 2.26, 2.72};
   const bool small = what == kFwd4 || what == kBwd4;
   const double* step_us = what == kFwd4 ? kFwdStep4 : what == kBwd4 ? kBwdStep4 : kStep8;
   const Scan k = scan_for(a, al, what);
@@ -1194,17 +1174,17 @@ gdn_status launch_scan(const GlrArgs& a, bool bwd, cudaStream_t stream) {
   if (c.cluster == 0) return GDN_ERR_CUDA;
   const Scan& k = c.scan;
   ScanMaps maps = {};
-  if (al && a.total_T > 0) {
+  if (a.total_T > 0) {
     // (the order in which the kernels number their tensors)
     const bool beta = a.gate == kGateBeta;
     const void* in[4] = {a.x, a.log_alpha, beta ? a.beta : a.dy, a.dy};
     const void* out[3] = {bwd ? a.dx : a.y, a.dlog_alpha, a.dbeta};
     const int n_in = 2 + (beta ? 1 : 0) + (bwd ? 1 : 0);
-    const int n_out = bwd ? n_in - 1 : a.y != nullptr ? 1 : 0;
+    const int n_out = !al ? 0 : bwd ? n_in - 1 : a.y != nullptr ? 1 : 0;
     for (int i = 0; i < n_in; ++i)
-      if (!encode_map(&maps.in[i], a, in[i], k.rows)) return GDN_ERR_CUDA;
+      if (!encode_map(&maps.in[i], a, in[i], k.rows, al)) return GDN_ERR_CUDA;
     for (int i = 0; i < n_out; ++i)
-      if (!encode_map(&maps.out[i], a, out[i], k.rows)) return GDN_ERR_CUDA;
+      if (!encode_map(&maps.out[i], a, out[i], k.rows, al)) return GDN_ERR_CUDA;
   }
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg = scan_config(k, c.cluster, c.smem, groups, stream, &attr);
