@@ -8,8 +8,8 @@
 // (A1 A2, A2 h1 + h2).  A sequence's first token takes a = 0 and adds
 // a_t h_0 to its input, so packed sequences need no other care.
 //
-// Layout.  A CTA of W warps owns a tile of W kRun tokens x 64 channels: warp w
-// has the run of kRun tokens from w kRun on, a lane two channels.  The carry
+// Layout.  A CTA of W warps owns a tile of W runs (16 tokens, backward 8) x 64
+// channels: warp w has the tile's w-th run, a lane two channels.  The carry
 // along the tokens passes three levels, each in a fixed order (results do not
 // depend on timing): a thread's run in registers, the tile's runs through
 // shared memory, and the CTAs of a cluster, which hold consecutive tiles of
