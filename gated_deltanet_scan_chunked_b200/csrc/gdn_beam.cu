@@ -45,6 +45,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCap = 1024;  // candidates of one segment held at once
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNear = 67108864.f;  // 2^26: see Offset
 
 // Order-preserving map of a float (not NaN; -0 taken as +0) to an unsigned.
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -159,6 +160,21 @@ struct Row {
   __device__ __forceinline__ uint4 get(const Raw& r) const {
     return make_uint4(__funnelshift_r(r.w[0], r.w[1], bits), __funnelshift_r(r.w[1], r.w[2], bits),
                       __funnelshift_r(r.w[2], r.w[3], bits), __funnelshift_r(r.w[3], r.w[4], bits));
+  }
+};
+
+// What a sum of exp(x - m) subtracts: c = fl(m log2 e), so that a term is 2^(x
+// log2 e - c), one instruction.  c lacks r = m log2 e - c, up to half a step of
+// c, which makes each of the sum's terms 2^r times what it should be: at |m| < 2^26
+// at most 2^4, put right where sums of different m meet.  Beyond it r may pass
+// the exponents that a float has; there c = 0 and the difference x - m is formed
+// first.
+struct Offset {
+  float c, r;
+  __device__ __forceinline__ explicit Offset(float m) {
+    const bool near = fabsf(m) < kNear;
+    c = near ? __fmul_rn(m, kLog2e) : 0.f;
+    r = near ? __fmaf_rn(m, kLog2e, -c) : 0.f;
   }
 };
 
@@ -303,10 +319,8 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
   // value, the first vector that has it) and the largest value of its other
   // vectors.  m need not be the maximum: it is the first batch's and moves
   // only when exp(x - m) would grow past e^40, so that most batches cost no
-  // rescaling.  With c = fl(m log2 e), the exponent is x log2 e - c, one
-  // instruction; what c is off by is a factor common to the thread's terms, put
-  // right at the end.  Values beyond 1e30 and batches with NaN take the long
-  // way.
+  // rescaling.  m beyond 2^26 (Offset) and batches with NaN take the long way; a
+  // batch of nothing but -inf adds nothing to any sum.
   float m = -FLT_MAX, c = 0.f, s = 0.f, best = -INFINITY, other = -INFINITY;
   uint32_t best_v = (uint32_t)tid;
   for (int v0 = tid; v0 < n_vec; v0 += U * kThreads) {
@@ -326,9 +340,10 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
       peak = fmaxf(peak, top);
     }
     if (peak > m + 40.f) {  // (-FLT_MAX + 40 is -FLT_MAX; what was summed vanishes, if any was)
-      s *= sm100::ex2_approx(__fmul_rn(__fadd_rn(m, -peak), kLog2e));
+      const Offset old(m), now(peak);
+      s *= sm100::ex2_approx(__fmaf_rn(__fadd_rn(m, -peak), kLog2e, now.r - old.r));
       m = peak;
-      c = fabsf(m) < 1e30f ? __fmul_rn(m, kLog2e) : 0.f;
+      c = now.c;
     }
     float sum = 0.f;
 #pragma unroll
@@ -339,22 +354,22 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
       for (int j = 0; j < E; ++j) part += sm100::ex2_approx(__fmaf_rn(f[j], kLog2e, -c));
       sum += part;
     }
-    if (!(sum <= FLT_MAX) || !(fabsf(m) < 1e30f)) {
-      const float c_off = fabsf(m) < 1e30f ? __fmaf_rn(m, kLog2e, -c) : 0.f;
+    if (!(sum <= FLT_MAX) || !(fabsf(m) < kNear)) {
+      const float r_m = Offset(m).r;
+      const int end = peak > -INFINITY ? min(n_vec, v0 + U * kThreads) : 0;
       sum = 0.f;
 #pragma unroll 1
-      for (int v = v0; v < n_vec && v < v0 + U * kThreads; v += kThreads) {
+      for (int v = v0; v < end; v += kThreads) {
         float f[E];
         Vec<T>::get(x.get(x.load(e0 + (int64_t)v * E)), f);
 #pragma unroll
         for (int j = 0; j < E; ++j)
-          sum += sm100::ex2_approx(__fmaf_rn(__fadd_rn(tame(f[j]), -m), kLog2e, c_off));
+          sum += sm100::ex2_approx(__fmaf_rn(__fadd_rn(tame(f[j]), -m), kLog2e, r_m));
       }
     }
     s += sum;
   }
-  if (fabsf(m) < 1e30f)  // 2^(c - m log2 e)
-    s = __fmaf_rn(s, -0.6931471805599453f * __fmaf_rn(m, kLog2e, -c), s);
+  s *= exp2f(-Offset(m).r);
   float wm = m;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, o));
