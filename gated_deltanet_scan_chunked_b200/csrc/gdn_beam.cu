@@ -58,9 +58,14 @@ __device__ __forceinline__ float unordered(uint32_t o) {
 __device__ __forceinline__ u64 key_of(float x, uint32_t idx) {
   return (u64)ordered(x) << 32 | (uint32_t)~idx;
 }
-// What a logit counts as: NaN as -inf (never chosen before a number), +inf as
-// the largest finite value (so that equal shares go to the infinite entries).
-__device__ __forceinline__ float tame(float x) { return fminf(fmaxf(x, -INFINITY), FLT_MAX); }
+// What a logit counts as: NaN as -inf (never chosen before a number).
+__device__ __forceinline__ float tame(float x) { return fmaxf(x, -INFINITY); }
+// a - b, 0 for equal infinities: where the largest is +inf, the entries that are
+// it share the row equally and the others have nothing.
+template <typename F>
+__device__ __forceinline__ F gap(F a, F b) {
+  return a == b ? F(0) : a - b;
+}
 
 // 16 bytes of a row as floats.
 template <typename T>
@@ -269,6 +274,7 @@ struct __align__(16) BeamShared {
   // the merge
   double score[kMaxBeams], log_sum[kMaxBeams];  // score -inf: no finite candidate
   float top[kMaxBeams];
+  int n_inf[kMaxBeams];  // +inf logits of a row with fewer than M of them, else 0
   unsigned char done[kMaxBeams];
 };
 
@@ -364,7 +370,7 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
         Vec<T>::get(x.get(x.load(e0 + (int64_t)v * E)), f);
 #pragma unroll
         for (int j = 0; j < E; ++j)
-          sum += sm100::ex2_approx(__fmaf_rn(__fadd_rn(tame(f[j]), -m), kLog2e, r_m));
+          sum += sm100::ex2_approx(__fmaf_rn(gap(tame(f[j]), m), kLog2e, r_m));
       }
     }
     s += sum;
@@ -373,7 +379,7 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
   float wm = m;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, o));
-  const float ws = warp_sum(s * sm100::ex2_approx(__fmul_rn(__fadd_rn(m, -wm), kLog2e)));
+  const float ws = warp_sum(s * sm100::ex2_approx(__fmul_rn(gap(m, wm), kLog2e)));
   if (lane == 0) {
     sh.red_m[warp] = wm;
     sh.red_s[warp] = ws;
@@ -460,7 +466,7 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
     for (int w = 1; w < kWarps; ++w) bm = fmaxf(bm, sh.red_m[w]);
     float bs = 0.f;
     for (int w = 0; w < kWarps; ++w)
-      bs += sh.red_s[w] * sm100::ex2_approx(__fmul_rn(__fadd_rn(sh.red_m[w], -bm), kLog2e));
+      bs += sh.red_s[w] * sm100::ex2_approx(__fmul_rn(gap(sh.red_m[w], bm), kLog2e));
     sums(bm, bs);
   }
   __syncthreads();
@@ -566,21 +572,52 @@ __global__ void __launch_bounds__(kThreads, 3) beam_select_kernel(const BeamArgs
     double s = 0.0;
     for (int i = 0; i < S; ++i) {
       const float2 p = sums[tid * S + i];
-      s += (double)(p.y * sm100::ex2_approx(__fmul_rn(__fadd_rn(p.x, -m), kLog2e)));
+      s += (double)(p.y * sm100::ex2_approx(__fmul_rn(gap(p.x, m), kLog2e)));
     }
     // (a row of -inf has s = 0: it takes part like a dead beam)
     const bool some = my_kind != kDead && s > 0.0, live = some && my_kind == kLive;
     sh.score[tid] = some ? (double)my_score : -INFINITY;
     sh.log_sum[tid] = live ? log(s) : 0.0;
     sh.top[tid] = live ? m : 0.f;
+    sh.n_inf[tid] = live && m == INFINITY && s < (double)M ? (int)s : 0;
   }
   if (tid == 0) sh.n_cand = 0;
   __syncthreads();
+  // Of a row with +inf logits all other tokens score -inf, and go by index, not by
+  // logit: its lists are made anew, the infinite tokens and the lowest others.
+  // (Where there are M infinite ones, no others are chosen.)
+  for (int k = 0; k < K; ++k) {
+    const int n_inf = sh.n_inf[k];
+    if (n_inf == 0) continue;
+    auto slot = [&](int i) { return i / S * lists + k * S + i % S; };
+    if (tid == 0) sh.n_multi = 0;
+    __syncthreads();
+    for (int i = tid; i < S * M; i += kThreads) {
+      const u64 key = keys[slot(i)];
+      if ((uint32_t)(key >> 32) == ordered(INFINITY))
+        sh.multi[atomicAdd(&sh.n_multi, 1)] = (int)~(uint32_t)key;
+    }
+    __syncthreads();
+    for (int i = tid; i < S * M; i += kThreads)
+      keys[slot(i)] = i < n_inf ? key_of(INFINITY, (uint32_t)sh.multi[i]) : 0;
+    __syncthreads();
+    if (tid < M && tid < a.V) {  // (the lowest M tokens hold enough others)
+      int below = 0;
+      bool one = false;
+      for (int i = 0; i < n_inf; ++i) {
+        below += sh.multi[i] < tid;
+        one |= sh.multi[i] == tid;
+      }
+      const int i = n_inf + tid - below;
+      if (!one && i < M) keys[slot(i)] = key_of(-INFINITY, (uint32_t)tid);
+    }
+    __syncthreads();
+  }
   auto candidate = [&](int i, u64& o, uint32_t& flat) {  // (o = 0: none)
     const u64 key = keys[i];
     const int k = (i % lists) / S;
     const float x = unordered((uint32_t)(key >> 32));
-    o = key == 0 ? 0 : ordered64(sh.score[k] + (((double)x - (double)sh.top[k]) - sh.log_sum[k]));
+    o = key == 0 ? 0 : ordered64(sh.score[k] + (gap((double)x, (double)sh.top[k]) - sh.log_sum[k]));
     flat = (uint32_t)k * (uint32_t)a.V + ~(uint32_t)key;
   };
   // The best M by (score, then the lowest flat index): those at or above the

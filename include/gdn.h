@@ -577,7 +577,9 @@ gdn_status gdn_glr_step(const void* x, const void* log_alpha, const void* beta,
  * and so does a row of logits that are all -inf; these beams' logits, and
  * finished beams', do not count.  If fewer than M candidates are finite, the
  * rest of the M are candidates of score -inf, the lowest k V + v first.
- * A NaN logit counts as -inf; +inf logits share their row equally.
+ * A NaN logit counts as -inf; +inf logits share their row equally, and its
+ * other tokens score -inf.  (A score below fp32's range is -inf too, but stands
+ * before those.)
  *
  *   logits         n_groups * K rows of V logits, in_dtype; row r begins at
  *                  logits + r ld (elements).  Aligned to its element size

@@ -1,11 +1,13 @@
 """Beam search's choice where logits are far from 0 or from each other: mask
 values of any size, offsets, infinities, ties.  Against the fp64 oracle, or
 against the definition where the answer is plain."""
+import numpy as np
 import pytest
 import torch
 
 import gated_deltanet_scan_chunked_b200 as lib
-from tests.test_beam_gpu import BF16, F32, check, rows
+from oracle import beam
+from tests.test_beam_gpu import BF16, F32, LOG_SUM, check, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -67,3 +69,59 @@ def test_sums_that_grow_in_steps(m):
     x[:, :, 4096] = x[0, 0, 0] + 39.75
     x[:, :, 8192] = x[0, 0, 0] + 40.25
     check(x, torch.zeros(G, K, device="cuda"), 8, groups=[0, 77, 149])
+
+
+INF = float("inf")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("V", [40, 5003, 70001])
+def test_infinite_logits_leave_the_others_nothing(V, dtype):
+    """+inf logits share their row; its other tokens score -inf and come by index."""
+    x, s = rows(6, 8, 3, V, dtype, 3, 1)
+    hot = [V - 1, 5, V // 2]
+    x[0, :, hot] = INF                       # all beams: 9 candidates that are finite
+    x[1, 0, hot] = INF                       # one beam, the others as usual
+    x[2, :, 0] = INF
+    x[2, 1, 1::3] = float("nan")
+    x[3, :, ::2] = INF                       # far more than are asked for
+    x[4, 2, :] = INF
+    x[5, 0, hot], x[5, 1:] = INF, -INF       # 3 finite candidates in all
+    x[6, :, hot], s[6, :2] = INF, -INF       # dead beams beside it
+    x[7, 0, 3], x[7, 1, 4], x[7, 2] = INF, torch.finfo(dtype).max, -INF
+    x[7, 1, 5:] = torch.finfo(dtype).min
+    for M in (2, 8, 20):
+        out = check(x, s, M, groups=range(7))
+        # Group 7's lowest candidates lie 2 max(type) below its highest, beyond fp32's
+        # range: the score nearest to them is -inf.
+        want, wp, wt, _ = beam.select(x[7].double().cpu().numpy(), s[7].double().cpu().numpy(), M)
+        with np.errstate(over="ignore"):
+            want = want.astype(np.float32)
+        got, out_of_range = out[0][7].cpu().numpy(), np.isinf(want)
+        assert np.array_equal(np.isinf(got), out_of_range)
+        got, want = got[~out_of_range], want[~out_of_range]
+        assert (np.abs(got - want) <= LOG_SUM + 2.0 ** -24 * np.abs(want)).all()
+        assert out[1][7].tolist() == wp.tolist() and out[2][7].tolist() == wt.tolist()
+    assert torch.isfinite(out[0][0]).sum() == 9 and torch.isfinite(out[0][5]).sum() == 3
+    assert out[1][5].tolist() == [0] * 20
+    low = [v for v in range(20) if v not in hot][:17]
+    assert out[2][5].tolist() == sorted(hot) + low
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_one_beam_with_an_infinite_logit(dtype):
+    x, s = rows(7, 150, 1, 9000, dtype)
+    x[:, 0, 7000] = INF
+    sc, pa, to, fi = lib.gdn_beam_select(x, s, 4)
+    assert torch.equal(sc[:, 0], s[:, 0]) and (sc[:, 1:] == -INF).all()
+    assert to.tolist() == [[7000, 0, 1, 2]] * 150
+    # a step later only one beam lives
+    y = torch.randn(150, 4, 9000, device="cuda").to(dtype)
+    assert (lib.gdn_beam_select(y, sc, 4)[1] == 0).all()
+
+
+def test_the_largest_finite_logit_is_not_infinite():
+    x = torch.zeros(1, 1, 5000, device="cuda")
+    x[0, 0, 9], x[0, 0, 4] = INF, torch.finfo(F32).max
+    sc, _, to, _ = lib.gdn_beam_select(x, torch.zeros(1, 1, device="cuda"), 3)
+    assert to.tolist() == [[9, 0, 1]] and sc.tolist() == [[0.0, -INF, -INF]]
