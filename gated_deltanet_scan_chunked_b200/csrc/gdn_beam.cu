@@ -12,7 +12,8 @@
 // keys (ordered value, then the complement of the index: keys are distinct, and
 // the lower index wins a tie), and leaves them in the first CTA's shared
 // memory, which then forms the rows' log sums and merges the K S lists by score
-// (64-bit floating point, ties to the lowest k V + v).
+// (64-bit floating point, ties to the lowest beam, then to the largest logit, then
+// to the lowest token).
 // Work is cut by element index, never by address, so rows with equal logits
 // get equal sums bit for bit, wherever they lie.
 //
@@ -214,38 +215,35 @@ __device__ __forceinline__ u64 least_of_groups(u64 mine, int g, u64 (*best)[32])
   return v;
 }
 
-// For every c in [0, n): use(c, r), once, r the number of keys above key c; TIE:
-// of equal keys the one with the lower tie value is above.  All threads,
-// several to a c where there are enough; keys and ties 16-byte aligned, n
-// rounded up to even of them there (a key behind the last, 0).
-template <bool TIE, typename Use>
-__device__ __forceinline__ void rank_by_count(const u64* keys, const uint32_t* ties, int n,
-                                              Use use) {
+// For every c in [0, n): use(c, r), once, r the number of keys above key c; of
+// equal keys d is above c where tie(d, c).  All threads, several to a c where
+// there are enough; keys 16-byte aligned, n rounded up to even of them there (a
+// key behind the last, 0).
+template <typename Tie, typename Use>
+__device__ __forceinline__ void rank_by_count(const u64* keys, int n, Tie tie, Use use) {
   const int fit = n > 0 ? kThreads / n : 32;
   const int shift = fit >= 32 ? 5 : fit >= 2 ? 31 - __clz(fit) : 0, team = 1 << shift;
   const int me = threadIdx.x & (team - 1), pairs = (n + 1) >> 1;
   const ulonglong2* two = reinterpret_cast<const ulonglong2*>(keys);
-  [[maybe_unused]] const uint2* tie = reinterpret_cast<const uint2*>(ties);
   for (int c = threadIdx.x >> shift; c < ((n + kThreads - 1) & ~(kThreads - 1));
        c += shift > 0 ? 2 * kThreads : kThreads) {  // (teams of several: once is enough)
     int r = 0;
     const u64 k = c < n ? keys[c] : ~0ull;
-    [[maybe_unused]] const uint32_t f = TIE && c < n ? ties[c] : 0;
 #pragma unroll 4
     for (int d = me; d < pairs; d += team) {
       const ulonglong2 q = two[d];
-      bool x = q.x > k, y = q.y > k;
-      if constexpr (TIE) {
-        const uint2 e = tie[d];
-        x |= (q.x == k) & (e.x < f);
-        y |= (q.y == k) & (e.y < f);
-      }
-      r += (x ? 1 : 0) + (y ? 1 : 0);
+      r += (q.x > k || (q.x == k && tie(2 * d, c)) ? 1 : 0) +
+           (q.y > k || (q.y == k && tie(2 * d + 1, c)) ? 1 : 0);
     }
     for (int o = team >> 1; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
     if (c < n && me == 0) use(c, r);
   }
 }
+
+// (of distinct keys)
+struct NoTies {
+  __device__ __forceinline__ bool operator()(int, int) const { return false; }
+};
 
 // A whole warp: room for `count` items of each lane behind *counter; the first
 // of this lane's places.
@@ -397,7 +395,7 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
     __syncthreads();
     if (tid == 0) sh.win_key[sh.n_win] = 0;
     __syncthreads();
-    rank_by_count<false>(sh.win_key, nullptr, sh.n_win, [&](int i, int r) {
+    rank_by_count(sh.win_key, sh.n_win, NoTies(), [&](int i, int r) {
       if (r == M - 1) sh.lim = sh.win_key[i];
     });
     __syncthreads();
@@ -474,7 +472,7 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
   if (n <= kCap) {
     if (tid == 0) sh.cand[n] = 0;
     __syncthreads();
-    rank_by_count<false>(sh.cand, nullptr, n, [&](int i, int r) {
+    rank_by_count(sh.cand, n, NoTies(), [&](int i, int r) {
       if (r < M) put(r, sh.cand[i]);
     });
     for (int r = n + tid; r < M; r += kThreads) put(r, (u64)0);
@@ -533,8 +531,8 @@ __global__ void __launch_bounds__(kThreads, 3) beam_select_kernel(const BeamArgs
   u64* keys = reinterpret_cast<u64*>(beam_smem);
   const int Np = (N + 3) & ~1;  // (room for a key behind the last, 16-byte steps)
   u64* cand_o = keys + Np;
-  uint32_t* cand_f = reinterpret_cast<uint32_t*>(cand_o + Np);
-  float2* sums = reinterpret_cast<float2*>(cand_f + Np);
+  uint32_t* cand_i = reinterpret_cast<uint32_t*>(cand_o + Np);
+  float2* sums = reinterpret_cast<float2*>(cand_i + Np);
   const uint32_t keys0 = sm100::mapa_shared(sm100::smem_u32(keys), 0);
   const uint32_t sums0 = sm100::mapa_shared(sm100::smem_u32(sums), 0);
   float my_score = 0.f;  // (the first CTA's thread k: beam k's, loaded ahead)
@@ -613,21 +611,20 @@ __global__ void __launch_bounds__(kThreads, 3) beam_select_kernel(const BeamArgs
     }
     __syncthreads();
   }
-  auto candidate = [&](int i, u64& o, uint32_t& flat) {  // (o = 0: none)
+  auto candidate = [&](int i) -> u64 {  // (0: none)
     const u64 key = keys[i];
     const int k = (i % lists) / S;
     const float x = unordered((uint32_t)(key >> 32));
-    o = key == 0 ? 0 : ordered64(sh.score[k] + (gap((double)x, (double)sh.top[k]) - sh.log_sum[k]));
-    flat = (uint32_t)k * (uint32_t)a.V + ~(uint32_t)key;
+    return key == 0 ? 0 : ordered64(sh.score[k] + (gap((double)x, (double)sh.top[k]) - sh.log_sum[k]));
   };
-  // The best M by (score, then the lowest flat index): those at or above the
-  // limit, ranked by counting.  (Equal scores may put more there than ranks
-  // need, never fewer.)
+  // The best M: those at or above the limit, ranked by counting.  (Equal scores
+  // may put more there than ranks need, never fewer.)  Of equal scores the lower
+  // beam's goes first, within a beam the larger key: where a large top or score
+  // makes the scores of different logits one number, they keep the logits' order,
+  // by which the lists were cut.
   u64 mine = 0;
   for (int i = tid; i < N; i += kThreads) {
-    u64 o;
-    uint32_t flat;
-    candidate(i, o, flat);
+    const u64 o = candidate(i);
     mine = o > mine ? o : mine;
   }
   int groups = 1;
@@ -635,26 +632,29 @@ __global__ void __launch_bounds__(kThreads, 3) beam_select_kernel(const BeamArgs
   const u64 lim = least_of_groups(mine, groups, sh.best);
   for (int i0 = tid & ~31; i0 < N; i0 += kThreads) {
     const int i = i0 + (tid & 31);
-    u64 o = 0;
-    uint32_t flat = 0;
-    if (mine >= lim && i < N) candidate(i, o, flat);
+    const u64 o = mine >= lim && i < N ? candidate(i) : 0;
     const bool in = o != 0 && o >= lim;
     if (!__any_sync(0xffffffffu, in)) continue;
     const int c = places(in, &sh.n_cand);
     if (in) {
       cand_o[c] = o;
-      cand_f[c] = flat;
+      cand_i[c] = (uint32_t)(i % lists / S) << 16 | (uint32_t)i;
     }
   }
   __syncthreads();
   const int n = sh.n_cand;
   if (tid == 0) cand_o[n] = 0;
   __syncthreads();
-  rank_by_count<true>(cand_o, cand_f, n, [&](int c, int r) {
+  auto first = [&](int d, int c) {
+    const uint32_t x = cand_i[d], y = cand_i[c];
+    return x >> 16 != y >> 16 ? x < y : keys[x & 0xffffu] > keys[y & 0xffffu];
+  };
+  static_assert(kBeamMergeKeys <= 0x10000, "the list's place in 16 bits");
+  rank_by_count(cand_o, n, first, [&](int c, int r) {
     if (r >= M) return;
     const u64 o = cand_o[c];
-    const uint32_t flat = cand_f[c];
-    const int k = (int)(flat / (uint32_t)a.V), token = (int)(flat % (uint32_t)a.V);
+    const int k = (int)(cand_i[c] >> 16);
+    const int token = (int)~(uint32_t)keys[cand_i[c] & 0xffffu];
     const int64_t at = g * M + r;
     a.out_scores[at] = (float)unordered64(o);
     a.out_parents[at] = k;

@@ -571,7 +571,8 @@ gdn_status gdn_glr_step(const void* x, const void* log_alpha, const void* beta,
  *
  * The candidates of a group are all (beam k, token v), scored
  *     c = scores[k] + logits[k][v] - log sum_v' exp(logits[k][v'])
- * and ordered by c, then by the lowest k V + v (within a beam, by the logit).
+ * and ordered by c, then by the lowest k V + v; within a beam by the logit, also
+ * where 64 bits do not tell the scores of different logits apart.
  * A finished beam has one continuation, end_token at c = scores[k]; its other
  * tokens score -inf.  A beam whose score is not finite scores -inf throughout,
  * and so does a row of logits that are all -inf; these beams' logits, and

@@ -19,6 +19,18 @@ pytestmark = pytest.mark.gpu
 # 2 (20 * 0.7 * 2^-24 in the worst case, if all weight lay there; at most a
 # difference of 4.5 + 9.5 counts): 2.5 * 9.5 + 5 + 4 < 35.
 
+
+def choice(x, s, M):
+    """(scores, parents, tokens) of one group by the definition: the score, then the
+    beam, then the logit (of finite scores), then the token."""
+    x, s = x.double().cpu().numpy(), s.double().cpu().numpy()
+    c = beam.table(x, s)
+    k, v = np.indices(c.shape)
+    by = np.where(np.isfinite(c), -x, 0.0)
+    at = np.lexsort([a.reshape(-1) for a in (v, by, k, -c)])[:M]
+    return c.reshape(-1)[at], at // x.shape[1], at % x.shape[1]
+
+
 FILLS = [-1e4, -65504.0, -1e5, -1e7, -3e7, -6.7e7, -6.8e7, -1e9, -1e10, -1e12, -1e18, -1e20,
          -1e25, -1e31]
 
@@ -94,7 +106,7 @@ def test_infinite_logits_leave_the_others_nothing(V, dtype):
         out = check(x, s, M, groups=range(7))
         # Group 7's lowest candidates lie 2 max(type) below its highest, beyond fp32's
         # range: the score nearest to them is -inf.
-        want, wp, wt, _ = beam.select(x[7].double().cpu().numpy(), s[7].double().cpu().numpy(), M)
+        want, wp, wt = choice(x[7], s[7], M)
         with np.errstate(over="ignore"):
             want = want.astype(np.float32)
         got, out_of_range = out[0][7].cpu().numpy(), np.isinf(want)
@@ -125,3 +137,24 @@ def test_the_largest_finite_logit_is_not_infinite():
     x[0, 0, 9], x[0, 0, 4] = INF, torch.finfo(F32).max
     sc, _, to, _ = lib.gdn_beam_select(x, torch.zeros(1, 1, device="cuda"), 3)
     assert to.tolist() == [[9, 0, 1]] and sc.tolist() == [[0.0, -INF, -INF]]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("top,score", [(1e20, 0.0), (3.0, 1e20), (1e17, -1e17)])
+def test_a_beam_keeps_the_order_of_its_logits(top, score, dtype):
+    """Where the top logit or the score swallows the others' differences in 64 bits,
+    a beam's candidates still go by logit; of different beams, the lower first."""
+    V, M = 5003, 12
+    g = torch.Generator().manual_seed(2)
+    x = torch.randn(2, 2, V, generator=g).clamp_(-2.9, 2.9).to(dtype).cuda()
+    x[0, :, 4001] = top
+    x[1, 0, 17] = top
+    s = torch.full((2, 2), score, device="cuda")
+    s[1, 1] = -INF                           # one beam; in group 0 two with equal scores
+    sc, pa, to, _ = lib.gdn_beam_select(x, s, M)
+    for n, k, M_k in ((1, 0, M), (0, 0, M if score == 1e20 else M - 1)):
+        order = torch.sort(x[n, k].float(), descending=True, stable=True).indices
+        mine = to[n][pa[n] == k].tolist()
+        assert mine == order[:M_k].tolist() and len(mine) == M_k
+    if score != 1e20:                        # the other beam's top comes before all the rest
+        assert pa[0].tolist() == [0, 1] + [0] * (M - 2) and to[0, 1] == 4001
