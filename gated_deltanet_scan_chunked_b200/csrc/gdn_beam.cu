@@ -775,7 +775,7 @@ gdn_status launch_beam_select(BeamArgs a, cudaStream_t stream) {
       segs = s;
     }
   }
-  a.seg_len = ((a.V + segs - 1) / segs + step - 1) / step * step;
+  a.seg_len = (((int64_t)a.V + segs - 1) / segs + step - 1) / step * step;
   a.n_seg = (int)((a.V + a.seg_len - 1) / a.seg_len);
   const int lists = a.K * a.n_seg;
   attr.val.clusterDim.x = (unsigned)cluster;

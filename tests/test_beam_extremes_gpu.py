@@ -158,3 +158,17 @@ def test_a_beam_keeps_the_order_of_its_logits(top, score, dtype):
         assert mine == order[:M_k].tolist() and len(mine) == M_k
     if score != 1e20:                        # the other beam's top comes before all the rest
         assert pa[0].tolist() == [0, 1] + [0] * (M - 2) and to[0, 1] == 4001
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("V", [2 ** 31 - 1, 2 ** 31 - 9])
+def test_the_longest_vocabulary(V, dtype):
+    """K V just below 2^31.  The row's sum is V - 4 ones (exact: no partial sum but
+    the last few is above 2^24, and those are multiples of its step) and 4 e^9."""
+    x = torch.zeros(1, 1, V, dtype=dtype, device="cuda")
+    at = [7, V // 2, V - 2, V - 1]
+    x[0, 0, at] = 9.0
+    sc, pa, to, _ = lib.gdn_beam_select(x, torch.zeros(1, 1, device="cuda"), 6)
+    assert to.tolist() == [at + [0, 1]] and (pa == 0).all()
+    want = torch.tensor([9.0] * 4 + [0.0] * 2, dtype=torch.float64) - np.log(V - 4 + 4 * np.exp(9))
+    assert (sc[0].cpu().double() - want).abs().max() <= LOG_SUM + 2.0 ** -24 * 22
