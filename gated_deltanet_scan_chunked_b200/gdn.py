@@ -4,6 +4,11 @@ Argument marshalling only: every step of the computation runs in the CUDA
 kernels of libgdn.so.  PyTorch supplies device memory and the current
 stream.  There is no fallback: if the library is missing or the tensors are
 not on a CUDA device, the call raises.
+
+A call given ``stream=`` runs on that stream.  What it allocates is that
+stream's memory, and neither that nor its arguments' memory goes to others
+before both streams are done with it; but it is the caller who makes the
+stream wait for whatever still produces the arguments.
 """
 from __future__ import annotations
 
@@ -157,10 +162,43 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream_handle(stream) -> ctypes.c_void_p:
+def _stream_handle(stream=None) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _tensors(v):
+    """The tensors of an argument or result, lists and dicts of them included."""
+    if isinstance(v, torch.Tensor):
+        yield v
+    elif isinstance(v, (list, tuple)):
+        for w in v:
+            yield from _tensors(w)
+    elif isinstance(v, dict):
+        yield from _tensors(list(v.values()))
+
+
+def _on_stream(stream, call, *args):
+    """call(*args) with the given stream as torch's current one, so that what the
+    call allocates comes from that stream's own memory: a block just freed on
+    another stream may still be in use by work queued there.  The arguments must
+    not go to others before the stream has done with them, nor the results
+    before the caller's current stream has."""
+    used = [t for t in _tensors(args) if t.is_cuda]
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, used[0].device if used else None)
+    for t in used:
+        if t.device != stream.device:
+            raise ValueError("the stream is on %s, a tensor on %s" % (stream.device, t.device))
+    outer = torch.cuda.current_stream(stream.device)
+    for t in used:
+        t.record_stream(stream)
+    with torch.cuda.stream(stream):
+        out = call(*args)
+    for t in _tensors(out):
+        t.record_stream(outer)
+    return out
 
 
 def _dtype_code_of(dtype) -> int:
@@ -210,6 +248,10 @@ def gdn_chunk_fwd(q, k, v, log_alpha, beta, g=None, norm_w=None,
     layout), or "auto" (allocated here through torch when the path may use
     it).  A workspace must not be shared by calls that can overlap.
     """
+    if stream is not None:
+        return _on_stream(stream, gdn_chunk_fwd, q, k, v, log_alpha, beta, g, norm_w,
+                          initial_state, cu_seqlens, l2norm_qk, eps_l2, eps_norm, scale, y,
+                          final_state, output_final_state, path, workspace)
     lib = load()
     dev = q.device
     dt = _dtype_code(q)
@@ -242,7 +284,7 @@ def gdn_chunk_fwd(q, k, v, log_alpha, beta, g=None, norm_w=None,
         _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _ptr(g), _ptr(norm_w),
         _ptr(initial_state), _ptr(cu_seqlens), n_seq, T, Hqk, Hv, dk, dv, dt,
         1 if l2norm_qk else 0, float(eps_l2), float(eps_norm), float(scale), _ptr(y),
-        _ptr(final_state), PATHS[path], _ptr(workspace), ws_bytes, _stream_handle(stream))
+        _ptr(final_state), PATHS[path], _ptr(workspace), ws_bytes, _stream_handle())
     if st != GDN_OK:
         raise GdnError(st, "gdn_chunk_fwd")
     return y, final_state
@@ -256,6 +298,10 @@ def gdn_chunk_fwd_static_ws(q, k, v, log_alpha, beta, g=None, norm_w=None,
     """The split-layout prefill with the library's own fixed workspace (at
     most 48 sequence x head items); arguments and results as gdn_chunk_fwd.
     Calls that can overlap must not be made (they share that workspace)."""
+    if stream is not None:
+        return _on_stream(stream, gdn_chunk_fwd_static_ws, q, k, v, log_alpha, beta, g, norm_w,
+                          initial_state, cu_seqlens, l2norm_qk, eps_l2, eps_norm, scale, y,
+                          final_state, output_final_state)
     lib = load()
     dev = q.device
     dt = _dtype_code(q)
@@ -278,7 +324,7 @@ def gdn_chunk_fwd_static_ws(q, k, v, log_alpha, beta, g=None, norm_w=None,
         _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _ptr(g), _ptr(norm_w),
         _ptr(initial_state), _ptr(cu_seqlens), n_seq, T, Hqk, Hv, dk, dv, dt,
         1 if l2norm_qk else 0, float(eps_l2), float(eps_norm), float(scale), _ptr(y),
-        _ptr(final_state), _stream_handle(stream))
+        _ptr(final_state), _stream_handle())
     if st != GDN_OK:
         raise GdnError(st, "gdn_chunk_fwd_static_ws")
     return y, final_state
@@ -305,6 +351,10 @@ def gdn_chunk_bwd(q, k, v, log_alpha, beta, dy, g=None, norm_w=None,
     at least ``bwd_workspace_size(...)`` bytes, or None (allocated here
     through torch).
     """
+    if stream is not None:
+        return _on_stream(stream, gdn_chunk_bwd, q, k, v, log_alpha, beta, dy, g, norm_w,
+                          initial_state, d_final_state, cu_seqlens, l2norm_qk, eps_l2, eps_norm,
+                          scale, want_d_initial_state, want_dnorm_w, workspace)
     lib = load()
     dev = q.device
     dt = _dtype_code(q)
@@ -338,7 +388,7 @@ def gdn_chunk_bwd(q, k, v, log_alpha, beta, dy, g=None, norm_w=None,
         _ptr(d_final_state), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]),
         _ptr(out["dlog_alpha"]), _ptr(out["dbeta"]), _ptr(out.get("dg")),
         _ptr(out.get("dnorm_w")), _ptr(out.get("d_initial_state")), _ptr(workspace),
-        workspace.numel(), _stream_handle(stream))
+        workspace.numel(), _stream_handle())
     if st != GDN_OK:
         raise GdnError(st, "gdn_chunk_bwd")
     return out
@@ -350,6 +400,9 @@ def gdn_decode_step(q, k, v, log_alpha, beta, state, g=None, norm_w=None,
     """One token per sequence; ``state`` [N, H_v, d_k, d_v] fp32 is updated
     in place.  q, k [N, H_qk, d_k]; v [N, H_v, d_v]; gates [N, H_v].
     Returns y [N, H_v, d_v]."""
+    if stream is not None:
+        return _on_stream(stream, gdn_decode_step, q, k, v, log_alpha, beta, state, g, norm_w,
+                          l2norm_qk, eps_l2, eps_norm, scale, y)
     lib = load()
     dev = q.device
     dt = _dtype_code(q)
@@ -366,7 +419,7 @@ def gdn_decode_step(q, k, v, log_alpha, beta, state, g=None, norm_w=None,
     st = lib.gdn_decode_step(
         _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _ptr(g), _ptr(norm_w),
         _ptr(state), N, Hqk, Hv, dk, dv, dt, 1 if l2norm_qk else 0, float(eps_l2),
-        float(eps_norm), float(scale), _ptr(y), _stream_handle(stream))
+        float(eps_norm), float(scale), _ptr(y), _stream_handle())
     if st != GDN_OK:
         raise GdnError(st, "gdn_decode_step")
     return y
@@ -381,6 +434,9 @@ def gdn_decode_multi(q, k, v, log_alpha, beta, state_in, state_out="in_place",
     None (not written).  snapshots: None, True (allocated here), or a
     [T_s, N, H_v, d_k, d_v] fp32 tensor receiving the state after each
     token.  Returns (y, snapshots)."""
+    if stream is not None:
+        return _on_stream(stream, gdn_decode_multi, q, k, v, log_alpha, beta, state_in, state_out,
+                          snapshots, g, norm_w, l2norm_qk, eps_l2, eps_norm, scale, y)
     lib = load()
     dev = q.device
     dt = _dtype_code(q)
@@ -405,7 +461,7 @@ def gdn_decode_multi(q, k, v, log_alpha, beta, state_in, state_out="in_place",
         _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _ptr(g), _ptr(norm_w),
         _ptr(state_in), _ptr(state_out), _ptr(snapshots), N, T_s, Hqk, Hv, dk, dv, dt,
         1 if l2norm_qk else 0, float(eps_l2), float(eps_norm), float(scale), _ptr(y),
-        _stream_handle(stream))
+        _stream_handle())
     if st != GDN_OK:
         raise GdnError(st, "gdn_decode_multi")
     return y, snapshots
@@ -423,6 +479,9 @@ def gdn_conv_frontend(q, k, v, conv_w, conv_state_in=None, cu_seqlens=None,
     k | v); conv_state_in [n_seq, H_v, 3, 2 d_k + d_v] fp32 or None;
     conv_state_out: True (allocated here), a tensor, or None (not written).
     Returns (q', k', v', conv_state_out)."""
+    if stream is not None:
+        return _on_stream(stream, gdn_conv_frontend, q, k, v, conv_w, conv_state_in, cu_seqlens,
+                          conv_state_out, out)
     lib = load()
     dev = q.device
     dt = _dtype_code(q)
@@ -443,7 +502,7 @@ def gdn_conv_frontend(q, k, v, conv_w, conv_state_in=None, cu_seqlens=None,
     st = lib.gdn_conv_frontend(
         _ptr(q), _ptr(k), _ptr(v), _ptr(conv_w), _ptr(conv_state_in), _ptr(conv_state_out),
         _ptr(cu_seqlens), n_seq, T, Hqk, Hv, dk, dv, dt, _ptr(qo), _ptr(ko), _ptr(vo),
-        _stream_handle(stream))
+        _stream_handle())
     if st != GDN_OK:
         raise GdnError(st, "gdn_conv_frontend")
     return qo, ko, vo, conv_state_out
@@ -464,6 +523,11 @@ def gdn_chunk_fwd_conv(q, k, v, conv_w, log_alpha, beta, conv_state_in=None,
     """Prefill on pre-conv q, k, v: the front end, then gdn_chunk_fwd.
     Returns (y, final_state, conv_state_out).  ``workspace``: a uint8 CUDA
     tensor of at least conv_workspace_size(...) bytes, or None (allocated)."""
+    if stream is not None:
+        return _on_stream(stream, gdn_chunk_fwd_conv, q, k, v, conv_w, log_alpha, beta,
+                          conv_state_in, conv_state_out, g, norm_w, initial_state, cu_seqlens,
+                          l2norm_qk, eps_l2, eps_norm, scale, y, final_state, output_final_state,
+                          path, workspace)
     lib = load()
     dev = q.device
     dt = _dtype_code(q)
@@ -495,7 +559,7 @@ def gdn_chunk_fwd_conv(q, k, v, conv_w, log_alpha, beta, conv_state_in=None,
         _ptr(log_alpha), _ptr(beta), _ptr(g), _ptr(norm_w), _ptr(initial_state),
         _ptr(cu_seqlens), n_seq, T, Hqk, Hv, dk, dv, dt, 1 if l2norm_qk else 0,
         float(eps_l2), float(eps_norm), float(scale), _ptr(y), _ptr(final_state), PATHS[path],
-        _ptr(workspace), workspace.numel(), _stream_handle(stream))
+        _ptr(workspace), workspace.numel(), _stream_handle())
     if st != GDN_OK:
         raise GdnError(st, "gdn_chunk_fwd_conv")
     return y, final_state, conv_state_out
@@ -509,6 +573,10 @@ def gdn_decode_conv(q, k, v, conv_w, log_alpha, beta, state_in, conv_state,
     [N, T_s, H_qk, d_k]; v [N, T_s, H_v, d_v]; conv_state [N, H_v, 3,
     2 d_k + d_v] fp32, updated in place (None: zeros, not written).  Returns
     (y, snapshots)."""
+    if stream is not None:
+        return _on_stream(stream, gdn_decode_conv, q, k, v, conv_w, log_alpha, beta, state_in,
+                          conv_state, state_out, snapshots, g, norm_w, l2norm_qk, eps_l2, eps_norm,
+                          scale, y)
     lib = load()
     dev = q.device
     dt = _dtype_code(q)
@@ -533,7 +601,7 @@ def gdn_decode_conv(q, k, v, conv_w, log_alpha, beta, state_in, conv_state,
         _ptr(q), _ptr(k), _ptr(v), _ptr(conv_w), _ptr(conv_state), _ptr(log_alpha),
         _ptr(beta), _ptr(g), _ptr(norm_w), _ptr(state_in), _ptr(state_out), _ptr(snapshots),
         N, T_s, Hqk, Hv, dk, dv, dt, 1 if l2norm_qk else 0, float(eps_l2), float(eps_norm),
-        float(scale), _ptr(y), _stream_handle(stream))
+        float(scale), _ptr(y), _stream_handle())
     if st != GDN_OK:
         raise GdnError(st, "gdn_decode_conv")
     return y, snapshots
@@ -548,6 +616,9 @@ def gdn_gr_read(codes, scales, gamma, W_d, W_u, W_w, eps=1e-6, x=None, s=None,
     """Gated Residual read: codes [T, n_r, d] uint8 (E4M3), scales [T, n_r]
     fp32, gamma [n_r, d] fp32, W_d [rank, n_r d], W_u [n_r d, rank], W_w
     [n_r, n_r d] bf16.  Returns (x [T, d] bf16, s [T, n_r] fp32)."""
+    if stream is not None:
+        return _on_stream(stream, gdn_gr_read, codes, scales, gamma, W_d, W_u, W_w, eps, x, s,
+                          workspace)
     lib = load()
     dev = codes.device
     T, n_r, d = codes.shape
@@ -566,7 +637,7 @@ def gdn_gr_read(codes, scales, gamma, W_d, W_u, W_w, eps=1e-6, x=None, s=None,
         workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
     st = lib.gdn_gr_read(_ptr(codes), _ptr(scales), _ptr(gamma), _ptr(W_d), _ptr(W_u),
                          _ptr(W_w), T, n_r, d, rank, float(eps), _ptr(x), _ptr(s),
-                         _ptr(workspace), workspace.numel(), _stream_handle(stream))
+                         _ptr(workspace), workspace.numel(), _stream_handle())
     if st != GDN_OK:
         raise GdnError(st, "gdn_gr_read")
     return x, s
@@ -574,6 +645,8 @@ def gdn_gr_read(codes, scales, gamma, W_d, W_u, W_w, eps=1e-6, x=None, s=None,
 
 def gdn_gr_write(codes, scales, y, s, stream=None):
     """Gated Residual write, in place: R'_i = R_i + s_i y, requantised."""
+    if stream is not None:
+        return _on_stream(stream, gdn_gr_write, codes, scales, y, s)
     lib = load()
     dev = codes.device
     T, n_r, d = codes.shape
@@ -582,7 +655,7 @@ def gdn_gr_write(codes, scales, y, s, stream=None):
     _check(y, "y", torch.bfloat16, dev)
     _check(s, "s", torch.float32, dev)
     st = lib.gdn_gr_write(_ptr(codes), _ptr(scales), _ptr(y), _ptr(s), T, n_r, d,
-                          _stream_handle(stream))
+                          _stream_handle())
     if st != GDN_OK:
         raise GdnError(st, "gdn_gr_write")
     return codes, scales
@@ -605,21 +678,6 @@ def _device_of(t: torch.Tensor, name: str) -> int:
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor (libgdn has no CPU path)" % name)
     return t.get_device()
-
-
-def _on(i: int, stream):
-    """Handle of the stream that a call on device i runs on: the given one, or
-    the device's current one."""
-    return _current_stream(i) if stream is None else stream.cuda_stream
-
-
-def _keep(stream, *tensors):
-    """Memory made here (on torch's current stream) is used on a given stream: it
-    must not go to others before that use is over."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
 
 
 def _addr(t: Optional[torch.Tensor]):
@@ -679,12 +737,15 @@ def gdn_glr_fwd(x, log_alpha, beta=None, initial_state=None, cu_seqlens=None, y=
     checkpoints: None (not written), True (allocated here) or a tensor of
     glr_checkpoint_shape(T, C) fp32, for gdn_glr_bwd.
     """
+    if stream is not None:
+        return _on_stream(stream, gdn_glr_fwd, x, log_alpha, beta, initial_state, cu_seqlens, y,
+                          final_state, output_final_state, checkpoints)
     lib = _lib or load()
     i = _device_of(x, "x")
     if i != _current_device():
         with torch.cuda.device(i):
             return gdn_glr_fwd(x, log_alpha, beta, initial_state, cu_seqlens, y, final_state,
-                               output_final_state, checkpoints, stream)
+                               output_final_state, checkpoints)
     dt, gate, beta = _glr_inputs(x, log_alpha, beta, i)
     T, C = x.shape
     n_seq = _glr_sequences(cu_seqlens, i)
@@ -692,7 +753,6 @@ def gdn_glr_fwd(x, log_alpha, beta=None, initial_state=None, cu_seqlens=None, y=
         _need(initial_state, "initial_state", torch.float32, (n_seq, C), i)
     if y is None:
         y = torch.empty_like(x)
-        _keep(stream, y)
     else:
         _need(y, "y", x.dtype, x.shape, i)
     if final_state is not None:
@@ -702,15 +762,13 @@ def gdn_glr_fwd(x, log_alpha, beta=None, initial_state=None, cu_seqlens=None, y=
             final_state = torch.empty_like(initial_state)
         else:
             final_state = x.new_empty((n_seq, C), dtype=torch.float32)
-        _keep(stream, final_state)
     if checkpoints is True:
         checkpoints = x.new_empty(glr_checkpoint_shape(T, C), dtype=torch.float32)
-        _keep(stream, checkpoints)
     elif checkpoints is not None:
         _need(checkpoints, "checkpoints", torch.float32, glr_checkpoint_shape(T, C), i)
     st = lib.gdn_glr_fwd(x.data_ptr(), log_alpha.data_ptr(), _addr(beta), gate,
                          _addr(initial_state), _addr(cu_seqlens), n_seq, T, C, dt, y.data_ptr(),
-                         _addr(final_state), _addr(checkpoints), _on(i, stream))
+                         _addr(final_state), _addr(checkpoints), _current_stream(i))
     if st != GDN_OK:
         raise GdnError(st, "gdn_glr_fwd")
     return y, final_state, checkpoints
@@ -730,12 +788,15 @@ def gdn_glr_bwd(x, log_alpha, dy, beta=None, initial_state=None, d_final_state=N
     ``checkpoints``: what the forward returned for them; without it they are
     computed again into ``workspace`` (a uint8 CUDA tensor of at least
     glr_bwd_workspace_size(T, C) bytes, or None: allocated here)."""
+    if stream is not None:
+        return _on_stream(stream, gdn_glr_bwd, x, log_alpha, dy, beta, initial_state,
+                          d_final_state, cu_seqlens, checkpoints, want_d_initial_state, workspace)
     lib = _lib or load()
     i = _device_of(x, "x")
     if i != _current_device():
         with torch.cuda.device(i):
             return gdn_glr_bwd(x, log_alpha, dy, beta, initial_state, d_final_state, cu_seqlens,
-                               checkpoints, want_d_initial_state, workspace, stream)
+                               checkpoints, want_d_initial_state, workspace)
     dt, gate, beta = _glr_inputs(x, log_alpha, beta, i)
     T, C = x.shape
     n_seq = _glr_sequences(cu_seqlens, i)
@@ -751,19 +812,17 @@ def gdn_glr_bwd(x, log_alpha, dy, beta=None, initial_state=None, d_final_state=N
     elif checkpoints is None:
         workspace = x.new_empty(max(int(lib.gdn_glr_bwd_workspace_size(T, C)), 1),
                                 dtype=torch.uint8)
-        _keep(stream, workspace)
     out = dict(dx=torch.empty_like(x), dlog_alpha=torch.empty_like(x))
     if gate == _GATE_BETA:
         out["dbeta"] = torch.empty_like(x)
     if want_d_initial_state:
         out["d_initial_state"] = x.new_empty((n_seq, C), dtype=torch.float32)
-    _keep(stream, *out.values())
     st = lib.gdn_glr_bwd(x.data_ptr(), log_alpha.data_ptr(), _addr(beta), gate,
                          _addr(initial_state), _addr(cu_seqlens), n_seq, T, C, dt, dy.data_ptr(),
                          _addr(d_final_state), _addr(checkpoints), out["dx"].data_ptr(),
                          out["dlog_alpha"].data_ptr(), _addr(out.get("dbeta")),
                          _addr(out.get("d_initial_state")), _addr(workspace),
-                         0 if workspace is None else workspace.numel(), _on(i, stream))
+                         0 if workspace is None else workspace.numel(), _current_stream(i))
     if st != GDN_OK:
         raise GdnError(st, "gdn_glr_bwd")
     return out
@@ -773,22 +832,23 @@ def gdn_glr_step(x, log_alpha, state, beta=None, y=None, stream=None) -> torch.T
     """One token per sequence of the gated linear recurrence: x, log_alpha [N,
     C]; beta as for gdn_glr_fwd; ``state`` [N, C] fp32 is updated in place.
     Returns y [N, C]."""
+    if stream is not None:
+        return _on_stream(stream, gdn_glr_step, x, log_alpha, state, beta, y)
     lib = _lib or load()
     i = _device_of(x, "x")
     if i != _current_device():
         with torch.cuda.device(i):
-            return gdn_glr_step(x, log_alpha, state, beta, y, stream)
+            return gdn_glr_step(x, log_alpha, state, beta, y)
     dt, gate, beta = _glr_inputs(x, log_alpha, beta, i)
     shape = x.shape
     _need(state, "state", torch.float32, shape, i)
     if y is None:
         y = torch.empty_like(x)
-        _keep(stream, y)
     else:
         _need(y, "y", x.dtype, shape, i)
     st = lib.gdn_glr_step(x.data_ptr(), log_alpha.data_ptr(), _addr(beta), gate,
                           state.data_ptr(), shape[0], shape[1], dt, y.data_ptr(),
-                          _on(i, stream))
+                          _current_stream(i))
     if st != GDN_OK:
         raise GdnError(st, "gdn_glr_step")
     return y
@@ -807,12 +867,14 @@ def gdn_beam_select(logits, scores, n_candidates, finished=None, end_token=-1, o
     parents, tokens, finished), [G, M] fp32, int32, int32 and uint8, or writes
     them into ``out``, four such tensors (with M = K, out[0] may be scores and
     out[3] finished)."""
+    if stream is not None:
+        return _on_stream(stream, gdn_beam_select, logits, scores, n_candidates, finished,
+                          end_token, out)
     lib = _lib or load()
     i = _device_of(logits, "logits")
     if i != _current_device():
         with torch.cuda.device(i):
-            return gdn_beam_select(logits, scores, n_candidates, finished, end_token, out,
-                                   stream)
+            return gdn_beam_select(logits, scores, n_candidates, finished, end_token, out)
     dt = _CODES.get(logits.dtype)
     if dt is None:
         raise TypeError("logits must be bfloat16 or float32, got %s" % logits.dtype)
@@ -838,7 +900,6 @@ def gdn_beam_select(logits, scores, n_candidates, finished=None, end_token=-1, o
         best = torch.empty_like(scores) if M == K else scores.new_empty((G, M))
         parents = torch.empty_like(best, dtype=torch.int32)
         out = (best, parents, torch.empty_like(parents), torch.empty_like(best, dtype=torch.uint8))
-        _keep(stream, *out)
     else:
         out = tuple(out)
         for t, name, dtype in zip(out, ("out scores", "out parents", "out tokens", "out finished"),
@@ -847,7 +908,7 @@ def gdn_beam_select(logits, scores, n_candidates, finished=None, end_token=-1, o
     st = lib.gdn_beam_select(logits.data_ptr(), ld, scores.data_ptr(), _addr(finished),
                              int(end_token), G, K, V, M, dt, out[0].data_ptr(),
                              out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(),
-                             _on(i, stream))
+                             _current_stream(i))
     if st != GDN_OK:
         raise GdnError(st, "gdn_beam_select")
     return out
@@ -858,11 +919,13 @@ def gdn_state_reorder(states, parents, stream=None):
     g K + j of every tensor becomes what row g K + parents[g, j] was.
     ``states``: a tensor or a list of up to 16, each contiguous with G * K rows
     (recurrent states, conv states, token histories; any type)."""
+    if stream is not None:
+        return _on_stream(stream, gdn_state_reorder, states, parents)
     lib = _lib or load()
     i = _device_of(parents, "parents")
     if i != _current_device():
         with torch.cuda.device(i):
-            return gdn_state_reorder(states, parents, stream)
+            return gdn_state_reorder(states, parents)
     if parents.dim() != 2:
         raise ValueError("parents must be [groups, beams], got %s" % (tuple(parents.shape),))
     _need(parents, "parents", torch.int32, parents.shape, i)
@@ -879,7 +942,7 @@ def gdn_state_reorder(states, parents, stream=None):
             raise ValueError("states[%d] must have %d rows, got %s" % (j, rows, tuple(t.shape)))
         ptrs[j] = t.data_ptr()
         sizes[j] = t.nbytes // rows if rows else 0
-    st = lib.gdn_state_reorder(ptrs, sizes, n, parents.data_ptr(), G, K, _on(i, stream))
+    st = lib.gdn_state_reorder(ptrs, sizes, n, parents.data_ptr(), G, K, _current_stream(i))
     if st != GDN_OK:
         raise GdnError(st, "gdn_state_reorder")
     return states

@@ -1,0 +1,32 @@
+"""Rules of the Python binding, checked without a GPU."""
+import inspect
+
+import pytest
+import torch
+
+import gated_deltanet_scan_chunked_b200 as lib
+from gated_deltanet_scan_chunked_b200 import gdn
+
+
+def test_every_call_that_takes_a_stream_runs_under_it():
+    """Allocations of a call with a stream come from that stream's memory: the
+    call is made again with the stream as torch's current one."""
+    calls = [n for n in dir(gdn) if n.startswith("gdn_") and callable(getattr(gdn, n))
+             and n != "gdn_check_device_error"]
+    assert len(calls) >= 15
+    for n in calls:
+        f = getattr(gdn, n)
+        names = list(inspect.signature(f).parameters)
+        assert names[-1] == "stream", n
+        text = inspect.getsource(f)
+        body = text[text.index('"""', text.index('"""') + 3) + 3:]
+        want = "if stream is not None: return _on_stream(stream, %s, %s)" % (
+            n, ", ".join(names[:-1]))
+        assert " ".join(body.split()).startswith(want), n
+        assert body.count("stream, ") == 1, n
+
+
+def test_tensors_of_arguments_and_results():
+    a, b, c = (torch.zeros(1) for _ in range(3))
+    got = list(gdn._tensors((a, None, [b, 3], dict(x=c, y="z"), 1.5)))
+    assert [t is u for t, u in zip(got, (a, b, c))] == [True] * 3 and len(got) == 3
