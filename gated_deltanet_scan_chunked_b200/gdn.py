@@ -668,9 +668,17 @@ _GATE_NONE, _GATE_BETA, _GATE_COMPLEMENT = 0, 1, 2
 
 
 # These calls may be as short as a few microseconds, so the binding asks torch
-# for the device and the stream by its cheapest ways.
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
+# for the device and the stream by its cheapest ways.  (Looked up when a call is
+# made: a torch without CUDA has neither, and the rest of the binding, such as
+# header_functions, needs neither.)
+def _current_device() -> int:
+    return torch._C._cuda_getDevice()
+
+
+def _current_stream(i: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(i)
+
+
 _CODES = {torch.bfloat16: GDN_BF16, torch.float32: GDN_FP32}
 
 

@@ -1,10 +1,11 @@
 """Rules of the Python binding, checked without a GPU."""
 import inspect
+import pathlib
+import subprocess
+import sys
 
-import pytest
 import torch
 
-import gated_deltanet_scan_chunked_b200 as lib
 from gated_deltanet_scan_chunked_b200 import gdn
 
 
@@ -30,3 +31,24 @@ def test_tensors_of_arguments_and_results():
     a, b, c = (torch.zeros(1) for _ in range(3))
     got = list(gdn._tensors((a, None, [b, 3], dict(x=c, y="z"), 1.5)))
     assert [t is u for t, u in zip(got, (a, b, c))] == [True] * 3 and len(got) == 3
+
+
+def test_imports_with_a_torch_that_has_no_cuda():
+    code = """
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+import gated_deltanet_scan_chunked_b200 as lib
+from gated_deltanet_scan_chunked_b200 import gdn
+assert "gdn_glr_fwd" in gdn.header_functions()
+x = torch.zeros(4, 8)
+try:
+    lib.gdn_glr_fwd(x, x)
+except ValueError as e:
+    print("refused:", e)
+"""
+    root = str(pathlib.Path(__file__).resolve().parent.parent)
+    out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                         timeout=300)
+    assert out.returncode == 0 and out.stdout.startswith("refused:"), out.stderr[-2000:]

@@ -40,7 +40,7 @@ def cases():
     z, s = randn(8, 4, 5000), torch.zeros(8, 4, device="cuda")
     q5, (q6, S) = delta(), steps()
     dy, w, r = randn(200, 4, 32), conv_w(), residual()
-    h = torch.zeros(1000, 512, device="cuda")  # (not in the calls, whose streams would not wait for it)
+    h = torch.zeros(1000, 512, device="cuda")  # (here: no call waits for the current stream)
     return {
         "glr_fwd": lambda **k: lib.gdn_glr_fwd(x, la, checkpoints=True, **k),
         "glr_bwd": lambda **k: lib.gdn_glr_bwd(x, la, x, **k),
