@@ -692,6 +692,13 @@ def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+def _int32(v: int, name: str) -> int:
+    """v, which goes to an int32 argument (ctypes would cut it to its low 32 bits)."""
+    if not -(1 << 31) <= v < 1 << 31:
+        raise ValueError("%s = %d does not fit in 32 bits" % (name, v))
+    return v
+
+
 def _need(t: torch.Tensor, name: str, dtype, shape, i: int):
     """t is a dense CUDA tensor on device i of that type and shape."""
     if not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == i):
@@ -707,6 +714,7 @@ def _glr_inputs(x, log_alpha, beta, i):
         raise TypeError("x must be bfloat16 or float32, got %s" % dtype)
     if len(shape) != 2 or not x.is_contiguous():
         raise ValueError("x must be contiguous [tokens, channels], got %s" % (tuple(shape),))
+    _int32(shape[1], "channels")
     _need(log_alpha, "log_alpha", dtype, shape, i)
     if beta is None:
         return dt, _GATE_NONE, None
@@ -724,7 +732,7 @@ def _glr_sequences(cu_seqlens, i):
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
         raise ValueError("cu_seqlens must be [n_seq + 1]")
     _need(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, i)
-    return cu_seqlens.shape[0] - 1
+    return _int32(cu_seqlens.shape[0] - 1, "sequences")
 
 
 def glr_checkpoint_shape(total_T: int, C: int):
@@ -849,6 +857,7 @@ def gdn_glr_step(x, log_alpha, state, beta=None, y=None, stream=None) -> torch.T
             return gdn_glr_step(x, log_alpha, state, beta, y)
     dt, gate, beta = _glr_inputs(x, log_alpha, beta, i)
     shape = x.shape
+    _int32(shape[0], "rows")
     _need(state, "state", torch.float32, shape, i)
     if y is None:
         y = torch.empty_like(x)
@@ -890,7 +899,10 @@ def gdn_beam_select(logits, scores, n_candidates, finished=None, end_token=-1, o
         raise ValueError("logits must be [groups, beams, vocabulary], got %s"
                          % (tuple(logits.shape),))
     G, K, V = logits.shape
-    M = int(n_candidates)
+    M, end_token = int(n_candidates), int(end_token)
+    for v, name in ((G, "groups"), (K, "beams"), (V, "vocabulary"), (M, "n_candidates"),
+                    (end_token, "end_token")):
+        _int32(v, name)
     sg, ld, sv = logits.stride()
     if K == 1:
         ld = sg
@@ -914,7 +926,7 @@ def gdn_beam_select(logits, scores, n_candidates, finished=None, end_token=-1, o
                                   (torch.float32, torch.int32, torch.int32, torch.uint8)):
             _need(t, name, dtype, (G, M), i)
     st = lib.gdn_beam_select(logits.data_ptr(), ld, scores.data_ptr(), _addr(finished),
-                             int(end_token), G, K, V, M, dt, out[0].data_ptr(),
+                             end_token, G, K, V, M, dt, out[0].data_ptr(),
                              out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(),
                              _current_stream(i))
     if st != GDN_OK:
@@ -939,7 +951,7 @@ def gdn_state_reorder(states, parents, stream=None):
     _need(parents, "parents", torch.int32, parents.shape, i)
     many = [states] if isinstance(states, torch.Tensor) else states
     G, K = parents.shape
-    rows, n = G * K, len(many)
+    rows, n = _int32(G, "groups") * _int32(K, "beams"), len(many)
     if n == 0:
         raise ValueError("there must be a state to reorder")
     ptrs, sizes = (ctypes.c_void_p * n)(), (ctypes.c_size_t * n)()

@@ -4,6 +4,7 @@ import pathlib
 import subprocess
 import sys
 
+import pytest
 import torch
 
 from gated_deltanet_scan_chunked_b200 import gdn
@@ -52,3 +53,11 @@ except ValueError as e:
     out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
                          timeout=300)
     assert out.returncode == 0 and out.stdout.startswith("refused:"), out.stderr[-2000:]
+
+
+def test_numbers_past_32_bits_are_refused():
+    for v in (0, -1, 2 ** 31 - 1, -2 ** 31):
+        assert gdn._int32(v, "v") == v
+    for v in (2 ** 31, -2 ** 31 - 1, 2 ** 32, 2 ** 32 + 5):
+        with pytest.raises(ValueError, match="v = "):
+            gdn._int32(v, "v")
