@@ -781,7 +781,7 @@ gdn_status launch_beam_select(BeamArgs a, cudaStream_t stream) {
   attr.val.clusterDim.x = (unsigned)cluster;
   cfg.gridDim = dim3((unsigned)cluster, (unsigned)a.n_groups);
   cfg.dynamicSmemBytes = ((size_t)lists * a.M + 3) * 20 + (size_t)lists * sizeof(float2);
-  return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  return launch_status(cudaLaunchKernelEx(&cfg, kernel, a));
 }
 
 gdn_status launch_state_reorder(ReorderArgs a, cudaStream_t stream) {
@@ -797,15 +797,15 @@ gdn_status launch_state_reorder(ReorderArgs a, cudaStream_t stream) {
     if (blocks > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
   }
   if (blocks == 0) return GDN_OK;
-  if (a.K <= 4)
-    state_reorder_kernel<4><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
-  else if (a.K <= 8)
-    state_reorder_kernel<8><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
-  else if (a.K <= 16)
-    state_reorder_kernel<16><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
-  else
-    state_reorder_kernel<32><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
-  return cudaPeekAtLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  void (*kernel)(ReorderArgs) = a.K <= 4    ? state_reorder_kernel<4>
+                                : a.K <= 8  ? state_reorder_kernel<8>
+                                : a.K <= 16 ? state_reorder_kernel<16>
+                                            : state_reorder_kernel<32>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  return launch_status(cudaLaunchKernelEx(&cfg, kernel, a));
 }
 
 }  // namespace gdn

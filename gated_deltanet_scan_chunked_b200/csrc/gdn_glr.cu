@@ -1188,27 +1188,22 @@ gdn_status launch_scan(const GlrArgs& a, bool bwd, cudaStream_t stream) {
   }
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg = scan_config(k, c.cluster, c.smem, groups, stream, &attr);
-  return cudaLaunchKernelEx(&cfg, k.kernel, a, maps) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  return launch_status(cudaLaunchKernelEx(&cfg, k.kernel, a, maps));
 }
 
 template <typename Tin>
 gdn_status launch_step(const GlrArgs& a, int64_t n, cudaStream_t stream) {
-  const unsigned blocks = (unsigned)((n + 8 * 256 - 1) / (8 * 256));
-  const Tin* x = static_cast<const Tin*>(a.x);
-  const Tin* l = static_cast<const Tin*>(a.log_alpha);
-  const Tin* b = static_cast<const Tin*>(a.beta);
-  Tin* y = static_cast<Tin*>(a.y);
-  switch (a.gate) {
-    case kGateNone:
-      glr_step_kernel<Tin, kGateNone><<<blocks, 256, 0, stream>>>(x, l, b, a.final_state, y, n);
-      break;
-    case kGateBeta:
-      glr_step_kernel<Tin, kGateBeta><<<blocks, 256, 0, stream>>>(x, l, b, a.final_state, y, n);
-      break;
-    default:
-      glr_step_kernel<Tin, kGateComp><<<blocks, 256, 0, stream>>>(x, l, b, a.final_state, y, n);
-  }
-  return cudaPeekAtLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  void (*kernel)(const Tin*, const Tin*, const Tin*, float*, Tin*, int64_t) =
+      a.gate == kGateNone   ? glr_step_kernel<Tin, kGateNone>
+      : a.gate == kGateBeta ? glr_step_kernel<Tin, kGateBeta>
+                            : glr_step_kernel<Tin, kGateComp>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((n + 8 * 256 - 1) / (8 * 256)));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  return launch_status(cudaLaunchKernelEx(
+      &cfg, kernel, static_cast<const Tin*>(a.x), static_cast<const Tin*>(a.log_alpha),
+      static_cast<const Tin*>(a.beta), a.final_state, static_cast<Tin*>(a.y), n));
 }
 
 }  // namespace

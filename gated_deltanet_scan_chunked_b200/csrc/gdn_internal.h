@@ -229,6 +229,14 @@ struct ReorderArgs {
 };
 gdn_status launch_state_reorder(ReorderArgs a, cudaStream_t stream);
 
+// A launch's own status.  An error is reported by the call that met it and not
+// left pending: a later launch of the same host thread would be taken for it.
+inline gdn_status launch_status(cudaError_t e) {
+  if (e == cudaSuccess) return GDN_OK;
+  cudaGetLastError();
+  return GDN_ERR_CUDA;
+}
+
 // The library's device error word on the current device (nullptr on failure).
 int* device_error_word();
 
