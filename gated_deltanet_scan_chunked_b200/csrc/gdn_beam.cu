@@ -63,9 +63,8 @@ __device__ __forceinline__ u64 key_of(float x, uint32_t idx) {
 __device__ __forceinline__ float tame(float x) { return fmaxf(x, -INFINITY); }
 // a - b, 0 for equal infinities: where the largest is +inf, the entries that are
 // it share the row equally and the others have nothing.
-template <typename F>
-__device__ __forceinline__ F gap(F a, F b) {
-  return a == b ? F(0) : a - b;
+__device__ __forceinline__ float gap(float a, float b) {
+  return a == b ? 0.f : __fadd_rn(a, -b);
 }
 
 // 16 bytes of a row as floats.
@@ -215,35 +214,37 @@ __device__ __forceinline__ u64 least_of_groups(u64 mine, int g, u64 (*best)[32])
   return v;
 }
 
-// For every c in [0, n): use(c, r), once, r the number of keys above key c; of
-// equal keys d is above c where tie(d, c).  All threads, several to a c where
-// there are enough; keys 16-byte aligned, n rounded up to even of them there (a
-// key behind the last, 0).
-template <typename Tie, typename Use>
-__device__ __forceinline__ void rank_by_count(const u64* keys, int n, Tie tie, Use use) {
+// For every c in [0, n): use(c, r), once, r the number of keys above key c; TIE:
+// of equal keys the one with the lower tie value is above.  All threads,
+// several to a c where there are enough; keys and ties 16-byte aligned, n
+// rounded up to even of them there (a key behind the last, 0).
+template <bool TIE, typename Use>
+__device__ __forceinline__ void rank_by_count(const u64* keys, const u64* ties, int n, Use use) {
   const int fit = n > 0 ? kThreads / n : 32;
   const int shift = fit >= 32 ? 5 : fit >= 2 ? 31 - __clz(fit) : 0, team = 1 << shift;
   const int me = threadIdx.x & (team - 1), pairs = (n + 1) >> 1;
   const ulonglong2* two = reinterpret_cast<const ulonglong2*>(keys);
+  [[maybe_unused]] const ulonglong2* tie = reinterpret_cast<const ulonglong2*>(ties);
   for (int c = threadIdx.x >> shift; c < ((n + kThreads - 1) & ~(kThreads - 1));
        c += shift > 0 ? 2 * kThreads : kThreads) {  // (teams of several: once is enough)
     int r = 0;
     const u64 k = c < n ? keys[c] : ~0ull;
+    [[maybe_unused]] const u64 f = TIE && c < n ? ties[c] : 0;
 #pragma unroll 4
     for (int d = me; d < pairs; d += team) {
       const ulonglong2 q = two[d];
-      r += (q.x > k || (q.x == k && tie(2 * d, c)) ? 1 : 0) +
-           (q.y > k || (q.y == k && tie(2 * d + 1, c)) ? 1 : 0);
+      bool x = q.x > k, y = q.y > k;
+      if constexpr (TIE) {
+        const ulonglong2 e = tie[d];
+        x |= (q.x == k) & (e.x < f);
+        y |= (q.y == k) & (e.y < f);
+      }
+      r += (x ? 1 : 0) + (y ? 1 : 0);
     }
     for (int o = team >> 1; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
     if (c < n && me == 0) use(c, r);
   }
 }
-
-// (of distinct keys)
-struct NoTies {
-  __device__ __forceinline__ bool operator()(int, int) const { return false; }
-};
 
 // A whole warp: room for `count` items of each lane behind *counter; the first
 // of this lane's places.
@@ -272,7 +273,7 @@ struct __align__(16) BeamShared {
   // the merge
   double score[kMaxBeams], log_sum[kMaxBeams];  // score -inf: no finite candidate
   float top[kMaxBeams];
-  int n_inf[kMaxBeams];  // +inf logits of a row with fewer than M of them, else 0
+  int n_inf[kMaxBeams];  // +inf logits of a row (at most M counted)
   unsigned char done[kMaxBeams];
 };
 
@@ -395,7 +396,7 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
     __syncthreads();
     if (tid == 0) sh.win_key[sh.n_win] = 0;
     __syncthreads();
-    rank_by_count(sh.win_key, sh.n_win, NoTies(), [&](int i, int r) {
+    rank_by_count<false>(sh.win_key, nullptr, sh.n_win, [&](int i, int r) {
       if (r == M - 1) sh.lim = sh.win_key[i];
     });
     __syncthreads();
@@ -472,7 +473,7 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
   if (n <= kCap) {
     if (tid == 0) sh.cand[n] = 0;
     __syncthreads();
-    rank_by_count(sh.cand, n, NoTies(), [&](int i, int r) {
+    rank_by_count<false>(sh.cand, nullptr, n, [&](int i, int r) {
       if (r < M) put(r, sh.cand[i]);
     });
     for (int r = n + tid; r < M; r += kThreads) put(r, (u64)0);
@@ -508,6 +509,40 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
   }
 }
 
+// Of a row with +inf logits these share the score, and all other tokens score -inf
+// and go by index, not by logit: its lists are made anew, of M infinite tokens
+// (as 0 above a top of 0), or all and the lowest others.  keys: [M][K S].  All
+// threads.  (Apart from the kernel, whose common path it would lengthen.)
+__device__ __noinline__ void infinite_rows(u64* keys, BeamShared& sh, int K, int M, int S, int V) {
+  const int tid = threadIdx.x;
+  for (int k = 0; k < K; ++k) {
+    const int n_inf = sh.n_inf[k];
+    if (n_inf == 0) continue;
+    auto slot = [&](int i) { return i / S * (K * S) + k * S + i % S; };
+    if (tid == 0) sh.n_multi = 0;
+    __syncthreads();
+    for (int i = tid; i < S * M; i += kThreads) {
+      const u64 key = keys[slot(i)];
+      const bool one = (uint32_t)(key >> 32) == ordered(INFINITY);
+      if (one && n_inf < M) sh.multi[atomicAdd(&sh.n_multi, 1)] = (int)~(uint32_t)key;
+      keys[slot(i)] = one && n_inf == M ? key_of(0.f, ~(uint32_t)key) : 0;
+    }
+    __syncthreads();
+    if (n_inf < M && tid < M) {
+      if (tid < n_inf) keys[slot(tid)] = key_of(0.f, (uint32_t)sh.multi[tid]);
+      int below = 0;  // (the lowest M tokens hold enough others)
+      bool one = false;
+      for (int i = 0; i < n_inf; ++i) {
+        below += sh.multi[i] < tid;
+        one |= sh.multi[i] == tid;
+      }
+      const int i = n_inf + tid - below;
+      if (!one && i < M && tid < V) keys[slot(i)] = key_of(-INFINITY, (uint32_t)tid);
+    }
+    __syncthreads();
+  }
+}
+
 // Order-preserving map of a double (NaN as -inf, -0 as +0) to an unsigned.
 __device__ __forceinline__ u64 ordered64(double x) {
   if (x != x) x = -INFINITY;
@@ -531,8 +566,8 @@ __global__ void __launch_bounds__(kThreads, 3) beam_select_kernel(const BeamArgs
   u64* keys = reinterpret_cast<u64*>(beam_smem);
   const int Np = (N + 3) & ~1;  // (room for a key behind the last, 16-byte steps)
   u64* cand_o = keys + Np;
-  uint32_t* cand_i = reinterpret_cast<uint32_t*>(cand_o + Np);
-  float2* sums = reinterpret_cast<float2*>(cand_i + Np);
+  u64* cand_t = cand_o + Np;
+  float2* sums = reinterpret_cast<float2*>(cand_t + Np);
   const uint32_t keys0 = sm100::mapa_shared(sm100::smem_u32(keys), 0);
   const uint32_t sums0 = sm100::mapa_shared(sm100::smem_u32(sums), 0);
   float my_score = 0.f;  // (the first CTA's thread k: beam k's, loaded ahead)
@@ -564,6 +599,7 @@ __global__ void __launch_bounds__(kThreads, 3) beam_select_kernel(const BeamArgs
 
   // The rows: c = score + ((x - top) - log_sum), the difference of the logits
   // first, since x and top may be as large as the type allows.
+  bool inf = false;
   if (tid < K) {
     float m = -FLT_MAX;
     for (int i = 0; i < S; ++i) m = fmaxf(m, sums[tid * S + i].x);
@@ -576,85 +612,61 @@ __global__ void __launch_bounds__(kThreads, 3) beam_select_kernel(const BeamArgs
     const bool some = my_kind != kDead && s > 0.0, live = some && my_kind == kLive;
     sh.score[tid] = some ? (double)my_score : -INFINITY;
     sh.log_sum[tid] = live ? log(s) : 0.0;
-    sh.top[tid] = live ? m : 0.f;
-    sh.n_inf[tid] = live && m == INFINITY && s < (double)M ? (int)s : 0;
+    inf = live && m == INFINITY;
+    sh.top[tid] = live && !inf ? m : 0.f;
+    sh.n_inf[tid] = inf ? (s < (double)M ? (int)s : M) : 0;
   }
   if (tid == 0) sh.n_cand = 0;
-  __syncthreads();
-  // Of a row with +inf logits all other tokens score -inf, and go by index, not by
-  // logit: its lists are made anew, the infinite tokens and the lowest others.
-  // (Where there are M infinite ones, no others are chosen.)
-  for (int k = 0; k < K; ++k) {
-    const int n_inf = sh.n_inf[k];
-    if (n_inf == 0) continue;
-    auto slot = [&](int i) { return i / S * lists + k * S + i % S; };
-    if (tid == 0) sh.n_multi = 0;
-    __syncthreads();
-    for (int i = tid; i < S * M; i += kThreads) {
-      const u64 key = keys[slot(i)];
-      if ((uint32_t)(key >> 32) == ordered(INFINITY))
-        sh.multi[atomicAdd(&sh.n_multi, 1)] = (int)~(uint32_t)key;
-    }
-    __syncthreads();
-    for (int i = tid; i < S * M; i += kThreads)
-      keys[slot(i)] = i < n_inf ? key_of(INFINITY, (uint32_t)sh.multi[i]) : 0;
-    __syncthreads();
-    if (tid < M && tid < a.V) {  // (the lowest M tokens hold enough others)
-      int below = 0;
-      bool one = false;
-      for (int i = 0; i < n_inf; ++i) {
-        below += sh.multi[i] < tid;
-        one |= sh.multi[i] == tid;
-      }
-      const int i = n_inf + tid - below;
-      if (!one && i < M) keys[slot(i)] = key_of(-INFINITY, (uint32_t)tid);
-    }
-    __syncthreads();
-  }
+  if (__syncthreads_or(inf)) infinite_rows(keys, sh, K, M, S, a.V);
   auto candidate = [&](int i) -> u64 {  // (0: none)
     const u64 key = keys[i];
     const int k = (i % lists) / S;
     const float x = unordered((uint32_t)(key >> 32));
-    return key == 0 ? 0 : ordered64(sh.score[k] + (gap((double)x, (double)sh.top[k]) - sh.log_sum[k]));
+    const double d = (double)x - (double)sh.top[k];
+    return key == 0 ? 0 : ordered64(sh.score[k] + (d - sh.log_sum[k]));
   };
   // The best M: those at or above the limit, ranked by counting.  (Equal scores
   // may put more there than ranks need, never fewer.)  Of equal scores the lower
-  // beam's goes first, within a beam the larger key: where a large top or score
-  // makes the scores of different logits one number, they keep the logits' order,
-  // by which the lists were cut.
+  // beam's goes first, within a beam the larger logit's (where a large top or
+  // score makes the scores of different logits one number, they keep the order by
+  // which the lists were cut), of equal logits the lower token's: in one word, since
+  // K V < 2^31 leaves beam and token 32 bits, the beam the upper `of_k`.
+  const int of_k = K > 2 ? 32 - __clz(K - 1) : 1, of_v = 32 - of_k;
+  // A thread's i-th key lies on a diagonal of the lists, so that a group of threads
+  // has keys of all of them: with a list each, the limit would be the best of the
+  // worst beam, and all keys above it to be ranked.
+  auto place = [&](int i) {
+    const int r = i / lists, u = i % lists - r % lists;
+    return r * lists + (u < 0 ? u + lists : u);
+  };
   u64 mine = 0;
   for (int i = tid; i < N; i += kThreads) {
-    const u64 o = candidate(i);
+    const u64 o = candidate(place(i));
     mine = o > mine ? o : mine;
   }
   int groups = 1;
   while (groups < M) groups *= 2;
   const u64 lim = least_of_groups(mine, groups, sh.best);
   for (int i0 = tid & ~31; i0 < N; i0 += kThreads) {
-    const int i = i0 + (tid & 31);
-    const u64 o = mine >= lim && i < N ? candidate(i) : 0;
+    const int at = i0 + (tid & 31), i = place(at);
+    const u64 o = mine >= lim && at < N ? candidate(i) : 0;
     const bool in = o != 0 && o >= lim;
     if (!__any_sync(0xffffffffu, in)) continue;
     const int c = places(in, &sh.n_cand);
     if (in) {
       cand_o[c] = o;
-      cand_i[c] = (uint32_t)(i % lists / S) << 16 | (uint32_t)i;
+      const u64 x = ~keys[i];  // logit, token; the lower first
+      cand_t[c] = (u64)(i % lists / S) << (32 + of_v) | x >> 32 << of_v | (uint32_t)x;
     }
   }
   __syncthreads();
   const int n = sh.n_cand;
   if (tid == 0) cand_o[n] = 0;
   __syncthreads();
-  auto first = [&](int d, int c) {
-    const uint32_t x = cand_i[d], y = cand_i[c];
-    return x >> 16 != y >> 16 ? x < y : keys[x & 0xffffu] > keys[y & 0xffffu];
-  };
-  static_assert(kBeamMergeKeys <= 0x10000, "the list's place in 16 bits");
-  rank_by_count(cand_o, n, first, [&](int c, int r) {
+  rank_by_count<true>(cand_o, cand_t, n, [&](int c, int r) {
     if (r >= M) return;
-    const u64 o = cand_o[c];
-    const int k = (int)(cand_i[c] >> 16);
-    const int token = (int)~(uint32_t)keys[cand_i[c] & 0xffffu];
+    const u64 o = cand_o[c], t = cand_t[c];
+    const int k = (int)(t >> (32 + of_v)), token = (int)((uint32_t)t << of_k >> of_k);
     const int64_t at = g * M + r;
     a.out_scores[at] = (float)unordered64(o);
     a.out_parents[at] = k;
@@ -748,7 +760,7 @@ gdn_status launch_beam_select(BeamArgs a, cudaStream_t stream) {
       cfg.gridDim = dim3(1u << i);
       cfg.dynamicSmemBytes = 16384;
       if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               kBeamMergeKeys * 28 + 60) != cudaSuccess ||
+                               kBeamMergeKeys * 32 + 72) != cudaSuccess ||
           cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
               cudaSuccess)
         return GDN_ERR_CUDA;
@@ -780,7 +792,7 @@ gdn_status launch_beam_select(BeamArgs a, cudaStream_t stream) {
   const int lists = a.K * a.n_seg;
   attr.val.clusterDim.x = (unsigned)cluster;
   cfg.gridDim = dim3((unsigned)cluster, (unsigned)a.n_groups);
-  cfg.dynamicSmemBytes = ((size_t)lists * a.M + 3) * 20 + (size_t)lists * sizeof(float2);
+  cfg.dynamicSmemBytes = ((size_t)lists * a.M + 3) * 24 + (size_t)lists * sizeof(float2);
   return launch_status(cudaLaunchKernelEx(&cfg, kernel, a));
 }
 
