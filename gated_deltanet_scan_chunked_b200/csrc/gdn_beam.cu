@@ -46,7 +46,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCap = 1024;  // candidates of one segment held at once
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kNear = 67108864.f;  // 2^26: see Offset
+constexpr float kNear = 1073741824.f;  // 2^30: see Offset
 
 // Order-preserving map of a float (not NaN; -0 taken as +0) to an unsigned.
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -170,10 +170,10 @@ struct Row {
 
 // What a sum of exp(x - m) subtracts: c = fl(m log2 e), so that a term is 2^(x
 // log2 e - c), one instruction.  c lacks r = m log2 e - c, up to half a step of
-// c, which makes each of the sum's terms 2^r times what it should be: at |m| < 2^26
-// at most 2^4, put right where sums of different m meet.  Beyond it r may pass
-// the exponents that a float has; there c = 0 and the difference x - m is formed
-// first.
+// c, which makes each of the sum's terms 2^r times what it should be: at |m| < 2^30
+// (so that masks of -1e9 are among them) at most 2^64, put right where sums of
+// different m meet.  Beyond it r may pass the exponents that a float has; there
+// c = 0 and the difference x - m is formed first.
 struct Offset {
   float c, r;
   __device__ __forceinline__ explicit Offset(float m) {
@@ -323,9 +323,10 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
   // One pass: the sum s of exp(x - m), the thread's best vector (its largest
   // value, the first vector that has it) and the largest value of its other
   // vectors.  m need not be the maximum: it is the first batch's and moves
-  // only when exp(x - m) would grow past e^40, so that most batches cost no
-  // rescaling.  m beyond 2^26 (Offset) and batches with NaN take the long way; a
-  // batch of nothing but -inf adds nothing to any sum.
+  // only when exp(x - m) would grow past e^20, so that most batches cost no
+  // rescaling (and 2^31 terms of 2^(64 + 20 log2 e) stay below 2^127).  m beyond
+  // 2^30 (Offset) and batches with NaN take the long way; a batch of nothing but
+  // -inf adds nothing to any sum.
   float m = -FLT_MAX, c = 0.f, s = 0.f, best = -INFINITY, other = -INFINITY;
   uint32_t best_v = (uint32_t)tid;
   for (int v0 = tid; v0 < n_vec; v0 += U * kThreads) {
@@ -344,7 +345,7 @@ __device__ __forceinline__ void scan_segment(const BeamArgs& a, BeamShared& sh, 
       }
       peak = fmaxf(peak, top);
     }
-    if (peak > m + 40.f) {  // (-FLT_MAX + 40 is -FLT_MAX; what was summed vanishes, if any was)
+    if (peak > m + 20.f) {  // (-FLT_MAX + 20 is -FLT_MAX; what was summed vanishes, if any was)
       const Offset old(m), now(peak);
       s *= sm100::ex2_approx(__fmaf_rn(__fadd_rn(m, -peak), kLog2e, now.r - old.r));
       m = peak;

@@ -12,12 +12,14 @@ from tests.test_beam_gpu import BF16, F32, LOG_SUM, check, rows
 pytestmark = pytest.mark.gpu
 
 # The bound on the log sum that `check` uses has 35 * 2^-24 for the exponents'
-# arguments: 2.5 * 2^-24 of a difference of up to 14.  The rows here have at
-# most 13,000 tokens, whose terms weigh nothing together below a difference of
-# log 13,000 = 9.5, and take besides a factor 2^-r (2 * 2^-23 and a rounding,
-# 5 * 2^-24) and a rounding of r + difference, up to 6 + 13.7 = 20 in units of
-# 2 (20 * 0.7 * 2^-24 in the worst case, if all weight lay there; at most a
-# difference of 4.5 + 9.5 counts): 2.5 * 9.5 + 5 + 4 < 35.
+# arguments.  The rows here have at most 13,000 tokens, whose terms weigh nothing
+# together below a difference of log 13,000 = 9.5.  Of the argument (x - m) log2 e
+# + r the constant is off by 2^-25 (0.5 * 9.5), and its one rounding, where
+# differing values count at all (from 2^27 on they lie 16 apart) of at most 8 +
+# 9.5 * 1.44 < 32, by 2^-20 * log 2 = 11; equal values have r exactly.  The factor
+# 2^-r is off by 2 * 2^-23 and a rounding, 5.  Where x - m is formed first, its
+# rounding (9.5) and that of at most 13.7 (5.5) take the place of 11 and 5.
+# 4.8 + max(11 + 5, 9.5 + 5.5) < 35.
 
 
 def choice(x, s, M):
@@ -72,14 +74,15 @@ def test_rows_far_from_zero(offset, dtype):
     check(x, s, 12)
 
 
+@pytest.mark.parametrize("step", [20, 40])
 @pytest.mark.parametrize("m", [12345.678, -98765.4, 4321987.0, 6.1e7])
-def test_sums_that_grow_in_steps(m):
-    """A thread meets values 40 above its first ones, then a little more, so that
-    its sum changes its reference while both still count."""
+def test_sums_that_grow_in_steps(m, step):
+    """A thread meets values about as far above its first ones as its sum's reference
+    lies below, then a little more, so that it changes while both still count."""
     G, K, V = 150, 4, 13000
     x = torch.full((G, K, V), m, device="cuda")
-    x[:, :, 4096] = x[0, 0, 0] + 39.75
-    x[:, :, 8192] = x[0, 0, 0] + 40.25
+    x[:, :, 4096] = x[0, 0, 0] + (step - 0.25)
+    x[:, :, 8192] = x[0, 0, 0] + (step + 0.25)
     check(x, torch.zeros(G, K, device="cuda"), 8, groups=[0, 77, 149])
 
 
