@@ -166,11 +166,7 @@ struct Marks {
     const int passed = __popc(upto(p, BACK ? t : t + n - 1, lane));
     if (passed < 32) {
       const uint32_t d = (uint32_t)off - (uint32_t)t;  // (others are at or above RUN)
-      uint32_t b = d < RUN ? 1u << d : 0, e = d - 1u < RUN ? 1u << (d - 1u) : 0;
-      if (BACK) {  // (the walk's own end is not among the 32)
-        const uint32_t z = (uint32_t)hi - (uint32_t)t - 1u;
-        if (z < RUN) e |= 1u << z;
-      }
+      const uint32_t b = d < RUN ? 1u << d : 0, e = d - 1u < RUN ? 1u << (d - 1u) : 0;
       first = __reduce_or_sync(0xffffffffu, b) & valid;
       last = __reduce_or_sync(0xffffffffu, e) & valid;
       const int x = __shfl_sync(0xffffffffu, off, passed);
