@@ -42,7 +42,7 @@ class GdnError(RuntimeError):
 
 def load(path: str = LIB_PATH):
     """Load libgdn.so (once).  Raises if it has not been built."""
-    global _lib
+    global _lib, _current_device, _current_stream
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
@@ -143,6 +143,8 @@ def load(path: str = LIB_PATH):
     lib.gdn_status_string.argtypes = [ctypes.c_int]
     lib.gdn_version.restype = ctypes.c_int32
     lib.gdn_version.argtypes = []
+    _current_device = getattr(torch._C, "_cuda_getDevice", None)
+    _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     _lib = lib
     return lib
 
@@ -668,17 +670,9 @@ _GATE_NONE, _GATE_BETA, _GATE_COMPLEMENT = 0, 1, 2
 
 
 # These calls may be as short as a few microseconds, so the binding asks torch
-# for the device and the stream by its cheapest ways.  (Looked up when a call is
-# made: a torch without CUDA has neither, and the rest of the binding, such as
-# header_functions, needs neither.)
-def _current_device() -> int:
-    return torch._C._cuda_getDevice()
-
-
-def _current_stream(i: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(i)
-
-
+# for the device and the stream by its cheapest ways.  (load() looks them up: a
+# torch without CUDA has neither, and what needs no GPU must import there.)
+_current_device = _current_stream = None
 _CODES = {torch.bfloat16: GDN_BF16, torch.float32: GDN_FP32}
 
 
@@ -692,9 +686,12 @@ def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+_INT32_MAX = (1 << 31) - 1
+
+
 def _int32(v: int, name: str) -> int:
     """v, which goes to an int32 argument (ctypes would cut it to its low 32 bits)."""
-    if not -(1 << 31) <= v < 1 << 31:
+    if not -_INT32_MAX - 1 <= v <= _INT32_MAX:
         raise ValueError("%s = %d does not fit in 32 bits" % (name, v))
     return v
 
@@ -714,7 +711,8 @@ def _glr_inputs(x, log_alpha, beta, i):
         raise TypeError("x must be bfloat16 or float32, got %s" % dtype)
     if len(shape) != 2 or not x.is_contiguous():
         raise ValueError("x must be contiguous [tokens, channels], got %s" % (tuple(shape),))
-    _int32(shape[1], "channels")
+    if shape[1] > _INT32_MAX:
+        _int32(shape[1], "channels")
     _need(log_alpha, "log_alpha", dtype, shape, i)
     if beta is None:
         return dt, _GATE_NONE, None
@@ -857,7 +855,8 @@ def gdn_glr_step(x, log_alpha, state, beta=None, y=None, stream=None) -> torch.T
             return gdn_glr_step(x, log_alpha, state, beta, y)
     dt, gate, beta = _glr_inputs(x, log_alpha, beta, i)
     shape = x.shape
-    _int32(shape[0], "rows")
+    if shape[0] > _INT32_MAX:
+        _int32(shape[0], "rows")
     _need(state, "state", torch.float32, shape, i)
     if y is None:
         y = torch.empty_like(x)
@@ -900,9 +899,10 @@ def gdn_beam_select(logits, scores, n_candidates, finished=None, end_token=-1, o
                          % (tuple(logits.shape),))
     G, K, V = logits.shape
     M, end_token = int(n_candidates), int(end_token)
-    for v, name in ((G, "groups"), (K, "beams"), (V, "vocabulary"), (M, "n_candidates"),
-                    (end_token, "end_token")):
-        _int32(v, name)
+    if max(G, K, V, M, end_token) > _INT32_MAX or end_token < -1:
+        for v, name in ((G, "groups"), (K, "beams"), (V, "vocabulary"), (M, "n_candidates"),
+                        (end_token, "end_token")):
+            _int32(v, name)
     sg, ld, sv = logits.stride()
     if K == 1:
         ld = sg
