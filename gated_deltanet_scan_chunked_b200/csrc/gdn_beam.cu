@@ -23,12 +23,16 @@
 // about g ln g.  These are collected and ranked by counting.
 //
 // What bounds it: for one group the chain behind the last load, which no other
-// work hides (best of the threads, limit, second look, rank, cluster, merge);
-// for many, about 90 instructions a vector of 8 elements, 32 of them for the sum
-// of exponentials, at 44% of the issue rate with 14 warps on an SM.  Measured on a
-// B200, bf16: 1 group, K = 4, V = 32000, M = 8 10.0 us, of which the chain is about
-// 8; 32 groups, K = 8, V = 130001 in rows of 130048, M = 16 30.2 us (66.6 MB, 2.2
-// TB/s of the copy's 6.5).
+// work hides (best of the threads, limit, second look, rank, cluster, merge), on
+// the 16 SMs of one cluster; for many, about 90 instructions a vector of 8
+// elements, 32 of them for the sum of exponentials, at 44% of the issue rate with 14
+// warps on an SM.  Measured on a B200 (calls in a CUDA graph), bf16: 1 group, K = 4,
+// V = 32000, M = 8 9.9 us, of which the chain is about 8; 1 group, K = 8, V =
+// 130000, M = 16 15.4; 32 groups, K = 8, V = 130001 in rows of 130048, M = 16 29.2 us
+// (66.6 MB, 2.3 TB/s of the copy's 6.5).  fp32, the same 32 groups: 41.5 us.  A
+// mask of -inf or -1e9 over 99 % of the tokens costs nothing (29.0); one of the
+// type's lowest value, whose rows are read a second time from the caches by the
+// threads that have met nothing else, 48.7.
 #include <float.h>
 
 #include <atomic>
@@ -747,9 +751,9 @@ gdn_status launch_beam_select(BeamArgs a, cudaStream_t stream) {
   // The group's cluster: the largest power of two at which all groups are on the
   // device at once, none of its CTAs with less than a vector a thread; at
   // most 16 (more than the portable 8 by leave of cudaFuncSetAttribute).
-  // Measured on a B200 (K = 8, V = 130000, M = 16, bf16): 32 groups in clusters
-  // of 16 (two waves) 37.9 us, of 8 29.4, of 4 45.2; 16 groups in clusters of
-  // 16 24.1, of 8 24.7.
+  // Measured on a B200 (K = 8, V = 130000, M = 16, bf16, in one run): 32 groups in
+  // clusters of 16 (two waves) 37.9 us, of 8 29.4, of 4 45.2; 16 groups in
+  // clusters of 16 24.1, of 8 24.7.
   const int64_t step = (int64_t)kThreads * (bf16 ? 8 : 4);
   const int64_t vectors = a.K * ((a.V + step - 1) / step);
   int cluster = 1;

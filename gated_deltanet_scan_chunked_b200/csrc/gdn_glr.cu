@@ -27,16 +27,17 @@
 // anywhere, but 4 (fp32) or 8 (bf16) of them together are such a multiple: the
 // inputs are then loaded as boxes of every 4th or 8th row, from the 16-byte
 // boundary below a piece on and 16 bytes wider, and outputs are stored from
-// registers.  (Against 16-byte asynchronous copies of all threads: fp32, C = 1333,
-// 20011 tokens of 24 sequences 80 us for 91, with beta, one sequence 74 for 100;
-// the backward 135 for 169 and 156 for 211.)
+// registers.  (Against 16-byte asynchronous copies of all threads, in one run: fp32,
+// C = 1333, 20011 tokens of 24 sequences 80 us for 91, with beta, one sequence 74
+// for 100; the backward 135 for 169 and 156 for 211.)
 //
 // What bounds it.  A dozen operations an element leave it memory bound in
 // principle.  In practice a step is a chain (inputs, fold, the cluster's
 // exchange, outputs) that the two to four CTAs of an SM overlap: at wide C the
 // memory is the limit, at others the part of the SMs that whole clusters of one
 // wave can fill, and with three tensors the latency of that chain.  Measured on a
-// B200 (a copy runs at 6.54 TB/s), time and bytes read and written by time:
+// B200 (a copy runs at 6.54 TB/s; calls in a CUDA graph), time and bytes read and
+// written by time:
 //   forward, bf16, beta, C = 6144, T = 4096          36.9 us   5.45 TB/s
 //   forward, bf16, beta, C = 9216, T = 16384          199 us   6.07 TB/s
 //   forward, bf16, b = 1 - a, C = 2560, T = 131072    449 us   4.48 TB/s
@@ -547,8 +548,10 @@ constexpr int ctas_of_sm(int w, int stages) {
   const int fit = 227 * 1024 / (runs_bytes(w, 1) + tiles_bytes(8) + kBarBytes + stages + 1024);
   return fit < 16 / w ? fit : 16 / w;
 }
-// The forward's outputs get room apart where that costs no CTA of an SM: loads
-// then have a step and a half to arrive, not a half (bf16, gate beta, us, apart
+// The forward's outputs get room apart where that costs no CTA of an SM in clusters
+// of 8 (of two bf16 inputs in clusters of 12 and more it costs the fourth CTA, which
+// `choose` sees and avoids): loads then have a step and a half to arrive, not a
+// half (bf16, gate beta, us, apart
 // against in place: 4 warps, C = 6144, T = 32768 263 for 290, C = 2560, T = 131072
 // 444 for 483; 8 warps, two CTAs of an SM in place and one apart, C = 9216, T =
 // 16384 216 for 199; fp32, gate beta, 4 warps likewise, C = 2560, T = 32768 233
@@ -913,9 +916,9 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
 }
 
 // One token: [N, C] arrays, all dense and of one shape, so n = N C values in
-// a row.  A thread takes 8 of them with 16-byte accesses; the last n % 8
-// are taken singly.  Bound by memory, and by its launch when small: bf16 with
-// beta, N = 256, C = 6144 5.3 us (25 MB, 4.7 TB/s), N = 3, C = 2561 2.2 us.
+// a row.  A thread takes 8 of them, four at a time (16 bytes of fp32, 8 of bf16);
+// the last n % 8 are taken singly.  Bound by memory, and by its launch when small:
+// bf16 with beta, N = 256, C = 6144 5.2 us (25 MB, 4.8 TB/s), N = 3, C = 2561 2.2 us.
 template <typename Tin, int GATE>
 __global__ void __launch_bounds__(256) glr_step_kernel(const Tin* __restrict__ x,
                                                        const Tin* __restrict__ la,
@@ -1112,7 +1115,8 @@ int clusters_that_fit(int dev, int variant, const Scan& k, int cluster, int shar
 // eight clusters of 16 CTAs two to an SM, some lie together on a few SMs and the
 // others' steps are half as long; so no more CTAs are let onto an SM than the
 // choice counts on, by the shared memory asked for.  Measured on a B200
-// (forward, bf16, gate beta, us a step): 8 warps 2.05 alone and 2.85 by twos, 4
+// (forward, bf16, gate beta, us a step; the table serves the other types, gates and
+// unaligned rows too, whose steps have not been measured each): 8 warps 2.05 alone and 2.85 by twos, 4
 // warps (half the tokens) 1.28, 1.65, 2.1 and 2.5; a further wave costs about a
 // tenth; the backward's 4 warps are slower by comparison (on the scale of its 8:
 // 1.46, 1.87, 2.26, 2.72).  What this settles (us, bf16):
