@@ -1116,9 +1116,9 @@ int clusters_that_fit(int dev, int variant, const Scan& k, int cluster, int shar
 // others' steps are half as long; so no more CTAs are let onto an SM than the
 // choice counts on, by the shared memory asked for.  Measured on a B200
 // (forward, bf16, gate beta, us a step; the table serves the other types, gates and
-// unaligned rows too, whose steps have not been measured each): 8 warps 2.05 alone and 2.85 by twos, 4
-// warps (half the tokens) 1.28, 1.65, 2.1 and 2.5; a further wave costs about a
-// tenth; the backward's 4 warps are slower by comparison (on the scale of its 8:
+// unaligned rows too, whose steps have not been measured each): 8 warps 2.05 alone
+// and 2.85 by twos, 4 warps (half the tokens) 1.28, 1.65, 2.1 and 2.5; a further
+// wave costs about a tenth; the backward's 4 warps are slower by comparison (on the scale of its 8:
 // 1.46, 1.87, 2.26, 2.72).  What this settles (us, bf16):
 //   forward, C = 6144, T = 32768: 8 warps in clusters of 2 (one wave, a third
 //     of the SMs with two CTAs) 336, of 8 (three waves) 307, 4 warps in

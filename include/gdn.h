@@ -609,8 +609,9 @@ gdn_status gdn_glr_step(const void* x, const void* log_alpha, const void* beta,
  *                  or the token is end_token
  * With M = K, out_scores may be scores and out_finished may be finished (in
  * place, for a loop without copies); otherwise outputs must not overlap
- * inputs or each other.  The logits are read once (in rows masked with finite
- * values past -2^30, once more from the caches).  One kernel, no workspace.
+ * inputs or each other.  The logits are read once (where they hold NaN or are
+ * past 2^30 in size, as some masks are, once more from the caches).  One kernel,
+ * no workspace.
  */
 gdn_status gdn_beam_select(const void* logits, int64_t ld, const float* scores,
                            const uint8_t* finished, int32_t end_token, int32_t n_groups,
